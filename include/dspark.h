@@ -14,6 +14,13 @@
  *                                                         (dspark_schedule)
  *   a8  verification of the admitted prefixes against target logits
  *                                                         (dspark_verify)
+ * Between a7 and a8 the target model runs over every request's anchor and
+ * admitted drafts.  What that pass needs of its paged KV cache:
+ *   rows, pages, slots and ancestor masks of the round    (dspark_kv_plan)
+ *   the rows' K and V into their slots                    (dspark_kv_append)
+ *   attention of a drafted tree (or chain) over the cache (dspark_tree_attention)
+ *   the path of the tree that the target's choices confirm (dspark_tree_accept)
+ *   that path's K and V moved together                    (dspark_kv_compact)
  *
  * Sources (page title, section):
  *   "DSpark 深度解读" (zhichai.net) §二 设计一 (Markov head, W1: V x r, W2: r x V),
@@ -92,8 +99,10 @@ enum {
   DSPARK_ERR_TOKEN = 5,      /* device status: token id outside [0, V)              */
   DSPARK_ERR_LENGTH = 6,     /* device status: verify length outside [0, gamma]     */
   DSPARK_ERR_TIMEOUT = 7,    /* device status: a bounded device-side wait ran out   */
-  DSPARK_ERR_TOO_LARGE = 8   /* problem exceeds a fixed library limit (static scratch,
+  DSPARK_ERR_TOO_LARGE = 8,  /* problem exceeds a fixed library limit (static scratch,
                                 sampling verify with V > 13107200)                 */
+  DSPARK_ERR_PAGES = 9       /* device status: no free cache page left, or a page or
+                                slot outside the cache                             */
 };
 
 enum {
@@ -324,6 +333,156 @@ int dspark_verify(const dspark_dims *dims, const int32_t *anchor, const int32_t 
 int dspark_verify_residual_rows(const dspark_dims *dims, const void *workspace,
                                 size_t workspace_bytes, int32_t *rejected,
                                 int32_t *explicit_rows, dspark_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The target model's paged KV cache in a round.
+ *
+ * A cache is n_pages pages of page_size tokens.  A request owns an ordered list
+ * of pages (its row of block_table); its token at position p lies in page
+ * block_table[r, p / page_size] at p % page_size, and slot = page * page_size +
+ * p % page_size names that place.  A round gives request r n_r new rows: node 0
+ * is its anchor, at position ctx[r], and nodes 1..n_r - 1 its admitted drafts,
+ * at positions ctx[r] + 1, ..: the chain x_1, x_2, .. of dspark_markov_draft, or
+ * a tree of drafts in which every node's parent comes before it.  The rows of
+ * all requests lie one after the other (request r's from row_start[r] on), and
+ * buffers over rows hold n_rows of them; those past row_start[R] are padding, so
+ * that every round can launch with the same arguments (CUDA graphs).
+ */
+enum {
+  DSPARK_KV_BF16 = 0, /* K and V as bf16                                            */
+  DSPARK_KV_E4M3 = 1  /* as 8-bit floats (4 exponent, 3 mantissa bits, finite), each
+                         standing for value * scale of its head                     */
+};
+
+/* One layer's cache.  Element i of head h of token t of page p of K is
+ * k[p * page_stride + t * token_stride + h * head_stride + i]; V likewise.
+ * k, v and the three strides (in bytes) must be multiples of 16 bytes, and the
+ * strides below 2^40 bytes. */
+typedef struct dspark_kv_cache {
+  void *k, *v;
+  const float *k_scale; /* DSPARK_KV_E4M3: f32 [heads], or NULL for scales of 1     */
+  const float *v_scale;
+  int64_t page_stride, token_stride, head_stride; /* in elements                    */
+  int32_t n_pages;
+  int32_t page_size; /* 16, 32, 64, 128 or 256                                      */
+  int32_t heads;     /* KV heads                                                    */
+  int32_t dim;       /* head dimension: 64 or 128                                   */
+  int32_t type;      /* DSPARK_KV_*                                                 */
+} dspark_kv_cache;
+
+#define DSPARK_MAX_NODES 64 /* rows of one request's tree: a mask is one 64-bit word */
+
+/* Rows, pages, slots, positions and masks of one round, built on the device from
+ * the committed lengths and the schedule's admitted lengths.
+ *   n_r = len[r] + extra, or 0 where ctx[r] < 0 (the request has left: its pages
+ *   go back); extra is 1 in a round (the anchor's row), 0 for a prompt
+ *   row_start[r]  = n_0 + .. + n_{r-1}
+ *   pages         first every page of the requests that left is pushed on the
+ *                 stack of free pages (request by request, in block order); then
+ *                 request r needs max(0, ceil((ctx + n_r) / page_size) - held[r])
+ *                 pages more, and the pages needed are popped request by request,
+ *                 in block order.  Once the stack does not cover a request's need,
+ *                 neither it nor any later request in need gets one: status
+ *                 DSPARK_ERR_PAGES, table entries and slots -1
+ *   anc[row]      bit j: node j is the row's node or one of its ancestors
+ *   position[row] = ctx[r] + the number of its ancestors
+ *   slot[row]     the place of position ctx[r] + node in the cache
+ *   ctx      int32 [R]   committed tokens, < 0 for a request that has left
+ *   len      int32 [R]   from dspark_schedule (a round), or a prompt's tokens
+ *   parent   int32 [R, gamma]  parent node of drafts 1..gamma: 0 <= parent[r, j-1]
+ *            < j (0: the anchor); NULL: chains.  Needs extra = 1, 1 <= gamma <= 63,
+ *            len[r] <= gamma.  The parent of an admitted node is itself admitted,
+ *            as len[r] cuts the tree in node order.
+ *   held     int32 [R], n_free int32 [1]: pages held by each request, and free;
+ *            held_out, n_free_out after the call, and may be the same memory
+ *   free_pages  int32 [n_pages]  the stack: entries 0..n_free-1 are free pages
+ *   block_table int32 [R, max_pages]  read for held pages, written for new ones
+ *   row_start int32 [R+1] out;  position int32 [n_rows], slot int64 [n_rows] out
+ *            (-1 in padding);  anc uint64 [n_rows] out (0 in padding), or NULL;
+ *            with anc, n_r <= DSPARK_MAX_NODES
+ * Device status: DSPARK_ERR_LENGTH for a len outside its range, for more rows
+ * than n_rows (the rows past it are dropped) or a request longer than max_pages;
+ * DSPARK_ERR_PAGES as above or for held / n_free outside their ranges;
+ * DSPARK_ERR_ARG for a parent out of range (taken as the anchor).  R <= 16384. */
+int dspark_kv_plan(int32_t R, int32_t gamma, int32_t extra, int32_t n_rows, int32_t page_size,
+                   int32_t n_pages, int32_t max_pages, const int32_t *ctx, const int32_t *len,
+                   const int32_t *parent, const int32_t *held, const int32_t *n_free,
+                   int32_t *free_pages, int32_t *block_table, int32_t *held_out,
+                   int32_t *n_free_out, int32_t *row_start, int32_t *position, int64_t *slot,
+                   uint64_t *anc, dspark_stream_t stream);
+
+/* New rows into their slots: cache[slot[row]] = row, as bf16, or in a
+ * DSPARK_KV_E4M3 cache as clamp(x / scale[head], -448, 448) rounded to nearest
+ * even (a NaN stays one).
+ *   k, v  bf16, element i of head h of row m at k[m * row_stride + h * head_stride
+ *         + i] (views of a fused projection need no copy); 16-byte aligned, strides
+ *         in elements, multiples of 8
+ *   slot  int64 [n_rows]: a negative one writes nothing; one past the cache
+ *         writes nothing and sets DSPARK_ERR_PAGES */
+int dspark_kv_append(const dspark_kv_cache *cache, int32_t n_rows, const void *k, const void *v,
+                     int64_t row_stride, int64_t head_stride, const int64_t *slot,
+                     dspark_stream_t stream);
+
+/* Workspace bytes dspark_tree_attention needs (0 when the sizes are invalid). */
+size_t dspark_tree_attention_workspace_bytes(const dspark_kv_cache *cache, int32_t R,
+                                             int32_t heads_q, int32_t max_nodes);
+
+/* Attention of every request's rows over its committed tokens and its tree.  Row
+ * i of request r sees the token at position p where p < ctx[r], or p = ctx[r] + j
+ * with j < n_r and bit j of anc set.  Over the tokens it sees, for query head h
+ * and KV head g = h / (heads_q / heads):
+ *   s_p = scale * q . K_p,  out = sum_p e^{s_p} V_p / sum_p e^{s_p},
+ *   lse = log sum_p e^{s_p}
+ * A row that sees nothing gives out = 0 and lse = -inf.  What a row does not see
+ * does not reach it, whatever its bits (infinities and NaN in unwritten or
+ * masked places included).  q, scores and statistics in f32; the weights are
+ * rounded to bf16 where they meet V.
+ *   q, out bf16: element i of head h of row m at m * row_stride + h * head_stride
+ *          + i; q 16-byte aligned with strides (in elements) that are multiples of 8
+ *   ctx    int32 [R] as dspark_kv_plan took it; row_start int32 [R+1], anc uint64
+ *          [n_rows] and block_table int32 [R, max_pages] as it left them; anc
+ *          NULL: chains (row i sees nodes 0..i)
+ *   max_nodes  the most rows of a request, 1..DSPARK_MAX_NODES: rows past it are
+ *          not computed (status DSPARK_ERR_LENGTH)
+ *   lse    f32 [n_rows, heads_q] out, may be NULL
+ *   workspace  dspark_tree_attention_workspace_bytes(...) bytes, 256-byte aligned
+ * Padding rows of out and lse are left as they are.  heads_q is a multiple of
+ * cache->heads, at most 64 times as many.  A block-table entry outside the cache
+ * reads as zeros (status DSPARK_ERR_PAGES); a request longer than its row of the
+ * table is cut there (DSPARK_ERR_LENGTH). */
+int dspark_tree_attention(const dspark_kv_cache *cache, int32_t R, int32_t heads_q,
+                          int32_t max_nodes, int32_t n_rows, int32_t max_pages, const void *q,
+                          int64_t q_row_stride, int64_t q_head_stride, const int32_t *ctx,
+                          const int32_t *row_start, const uint64_t *anc,
+                          const int32_t *block_table, float scale, void *out,
+                          int64_t out_row_stride, int64_t out_head_stride, float *lse,
+                          void *workspace, size_t workspace_bytes, dspark_stream_t stream);
+
+/* The path of each request's tree that the target confirms: from the anchor on,
+ * a node's child with token == choice[node] follows (the lowest node of several),
+ * until there is none.  With choices drawn from (or the argmax of) the target's
+ * distribution at each node, anchor, path and bonus follow the target's law.
+ *   row_start int32 [R+1];  parent int32 [R, gamma] or NULL (chains), 1 <= gamma <= 63
+ *   tokens    int32 [R, gamma]   token of drafts 1..gamma
+ *   choice    int32 [n_rows]     the target's token after each row
+ *   ctx       int32 [R]
+ *   accepted  int32 [R] out: drafts on the path
+ *   bonus     int32 [R] out: the choice at its last node (-1 without rows)
+ *   path      int32 [R, gamma] out: its nodes, then -1
+ *   ctx_out   int32 [R] out: ctx + 1 + accepted (ctx without rows); may be ctx */
+int dspark_tree_accept(int32_t R, int32_t gamma, int32_t n_rows, const int32_t *row_start,
+                       const int32_t *parent, const int32_t *tokens, const int32_t *choice,
+                       const int32_t *ctx, int32_t *accepted, int32_t *bonus, int32_t *path,
+                       int32_t *ctx_out, dspark_stream_t stream);
+
+/* The accepted path's K and V moved to consecutive positions: position ctx[r] + j
+ * receives what position ctx[r] + path[r, j-1] holds, for j = 1..accepted[r], with
+ * ctx as it was before dspark_tree_accept.  Chains need no such call: their path
+ * is in place.  A path that does not ascend or leaves 1..63 sets DSPARK_ERR_ARG,
+ * and one whose pages are outside the cache DSPARK_ERR_PAGES; neither is moved. */
+int dspark_kv_compact(const dspark_kv_cache *cache, int32_t R, int32_t gamma, int32_t max_pages,
+                      const int32_t *ctx, const int32_t *accepted, const int32_t *path,
+                      const int32_t *block_table, dspark_stream_t stream);
 
 /* Failure detection self-test (no fault is involved).  Every device-side wait
  * of the library is bounded in time; on expiry the kernel records

@@ -33,8 +33,13 @@ EXPORTS = [
     "dspark_sts_workspace_bytes", "dspark_sts_fit", "dspark_rnn_workspace_bytes",
     "dspark_rnn_draft", "dspark_selftest_wait_timeout", "dspark_fused_workspace_bytes",
     "dspark_pack_fused", "dspark_fused_draft", "dspark_verify_residual_rows",
+    "dspark_kv_plan", "dspark_kv_append", "dspark_tree_attention_workspace_bytes",
+    "dspark_tree_attention", "dspark_tree_accept", "dspark_kv_compact",
 ]
 STATIC_SCRATCH_BYTES = 16 << 20
+KV_BF16 = 0
+KV_E4M3 = 1
+MAX_NODES = 64
 
 
 class DSparkError(RuntimeError):
@@ -44,6 +49,14 @@ class DSparkError(RuntimeError):
 class Dims(ctypes.Structure):
     _fields_ = [("R", ctypes.c_int32), ("gamma", ctypes.c_int32), ("V", ctypes.c_int32),
                 ("r", ctypes.c_int32), ("d", ctypes.c_int32)]
+
+
+class KVCacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("dim", ctypes.c_int32), ("type", ctypes.c_int32)]
 
 
 _lib = None
@@ -61,6 +74,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     P, I32, U64, SZ, F32 = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint64, ctypes.c_size_t,
                             ctypes.c_float)
     DP = ctypes.POINTER(Dims)
+    CP, I64 = ctypes.POINTER(KVCacheStruct), ctypes.c_int64
     sig = {
         "dspark_lm_head": (ctypes.c_int, [DP, P, P, P, P]),
         "dspark_pack_w2": (ctypes.c_int, [DP, P, P, P]),
@@ -88,6 +102,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "dspark_markov_draft_static": (ctypes.c_int, [DP, P, P, P, P, P, P, P, F32, U64, P, P, P,
                                                       P, P]),
         "dspark_verify_residual_rows": (ctypes.c_int, [DP, P, SZ, P, P, P]),
+        "dspark_kv_plan": (ctypes.c_int, [I32] * 7 + [P] * 13 + [P]),
+        "dspark_kv_append": (ctypes.c_int, [CP, I32, P, P, I64, I64, P, P]),
+        "dspark_tree_attention_workspace_bytes": (SZ, [CP, I32, I32, I32]),
+        "dspark_tree_attention": (ctypes.c_int, [CP, I32, I32, I32, I32, I32, P, I64, I64, P, P, P,
+                                                 P, F32, P, I64, I64, P, P, SZ, P]),
+        "dspark_tree_accept": (ctypes.c_int, [I32, I32, I32, P, P, P, P, P, P, P, P, P, P]),
+        "dspark_kv_compact": (ctypes.c_int, [CP, I32, I32, I32, P, P, P, P, P]),
         "dspark_device_status": (ctypes.c_int, [P, ctypes.c_int]),
         "dspark_error_string": (ctypes.c_char_p, [ctypes.c_int]),
         "dspark_launch_count": (U64, []),
@@ -272,6 +293,159 @@ def dspark_verify_residual_rows(dims, workspace, stream=None):
         ctypes.byref(dims), _ptr(workspace), workspace.numel(), ctypes.byref(rej),
         ctypes.byref(expl), _stream(stream)), "dspark_verify_residual_rows")
     return int(rej.value), int(expl.value)
+
+
+# ------------------------------------------- the target's paged KV cache ----
+
+def _want(what: str, name: str, t, dtype, shape, optional=False):
+    """The tensor's pointer, once its type and shape are what the call reads; a None
+    in `shape` is any size."""
+    if t is None and optional:
+        return None
+    if t is None or t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise DSparkError(f"{what}: {name} must be {dtype}")
+    if len(t.shape) != len(shape) or any(n is not None and n != m
+                                         for n, m in zip(shape, t.shape)):
+        raise DSparkError(f"{what}: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def _rows_view(what: str, name: str, t, heads, dim):
+    """A bf16 [rows, heads, dim] view whose last dimension is dense: (pointer, strides)."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1:] != (heads, dim):
+        raise DSparkError(f"{what}: {name} must be bfloat16 [rows, {heads}, {dim}]")
+    if not t.is_cuda:
+        raise DSparkError("tensor must live on the GPU")
+    if t.stride(2) != 1:
+        raise DSparkError(f"{what}: {name}'s last dimension must be dense")
+    # a dimension of one element may carry any stride: what the call would step by is unused
+    head = t.stride(1) if heads > 1 else dim
+    row = t.stride(0) if t.shape[0] > 1 else max(8, heads * head)
+    return ctypes.c_void_p(t.data_ptr()), row, head
+
+
+_MASK = (torch.int64, torch.uint64)
+
+
+class KVCache:
+    """One layer's paged cache: k and v [n_pages, page_size, heads, dim], bfloat16 or
+    float8_e4m3fn (then with f32 scales [heads], default 1), in any memory order whose
+    last dimension is dense."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
+            raise DSparkError("KVCache: k and v must be alike, [n_pages, page_size, heads, dim]")
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise DSparkError("KVCache: bfloat16 or float8_e4m3fn")
+        if not (k.is_cuda and v.is_cuda):
+            raise DSparkError("tensor must live on the GPU")
+        if k.stride(3) != 1:
+            raise DSparkError("KVCache: the last dimension must be dense")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.page_size, self.heads, self.dim = k.shape
+        fp8 = k.dtype == torch.float8_e4m3fn
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None and not fp8:
+                raise DSparkError("KVCache: a bfloat16 cache has no scales")
+            _want("KVCache", name, t, torch.float32, (self.heads,), optional=True)
+        # strides over a single page or head are never stepped by
+        head = k.stride(2) if self.heads > 1 else self.dim
+        page = k.stride(0) if self.n_pages > 1 else self.page_size * self.heads * self.dim
+        self.struct = KVCacheStruct(k.data_ptr(), v.data_ptr(),
+                                    k_scale.data_ptr() if k_scale is not None else None,
+                                    v_scale.data_ptr() if v_scale is not None else None,
+                                    page, k.stride(1), head, self.n_pages, self.page_size,
+                                    self.heads, self.dim, KV_E4M3 if fp8 else KV_BF16)
+
+
+def dspark_kv_plan(ctx, length, extra, parent, page_size, held, n_free, free_pages, block_table,
+                   held_out, n_free_out, row_start, position, slot, anc=None, stream=None):
+    """parent [R, gamma] or None (chains); anc int64 (the 64-bit words) or None."""
+    what, i32 = "dspark_kv_plan", torch.int32
+    R, rows = ctx.shape[0], position.shape[0]
+    if block_table.dim() != 2:
+        raise DSparkError(f"{what}: block_table must be [R, max_pages]")
+    gamma = parent.shape[1] if parent is not None and parent.dim() == 2 else 0
+    _check(load_library().dspark_kv_plan(
+        R, gamma, int(extra), rows, int(page_size), free_pages.shape[0], block_table.shape[1],
+        _want(what, "ctx", ctx, i32, (R,)), _want(what, "len", length, i32, (R,)),
+        _want(what, "parent", parent, i32, (R, gamma), optional=True),
+        _want(what, "held", held, i32, (R,)), _want(what, "n_free", n_free, i32, (1,)),
+        _want(what, "free_pages", free_pages, i32, (None,)),
+        _want(what, "block_table", block_table, i32, (R, None)),
+        _want(what, "held_out", held_out, i32, (R,)),
+        _want(what, "n_free_out", n_free_out, i32, (1,)),
+        _want(what, "row_start", row_start, i32, (R + 1,)),
+        _want(what, "position", position, i32, (rows,)),
+        _want(what, "slot", slot, torch.int64, (rows,)),
+        _want(what, "anc", anc, _MASK, (rows,), optional=True), _stream(stream)), what)
+
+
+def dspark_kv_append(cache: KVCache, k, v, slot, stream=None):
+    """k, v bf16 [rows, heads, dim] views of equal strides."""
+    what = "dspark_kv_append"
+    kp, row, head = _rows_view(what, "k", k, cache.heads, cache.dim)
+    vp, row_v, head_v = _rows_view(what, "v", v, cache.heads, cache.dim)
+    if k.shape != v.shape or (row, head) != (row_v, head_v):
+        raise DSparkError(f"{what}: k and v must have equal shapes and strides")
+    _check(load_library().dspark_kv_append(
+        ctypes.byref(cache.struct), k.shape[0], kp, vp, row, head,
+        _want(what, "slot", slot, torch.int64, (k.shape[0],)), _stream(stream)), what)
+
+
+def dspark_tree_attention_workspace_bytes(cache: KVCache, R, heads_q, max_nodes) -> int:
+    return int(load_library().dspark_tree_attention_workspace_bytes(
+        ctypes.byref(cache.struct), int(R), int(heads_q), int(max_nodes)))
+
+
+def dspark_tree_attention(cache: KVCache, q, ctx, row_start, anc, block_table, max_nodes, scale,
+                          out, lse, workspace, stream=None):
+    """q, out bf16 [rows, heads_q, dim] (views with a dense last dimension); anc or lse may
+    be None."""
+    what, i32 = "dspark_tree_attention", torch.int32
+    R, rows, heads_q = ctx.shape[0], q.shape[0], q.shape[1] if q.dim() == 3 else 0
+    qp, q_row, q_head = _rows_view(what, "q", q, heads_q, cache.dim)
+    op, o_row, o_head = _rows_view(what, "out", out, heads_q, cache.dim)
+    if out.shape[0] != rows:
+        raise DSparkError(f"{what}: out must have q's rows")
+    _check(load_library().dspark_tree_attention(
+        ctypes.byref(cache.struct), R, heads_q, int(max_nodes), rows,
+        block_table.shape[1] if block_table.dim() == 2 else 0, qp, q_row, q_head,
+        _want(what, "ctx", ctx, i32, (R,)), _want(what, "row_start", row_start, i32, (R + 1,)),
+        _want(what, "anc", anc, _MASK, (rows,), optional=True),
+        _want(what, "block_table", block_table, i32, (R, None)), float(scale), op, o_row, o_head,
+        _want(what, "lse", lse, torch.float32, (rows, heads_q), optional=True),
+        _ptr(workspace), workspace.numel(), _stream(stream)), what)
+
+
+def dspark_tree_accept(row_start, parent, tokens, choice, ctx, accepted, bonus, path, ctx_out,
+                       stream=None):
+    """parent [R, gamma] or None (chains)."""
+    what, i32 = "dspark_tree_accept", torch.int32
+    if tokens.dim() != 2:
+        raise DSparkError(f"{what}: tokens must be [R, gamma]")
+    R, gamma = tokens.shape
+    _check(load_library().dspark_tree_accept(
+        R, gamma, choice.shape[0], _want(what, "row_start", row_start, i32, (R + 1,)),
+        _want(what, "parent", parent, i32, (R, gamma), optional=True),
+        _want(what, "tokens", tokens, i32, (R, gamma)),
+        _want(what, "choice", choice, i32, (None,)), _want(what, "ctx", ctx, i32, (R,)),
+        _want(what, "accepted", accepted, i32, (R,)), _want(what, "bonus", bonus, i32, (R,)),
+        _want(what, "path", path, i32, (R, gamma)), _want(what, "ctx_out", ctx_out, i32, (R,)),
+        _stream(stream)), what)
+
+
+def dspark_kv_compact(cache: KVCache, ctx, accepted, path, block_table, stream=None):
+    """ctx as it was before dspark_tree_accept."""
+    what, i32 = "dspark_kv_compact", torch.int32
+    if path.dim() != 2 or block_table.dim() != 2:
+        raise DSparkError(f"{what}: path must be [R, gamma], block_table [R, max_pages]")
+    R, gamma = path.shape
+    _check(load_library().dspark_kv_compact(
+        ctypes.byref(cache.struct), R, gamma, block_table.shape[1],
+        _want(what, "ctx", ctx, i32, (R,)), _want(what, "accepted", accepted, i32, (R,)),
+        _want(what, "path", path, i32, (R, gamma)),
+        _want(what, "block_table", block_table, i32, (R, None)), _stream(stream)), what)
 
 
 def dspark_device_status(stream=None, clear: bool = True) -> int:

@@ -15,6 +15,8 @@ int dspark_status_verify(int clear);
 int dspark_status_sched(int clear);
 int dspark_status_sts(int clear);
 int dspark_status_selftest(int clear);
+int dspark_status_kv(int clear);
+int dspark_status_attention(int clear);
 
 extern "C" uint64_t dspark_launch_count(void) { return g_launches.load(); }
 
@@ -29,6 +31,7 @@ extern "C" const char *dspark_error_string(int code) {
     case DSPARK_ERR_LENGTH: return "verify length outside [0, gamma]";
     case DSPARK_ERR_TIMEOUT: return "device-side wait timed out";
     case DSPARK_ERR_TOO_LARGE: return "problem exceeds the library's static scratch";
+    case DSPARK_ERR_PAGES: return "no free cache page, or a page or slot outside the cache";
     default: return "unknown error";
   }
 }
@@ -36,9 +39,10 @@ extern "C" const char *dspark_error_string(int code) {
 extern "C" int dspark_device_status(dspark_stream_t stream, int clear) {
   if (cudaStreamSynchronize(stream) != cudaSuccess) return DSPARK_ERR_CUDA;
   int first = DSPARK_OK;
-  const int vals[6] = {dspark_status_lmhead(clear), dspark_status_markov(clear),
+  const int vals[8] = {dspark_status_lmhead(clear), dspark_status_markov(clear),
                        dspark_status_verify(clear), dspark_status_sched(clear),
-                       dspark_status_sts(clear),    dspark_status_selftest(clear)};
+                       dspark_status_sts(clear),    dspark_status_selftest(clear),
+                       dspark_status_kv(clear),     dspark_status_attention(clear)};
   for (int v : vals)
     if (first == DSPARK_OK && v != DSPARK_OK) first = v;
   return first;
