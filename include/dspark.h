@@ -435,8 +435,8 @@ size_t dspark_tree_attention_workspace_bytes(const dspark_kv_cache *cache, int32
  *   lse = log sum_p e^{s_p}
  * A row that sees nothing gives out = 0 and lse = -inf.  What a row does not see
  * does not reach it, whatever its bits (infinities and NaN in unwritten or
- * masked places included).  q, scores and statistics in f32; the weights are
- * rounded to bf16 where they meet V.
+ * masked places included).  Scores, statistics and sums in f32; the weights meet
+ * V with 16 bits (the sum of two bf16).
  *   q, out bf16: element i of head h of row m at m * row_stride + h * head_stride
  *          + i; q 16-byte aligned with strides (in elements) that are multiples of 8
  *   ctx    int32 [R] as dspark_kv_plan took it; row_start int32 [R+1], anc uint64

@@ -1,118 +1,99 @@
-// tree_attention.cu — attention of every request's drafted tree (or chain, or
-// single token) over its paged KV cache.
-//
-//   s_p = scale * q . K_p,  out = sum_p e^{s_p} V_p / sum_p e^{s_p}
-// over p < ctx, and p = ctx + j for the nodes j in the row's ancestor mask.
-#include <cuda_fp8.h>
-
+// tree_attention.cu — dspark_tree_attention: checks, the choice of the row tile,
+// and the launches of tree_attention.cuh.
 #include "kv_cache.cuh"
+#include "tcgen05.cuh"
 
 DSPARK_DECLARE_STATUS(s_status_attention)
 
+#include "tree_attention.cuh"
+
 namespace {
 
-struct AttnArgs {
-  const uint8_t *k, *v;
-  const float *k_scale, *v_scale;
-  int64_t page_stride, token_stride, head_stride;
-  int n_pages, page_shift, heads, dim;
-  int R, heads_q, max_nodes, n_rows, max_pages;
-  const bf16 *q;
-  int64_t q_row, q_head;
-  const int *ctx, *row_start;
-  const uint64_t *anc;
-  const int *block_table;
-  float scale;
-  bf16 *out;
-  int64_t out_row, out_head;
-  float *lse;
-};
+using attn::Args;
 
-template <int TYPE>
-__device__ __forceinline__ float element(const uint8_t *base, int64_t i) {
-  if constexpr (TYPE == DSPARK_KV_E4M3) {
-    __nv_fp8_e4m3 x;
-    x.__x = base[i];
-    return (float)x;
-  } else {
-    return __bfloat162float(reinterpret_cast<const bf16 *>(base)[i]);
-  }
+// Query rows of a tile: the narrowest that takes a request's rows, so that no
+// product, exponential or byte of shared memory is spent on empty columns; at
+// most 128 (TMEM holds two tiles of scores and O's two parts, four times as many
+// columns), or 64 beside the warps that widen an 8-bit cache.
+int row_tile(const dspark_kv_cache *c, int heads_q, int max_nodes) {
+  const int rows = max_nodes * (heads_q / c->heads);
+  if (rows <= 16) return 16;
+  if (rows <= 32) return 32;
+  return rows <= 64 || c->type == DSPARK_KV_E4M3 ? 64 : 128;
 }
 
-// Block (row, head): four warps stride over the tokens, a lane holding dim / 32
-// elements, each warp with its own running maximum and sum; joined at the end.
+struct Layout {
+  size_t ml, desc, bytes;
+};
+Layout layout_of(int ctas, int nt, int dim) {
+  Layout l;
+  l.ml = dspark_align_up((size_t)ctas * 2 * nt * dim * sizeof(float), 256);
+  l.desc = l.ml + dspark_align_up((size_t)ctas * 4 * nt * sizeof(float), 256);
+  l.bytes = l.desc + dspark_align_up((size_t)ctas * 8 * sizeof(int), 256);
+  return l;
+}
+
+struct Launch {
+  const dspark_kv_cache *cache;
+  Args a;
+  const void *q;
+  int64_t q_row, q_head;
+  int ctas;
+  cudaStream_t stream;
+};
+
+template <int TYPE, int D, int NT>
+int launch(const Launch &l) {
+  using G = attn::Geo<TYPE, D, NT>;
+  const dspark_kv_cache *c = l.cache;
+  const Args &a = l.a;
+  const uint64_t size = G::FP8 ? 1 : 2;
+  const uint64_t dims[4] = {(uint64_t)D, (uint64_t)c->page_size, (uint64_t)c->heads,
+                            (uint64_t)c->n_pages};
+  const uint64_t strides[3] = {c->token_stride * size, c->head_stride * size,
+                               c->page_stride * size};
+  const uint32_t rows = c->page_size < attn::BT ? c->page_size : attn::BT;
+  const uint32_t box[4] = {G::FP8 ? (uint32_t)D : 64u, rows, 1, 1};
+  const CUtensorMapDataType type =
+      G::FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle swizzle =
+      G::FP8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  const uint64_t q_dims[3] = {(uint64_t)D, (uint64_t)(a.heads * a.group), (uint64_t)a.n_rows};
+  const uint64_t q_strides[2] = {(uint64_t)l.q_head * 2, (uint64_t)l.q_row * 2};
+  const uint32_t q_box[3] = {64, (uint32_t)a.group, (uint32_t)(NT / a.group)};
+  CUtensorMap tk, tv, tq;
+  if (dspark_make_tmap(&tk, type, 4, c->k, dims, strides, box, swizzle) != 0 ||
+      dspark_make_tmap(&tv, type, 4, c->v, dims, strides, box, swizzle) != 0 ||
+      dspark_make_tmap(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, l.q, q_dims, q_strides, q_box,
+                       CU_TENSOR_MAP_SWIZZLE_128B) != 0)
+    return DSPARK_ERR_CUDA;
+  auto kernel = attn::tree_attention_kernel<TYPE, D, NT>;
+  static DsparkPerDevice attr;
+  if (dspark_per_device(attr, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    G::SMEM_BYTES) == cudaSuccess
+                   ? 1
+                   : -1;
+      }) < 0)
+    return DSPARK_ERR_CUDA;
+  if (dspark_launch_pdl(kernel, dim3(l.ctas), dim3(G::THREADS), G::SMEM_BYTES, l.stream, tk, tv,
+                        tq, a) != cudaSuccess)
+    return DSPARK_ERR_CUDA;
+  if (dspark_launch_pdl(attn::tree_attention_join<D>, dim3(l.ctas, NT / 4), dim3(128), 0,
+                        l.stream, a, NT) != cudaSuccess)
+    return DSPARK_ERR_CUDA;
+  DSPARK_CHECK_LAUNCH();
+  dspark_count_launches(2);
+  return DSPARK_OK;
+}
+
 template <int TYPE, int D>
-__global__ void __launch_bounds__(128) tree_attention_rows(const AttnArgs a) {
-  constexpr int E = D / 32;
-  __shared__ float sm[4], sl[4], so[4][D];
-  const int row = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (row >= a.row_start[a.R] || row < a.row_start[0]) return;
-  int lo = 0, hi = a.R - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.row_start[mid] <= row) lo = mid;
-    else hi = mid - 1;
-  }
-  const int r = lo, row0 = a.row_start[r], node = row - row0;
-  int n = a.row_start[r + 1] - row0;
-  if (n > a.max_nodes) {
-    if (threadIdx.x == 0) dspark_set_status(DSPARK_ERR_LENGTH);
-    n = a.max_nodes;
-  }
-  if (node >= n) return;
-  int64_t ctx = max(a.ctx[r], 0), total = ctx + n;
-  const int64_t most = (int64_t)a.max_pages << a.page_shift;
-  if (total > most) {
-    if (threadIdx.x == 0) dspark_set_status(DSPARK_ERR_LENGTH);
-    total = most;
-    ctx = min(ctx, total);
-  }
-  const uint64_t mask = a.anc ? a.anc[row] : (2ull << node) - 1;
-  const int kv = h / (a.heads_q / a.heads);
-  const float ks = a.k_scale ? a.k_scale[kv] : 1.0f, vs = a.v_scale ? a.v_scale[kv] : 1.0f;
-  float q[E], o[E] = {};
-  for (int e = 0; e < E; ++e)
-    q[e] = __bfloat162float(a.q[row * a.q_row + h * a.q_head + lane + 32 * e]) * a.scale * ks;
-  float m = -INFINITY, l = 0.0f;
-  bool any = false;
-  for (int64_t p = warp; p < total; p += 4) {
-    if (p >= ctx && !((mask >> (p - ctx)) & 1)) continue;
-    any = true;
-    const int page = a.block_table[(size_t)r * a.max_pages + (p >> a.page_shift)];
-    const bool in = page >= 0 && page < a.n_pages;
-    if (!in) dspark_set_status(DSPARK_ERR_PAGES);
-    const int64_t at = in ? page * a.page_stride + (p & ((1 << a.page_shift) - 1)) * a.token_stride +
-                                kv * a.head_stride
-                          : 0;
-    float s = 0.0f;
-    for (int e = 0; e < E; ++e)
-      s += in ? q[e] * element<TYPE>(a.k, at + lane + 32 * e) : 0.0f;
-    s = warp_sum(s);
-    const float top = fmaxf(m, s), keep = m == top ? 1.0f : __expf(m - top);
-    const float w = __expf(s - top);
-    l = l * keep + w;
-    for (int e = 0; e < E; ++e)
-      o[e] = o[e] * keep + (in ? w * element<TYPE>(a.v, at + lane + 32 * e) : 0.0f);
-    m = top;
-  }
-  const int seen = __syncthreads_or(any);
-  for (int e = 0; e < E; ++e) so[warp][lane + 32 * e] = o[e];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-  __syncthreads();
-  const float top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  float total_l = 0.0f;
-  for (int w = 0; w < 4; ++w) total_l += sl[w] == 0.0f ? 0.0f : sl[w] * __expf(sm[w] - top);
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float x = 0.0f;
-    for (int w = 0; w < 4; ++w) x += sl[w] == 0.0f ? 0.0f : so[w][d] * __expf(sm[w] - top);
-    a.out[row * a.out_row + h * a.out_head + d] =
-        __float2bfloat16_rn(seen ? x / total_l * vs : 0.0f);
-  }
-  if (a.lse && threadIdx.x == 0)
-    a.lse[(size_t)row * a.heads_q + h] = seen ? top + logf(total_l) : -INFINITY;
+int launch_tile(const Launch &l, int nt) {
+  if (nt == 16) return launch<TYPE, D, 16>(l);
+  if (nt == 32) return launch<TYPE, D, 32>(l);
+  if constexpr (TYPE == DSPARK_KV_BF16)
+    if (nt == 128) return launch<TYPE, D, 128>(l);
+  return launch<TYPE, D, 64>(l);
 }
 
 }  // namespace
@@ -122,7 +103,7 @@ extern "C" size_t dspark_tree_attention_workspace_bytes(const dspark_kv_cache *c
   if (!dspark_kv_cache_ok(cache) || R < 1 || heads_q < 1 || heads_q % cache->heads ||
       heads_q / cache->heads > 64 || max_nodes < 1 || max_nodes > DSPARK_MAX_NODES)
     return 0;
-  return 256;
+  return layout_of(dspark_sm_count(), row_tile(cache, heads_q, max_nodes), cache->dim).bytes;
 }
 
 extern "C" int dspark_tree_attention(const dspark_kv_cache *cache, int32_t R, int32_t heads_q,
@@ -136,53 +117,57 @@ extern "C" int dspark_tree_attention(const dspark_kv_cache *cache, int32_t R, in
   const size_t need = dspark_tree_attention_workspace_bytes(cache, R, heads_q, max_nodes);
   if (need == 0 || n_rows < 0 || max_pages < 1) return DSPARK_ERR_ARG;
   if (n_rows == 0) return DSPARK_OK;
-  if (!q || !ctx || !row_start || !block_table ||
-      !out || ((uintptr_t)q & 15) || ((uintptr_t)out & 1) || q_row_stride <= 0 ||
-      q_head_stride <= 0 || q_row_stride % 8 || q_head_stride % 8 || out_row_stride <= 0 ||
+  const int64_t most = (int64_t)1 << 39;  // elements: a tensor map's strides are below 2^40 bytes
+  if (!q || !ctx || !row_start || !block_table || !out || ((uintptr_t)q & 15) ||
+      ((uintptr_t)out & 1) || q_row_stride <= 0 || q_head_stride <= 0 || q_row_stride >= most ||
+      q_head_stride >= most || q_row_stride % 8 || q_head_stride % 8 || out_row_stride <= 0 ||
       out_head_stride <= 0)
     return DSPARK_ERR_ARG;
   if (!workspace || ((uintptr_t)workspace & 255) || workspace_bytes < need)
     return DSPARK_ERR_WORKSPACE;
-  AttnArgs a;
-  a.k = (const uint8_t *)cache->k;
-  a.v = (const uint8_t *)cache->v;
-  a.k_scale = cache->type == DSPARK_KV_E4M3 ? cache->k_scale : nullptr;
-  a.v_scale = cache->type == DSPARK_KV_E4M3 ? cache->v_scale : nullptr;
-  a.page_stride = cache->page_stride;
-  a.token_stride = cache->token_stride;
-  a.head_stride = cache->head_stride;
-  a.n_pages = cache->n_pages;
-  a.page_shift = 31 - __builtin_clz((unsigned)cache->page_size);
-  a.heads = cache->heads;
-  a.dim = cache->dim;
+  Launch l;
+  l.cache = cache;
+  l.q = q;
+  l.q_row = q_row_stride;
+  l.q_head = q_head_stride;
+  l.ctas = dspark_sm_count();
+  l.stream = stream;
+  const bool fp8 = cache->type == DSPARK_KV_E4M3;
+  const int nt = row_tile(cache, heads_q, max_nodes);
+  const Layout at = layout_of(l.ctas, nt, cache->dim);
+  const int64_t size = dspark_kv_bytes(cache->type);
+  Args &a = l.a;
   a.R = R;
-  a.heads_q = heads_q;
+  a.heads = cache->heads;
+  a.group = heads_q / cache->heads;
   a.max_nodes = max_nodes;
   a.n_rows = n_rows;
   a.max_pages = max_pages;
-  a.q = (const bf16 *)q;
-  a.q_row = q_row_stride;
-  a.q_head = q_head_stride;
+  a.page_shift = 31 - __builtin_clz((unsigned)cache->page_size);
+  a.n_pages = cache->n_pages;
   a.ctx = ctx;
   a.row_start = row_start;
-  a.anc = anc;
   a.block_table = block_table;
+  a.anc = anc;
+  a.k_scale = fp8 ? cache->k_scale : nullptr;
+  a.v_scale = fp8 ? cache->v_scale : nullptr;
+  a.v = (const uint8_t *)cache->v;
+  a.page_bytes = cache->page_stride * size;
+  a.token_bytes = cache->token_stride * size;
+  a.head_bytes = cache->head_stride * size;
   a.scale = scale;
   a.out = (bf16 *)out;
   a.out_row = out_row_stride;
   a.out_head = out_head_stride;
   a.lse = lse;
-  const dim3 grid(n_rows, heads_q);
-  if (cache->type == DSPARK_KV_E4M3) {
-    if (cache->dim == 64) tree_attention_rows<DSPARK_KV_E4M3, 64><<<grid, 128, 0, stream>>>(a);
-    else tree_attention_rows<DSPARK_KV_E4M3, 128><<<grid, 128, 0, stream>>>(a);
-  } else {
-    if (cache->dim == 64) tree_attention_rows<DSPARK_KV_BF16, 64><<<grid, 128, 0, stream>>>(a);
-    else tree_attention_rows<DSPARK_KV_BF16, 128><<<grid, 128, 0, stream>>>(a);
-  }
-  DSPARK_CHECK_LAUNCH();
-  dspark_count_launches(1);
-  return DSPARK_OK;
+  a.part_o = (float *)workspace;
+  a.part_ml = (float *)((uint8_t *)workspace + at.ml);
+  a.desc = (int *)((uint8_t *)workspace + at.desc);
+  if (fp8)
+    return cache->dim == 64 ? launch_tile<DSPARK_KV_E4M3, 64>(l, nt)
+                            : launch_tile<DSPARK_KV_E4M3, 128>(l, nt);
+  return cache->dim == 64 ? launch_tile<DSPARK_KV_BF16, 64>(l, nt)
+                          : launch_tile<DSPARK_KV_BF16, 128>(l, nt);
 }
 
 int dspark_status_attention(int clear) {

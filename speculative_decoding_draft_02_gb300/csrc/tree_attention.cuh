@@ -1,0 +1,914 @@
+// tree_attention.cuh — attention of every request's drafted tree (or chain, or
+// single token) over its paged KV cache, on the tensor cores.
+//
+//   s_p = scale * q . K_p,  out = sum_p e^{s_p} V_p / sum_p e^{s_p}
+// over p < ctx, and p = ctx + j for the nodes j in the row's ancestor mask.
+//
+// A round has few query rows for each KV head (nodes x query heads per KV head)
+// and long contexts, so the product is bound by reading K and V once.  Both
+// products therefore take the cache as the 128-row operand and the query rows as
+// the narrow one (N = NT columns):
+//   S^T [128 tokens x NT] = K_tile . Q^T       O^T [D x NT] += V_tile^T . P^T
+// With the rows on the 128-row side instead, a chain of 6 nodes x 4 heads would
+// leave 104 of 128 accumulator rows empty and one warp to do every exponential.
+// Here a thread owns one token (TMEM lane) and the rows run along registers.  Its
+// price is the maximum over tokens, which lies across lanes; it is paid only when
+// it matters: the exponent's reference is kept from tile to tile and raised (with
+// O rescaled) only when some score exceeds it by 2^8.
+//
+// A weight meets V as the sum of two bf16 numbers, its rounding and what that
+// left out (columns j and NT + j of P, and two parts of O added at the end):
+// rounded to one, a row's error would be of the output's own rounding's size,
+// and below 64 rows the wider product costs nothing, as reading V's tile bounds
+// it.
+//
+// Work is cut into units of (request, KV head, row tile, 128-token tile), listed
+// in that order, and every CTA takes an equal share of the list: ragged contexts
+// balance, and a long context is split over as many CTAs as there are.  A CTA's
+// first and last item may be cut; those leave (O, maximum, sum) in the workspace
+// and tree_attention_join adds the pieces in order (no atomics: the same bits
+// from call to call).
+//
+// One CTA per SM: warp 0 loads (TMA, one copy per page and 64 columns), warp 1
+// issues the MMAs, 4 * CG warps do the softmax (a group of four per 32 columns),
+// and for an 8-bit cache four more widen the tiles to bf16 between two rings.
+// Every wait is bounded; on expiry the CTA raises DSPARK_ERR_TIMEOUT, drains its
+// own copies and MMAs, frees TMEM and exits.
+#pragma once
+#include <cuda_fp8.h>
+
+#include "kv_cache.cuh"
+#include "tcgen05.cuh"
+
+namespace attn {
+
+constexpr int BT = 128;                 // tokens of a tile
+constexpr int SMEM_LIMIT = 232448;      // 227 KB
+constexpr int CTL_BYTES = 2048;
+constexpr int MAX_SLOTS = 12;
+constexpr float RAISE = 8.0f;           // log2: how far scores may pass the reference
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+struct Args {
+  int R, heads, group, max_nodes, n_rows, max_pages, page_shift, n_pages;
+  const int *ctx, *row_start, *block_table;
+  const uint64_t *anc;
+  const float *k_scale, *v_scale;
+  const uint8_t *v;                     // for non-finite values only
+  int64_t page_bytes, token_bytes, head_bytes;
+  float scale;
+  bf16 *out;
+  int64_t out_row, out_head;
+  float *lse;
+  float *part_o;                        // [ctas][2][NT][D]
+  float *part_ml;                       // [ctas][2][2][NT]
+  int *desc;                            // [ctas][8]: the item each CTA leaves to its successors
+};
+
+template <int TYPE, int D, int NT>
+struct Geo {
+  static constexpr bool FP8 = TYPE == DSPARK_KV_E4M3;
+  static constexpr int CW = NT < 32 ? NT : 32;  // columns of a softmax thread
+  static constexpr int CG = NT / CW;
+  static constexpr int SW = 4 * CG;
+  static constexpr int CV = FP8 ? 4 : 0;
+  static constexpr int THREADS = 32 * (2 + SW + CV);
+  static constexpr int SLOT = BT * D * 2;
+  static constexpr int Q_BYTES = NT * D * 2;
+  static constexpr int P_BYTES = BT * 128 * (NT > 32 ? NT / 32 : 1);
+  static constexpr int ROOM = SMEM_LIMIT - CTL_BYTES - Q_BYTES - P_BYTES;
+  static constexpr int RAW = FP8 ? BT * D : 0;
+  // 8-bit: three widened tiles (one read by each product, one being written);
+  // the copies in flight are the raw ring's
+  static constexpr int SLOTS = FP8 ? 3 : (ROOM / SLOT < MAX_SLOTS ? ROOM / SLOT : MAX_SLOTS);
+  static constexpr int RAWS_FIT = FP8 ? (ROOM - 3 * SLOT) / (RAW + !FP8) : 0;
+  static constexpr int RAWS = RAWS_FIT < MAX_SLOTS ? RAWS_FIT : MAX_SLOTS;
+  static constexpr int SMEM_BYTES = SLOTS * SLOT + RAWS * RAW + Q_BYTES + P_BYTES + CTL_BYTES;
+  static constexpr uint32_t TMEM_COLS = 4 * NT;  // two tiles of S, and O's two parts
+  static_assert(SLOTS >= 3 && (!FP8 || RAWS >= 3) && SMEM_BYTES <= SMEM_LIMIT, "shared memory");
+};
+
+struct Ctl {
+  uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], rfull[MAX_SLOTS], rempty[MAX_SLOTS];
+  uint64_t q_full, s_full[2], s_empty[2], p_full, pv_done, drain;
+  alignas(16) float nm[128];  // minus each column's reference exponent (log2); +inf: none yet
+  int top[128];           // its maximum score so far, as an ordered key
+  long long sums[32];
+  unsigned long long odd[3];  // nodes with non-finite V, by segment mod 3
+  long long start_off;
+  int start_r;
+  int abort;
+  uint32_t tmem;
+};
+static_assert(sizeof(Ctl) <= CTL_BYTES, "control block");
+
+// f32 as an int of the same order (-0 below +0; NaN outside the numbers).
+__device__ __forceinline__ int order_key(float x) {
+  const int b = __float_as_int(x);
+  return b >= 0 ? b : b ^ 0x7fffffff;
+}
+__device__ __forceinline__ float order_value(int k) {
+  return __int_as_float(k >= 0 ? k : k ^ 0x7fffffff);
+}
+
+// A request as the kernel takes it: every later index is in bounds by this.
+struct Request {
+  int row0, n, ctx, total, tiles, row_tiles;
+  __device__ __forceinline__ bool set(const Args &a, int nodes_tile, int c, int start, int end) {
+    bool ok = true;
+    row0 = min(max(start, 0), a.n_rows);
+    n = min(max(end, row0), a.n_rows) - row0;
+    if (n > a.max_nodes) {
+      n = a.max_nodes;
+      ok = false;
+    }
+    ctx = max(c, 0);
+    const long long cap = min((long long)a.max_pages << a.page_shift, 0x7fffff00ll);
+    if ((long long)ctx + n > cap) {
+      total = (int)cap;
+      ctx = min(ctx, total);
+      ok = false;
+    } else {
+      total = ctx + n;
+    }
+    tiles = n ? (total + BT - 1) / BT : 0;
+    row_tiles = (n + nodes_tile - 1) / nodes_tile;
+    return ok || n == 0;
+  }
+  __device__ __forceinline__ long long units(const Args &a) const {
+    return (long long)tiles * row_tiles * a.heads;
+  }
+};
+
+// One CTA's consecutive tiles of one item.
+struct Segment {
+  int r, row0, n, ctx, total, tiles, h, node0, nodes, tb, te;
+};
+
+// Walks a CTA's share of the list of units.  The next request's lengths are read
+// one request ahead.
+struct Walker {
+  const Args &a;
+  int nodes_tile, r, h, rt, tile, next_ctx, next_end, end;
+  long long pos, last;  // the next unit, and the end of the share
+  Request q;
+  __device__ Walker(const Args &args, int nt) : a(args), nodes_tile(nt) {}
+  __device__ __forceinline__ void ahead() {
+    if (r + 1 < a.R) {
+      next_ctx = a.ctx[r + 1];
+      next_end = a.row_start[r + 2];
+    }
+  }
+  __device__ __forceinline__ void begin(int r0, long long off, long long u0, long long u1) {
+    pos = u0;
+    last = u1;
+    if (u0 >= u1) return;
+    r = r0;
+    end = a.row_start[r + 1];
+    q.set(a, nodes_tile, a.ctx[r], a.row_start[r], end);
+    const long long item = off / q.tiles;
+    tile = (int)(off - item * q.tiles);
+    h = (int)(item / q.row_tiles);
+    rt = (int)(item - (long long)h * q.row_tiles);
+    ahead();
+  }
+  __device__ __forceinline__ bool next(Segment &s) {
+    if (pos >= last) return false;
+    if (h == a.heads) {
+      h = 0;
+      do {
+        if (++r >= a.R) {
+          pos = last;
+          return false;
+        }
+        const int start = end;
+        end = next_end;
+        q.set(a, nodes_tile, next_ctx, start, end);
+        ahead();
+      } while (q.n == 0);
+    }
+    s.r = r;
+    s.row0 = q.row0;
+    s.n = q.n;
+    s.ctx = q.ctx;
+    s.total = q.total;
+    s.tiles = q.tiles;
+    s.h = h;
+    s.node0 = rt * nodes_tile;
+    s.nodes = min(nodes_tile, q.n - s.node0);
+    s.tb = tile;
+    s.te = (int)min((long long)q.tiles, tile + (last - pos));
+    pos += s.te - s.tb;
+    tile = s.te;
+    if (tile == q.tiles) {
+      tile = 0;
+      if (++rt == q.row_tiles) {
+        rt = 0;
+        ++h;
+      }
+    }
+    return true;
+  }
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = tc::mbar_wait(bar, parity, abort) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+__device__ __forceinline__ void group_sync(int id) {
+  asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ bool group_any(int id, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)p), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Two 8-bit floats as two bf16 (exact): through f16, which holds every value.
+__device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+  return pack_bf16(f.x, f.y);
+}
+
+// Sum of v[j] over the warp's lanes, left in lane j (lanes j and j + 16 of 16
+// columns): 31 exchanges for 32 columns, in a fixed order.
+template <int CW>
+__device__ __forceinline__ float column_sums(float (&v)[CW], int lane) {
+  if constexpr (CW == 16) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], 16);
+  }
+#pragma unroll
+  for (int o = CW / 2; o; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int j = 0; j < o; ++j) {
+      const float send = up ? v[j] : v[j + o], keep = up ? v[j + o] : v[j];
+      v[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  return v[0];
+}
+
+template <int TYPE, int D, int NT>
+__global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
+    tree_attention_kernel(const __grid_constant__ CUtensorMap tma_k,
+                          const __grid_constant__ CUtensorMap tma_v,
+                          const __grid_constant__ CUtensorMap tma_q, const Args a) {
+  using G = Geo<TYPE, D, NT>;
+  constexpr int CW = G::CW, CG = G::CG, SLOTS = G::SLOTS, RAWS = G::RAWS;
+  constexpr int HALVES = D / 64;            // 64-column halves of a head
+  constexpr int HALF_BYTES = BT * 128;      // one half of a tile
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t *slots = smem;
+  uint8_t *raws = slots + SLOTS * G::SLOT;
+  uint8_t *sq = raws + RAWS * G::RAW;
+  uint8_t *sp = sq + G::Q_BYTES;
+  Ctl *ctl = reinterpret_cast<Ctl *>(sp + G::P_BYTES);
+  volatile int *abort = &ctl->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = blockIdx.x;
+  const int nodes_tile = NT / a.group;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < SLOTS; ++s) {
+      tc::mbar_init(&ctl->full[s], G::FP8 ? G::CV : 1);
+      tc::mbar_init(&ctl->empty[s], 1);
+    }
+    for (int s = 0; s < RAWS; ++s) {
+      tc::mbar_init(&ctl->rfull[s], 1);
+      tc::mbar_init(&ctl->rempty[s], G::CV);
+    }
+    tc::mbar_init(&ctl->q_full, 1);
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(&ctl->s_full[b], 1);
+      tc::mbar_init(&ctl->s_empty[b], G::SW);
+    }
+    tc::mbar_init(&ctl->p_full, G::SW);
+    tc::mbar_init(&ctl->pv_done, 1);
+    tc::mbar_init(&ctl->drain, 1);
+    for (int i = 0; i < 3; ++i) ctl->odd[i] = 0;
+    ctl->abort = 0;
+    tc::fence_barrier_init();
+    tc::tma_prefetch_desc(&tma_k);
+    tc::tma_prefetch_desc(&tma_v);
+    tc::tma_prefetch_desc(&tma_q);
+  }
+  if (warp == 1) tc::tmem_alloc(&ctl->tmem, G::TMEM_COLS);
+  pdl_trigger();
+  pdl_wait();
+
+  // the list's length, and where this CTA's share of it begins
+  const int per = (a.R + G::THREADS - 1) / G::THREADS;
+  const int r_lo = min((int)threadIdx.x * per, a.R), r_hi = min(r_lo + per, a.R);
+  long long mine = 0;
+  for (int r = r_lo; r < r_hi; ++r) {
+    Request q;
+    if (!q.set(a, nodes_tile, a.ctx[r], a.row_start[r], a.row_start[r + 1]) && cta == 0)
+      dspark_set_status(DSPARK_ERR_LENGTH);
+    mine += q.units(a);
+  }
+  long long upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += t;
+  }
+  if (lane == 31) ctl->sums[warp] = upto;
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  long long all = lane < G::THREADS / 32 ? ctl->sums[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, all, o);
+    if (lane >= o) all += t;
+  }
+  const long long before_warp = warp ? __shfl_sync(0xffffffffu, all, warp - 1) : 0;
+  const long long units = __shfl_sync(0xffffffffu, all, 31);
+  // with fewer units than CTAs the first ones take one each: an item's pieces lie
+  // in consecutive CTAs
+  const long long shares = min((long long)gridDim.x, units);
+  const long long u0 = cta < shares ? units * cta / shares : units;
+  const long long u1 = cta < shares ? units * (cta + 1) / shares : units;
+  const long long first = before_warp + upto - mine;
+  if (mine > 0 && first <= u0 && u0 < first + mine) {
+    long long at = first;
+    for (int r = r_lo; r < r_hi; ++r) {
+      Request q;
+      q.set(a, nodes_tile, a.ctx[r], a.row_start[r], a.row_start[r + 1]);
+      const long long m = q.units(a);
+      if (u0 < at + m) {
+        ctl->start_r = r;
+        ctl->start_off = u0 - at;
+        break;
+      }
+      at += m;
+    }
+  }
+  __syncthreads();
+  const uint32_t tmem = ctl->tmem, tmem_o = tmem + 2 * NT;
+  Walker walk(a, nodes_tile);
+  walk.begin(ctl->start_r, ctl->start_off, u0, u1);
+  Segment s;
+
+  if (warp == 0) {
+    // -------------------------------------------------- copies of K and V ----
+    // Row tiles of one item read the same K and V: keep them in L2 for the next.
+    const uint64_t pol =
+        a.max_nodes > nodes_tile ? tc::policy_evict_normal() : tc::policy_evict_first();
+    constexpr int RING = G::FP8 ? RAWS : SLOTS;
+    uint64_t *full = G::FP8 ? ctl->rfull : ctl->full, *empty = G::FP8 ? ctl->rempty : ctl->empty;
+    uint8_t *ring = G::FP8 ? raws : slots;
+    constexpr int RING_BYTES = G::FP8 ? G::RAW : G::SLOT;
+    const int rows = min(1 << a.page_shift, BT), boxes = BT / rows;
+    const uint32_t box_bytes = (uint32_t)(rows * D * (G::FP8 ? 1 : 2));
+    int slot = 0;
+    uint32_t phase = 0, used = 0;
+    bool ok = true;
+    while (ok && walk.next(s)) {
+      const int *table = a.block_table + (size_t)s.r * a.max_pages;
+      // the page of box `lane` of a tile; none past the request's end
+      auto page_of = [&](int tile) {
+        const int p = tile * BT + lane * rows;
+        return lane < boxes && p < s.total ? table[p >> a.page_shift] : 0;
+      };
+      int page = page_of(s.tb);
+      for (int tile = s.tb; ok && tile < s.te; ++tile) {
+        const int here = page, p = tile * BT + lane * rows;
+        const bool mine = lane < boxes && p < s.total;
+        if (tile + 1 < s.te) page = page_of(tile + 1);
+        const int n_boxes = __popc(__ballot_sync(0xffffffffu, mine));
+        const bool in = here >= 0 && here < a.n_pages;
+        if (mine && !in) dspark_set_status(DSPARK_ERR_PAGES);
+        const int z = in ? here : -1;  // outside the map: zeros
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          if (!warp_wait(&empty[slot], phase ^ 1, abort)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) tc::mbar_expect_tx(&full[slot], n_boxes * box_bytes);
+          __syncwarp();
+          if (mine) {
+            const CUtensorMap *map = kv ? &tma_v : &tma_k;
+            uint8_t *dst = ring + slot * RING_BYTES;
+            const int y = p & ((1 << a.page_shift) - 1);
+            if constexpr (G::FP8) {
+              tc::tma_load_4d(dst + lane * rows * D, map, 0, y, s.h, z, &full[slot], pol);
+            } else {
+#pragma unroll
+              for (int c = 0; c < HALVES; ++c)
+                tc::tma_load_4d(dst + c * HALF_BYTES + lane * rows * 128, map, c * 64, y, s.h, z,
+                                &full[slot], pol);
+            }
+          }
+          used |= 1u << slot;
+          if (++slot == RING) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+      }
+    }
+    // drain: every copy issued has landed (a slot's last fill is of this pass of
+    // the ring before `slot`, of the last pass from it on)
+    volatile int never = 0;
+    for (int i = 0; i < RING; ++i)
+      if (used >> i & 1) warp_wait(&full[i], i < slot ? phase : phase ^ 1, &never);
+  } else if (warp == 1) {
+    // -------------------------------------------------------- MMA issuer ----
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = tc::idesc_bf16(BT, NT);
+      constexpr uint32_t idesc_o = tc::idesc_bf16(128, 2 * NT) | tc::IDESC_A_MN | tc::IDESC_B_MN;
+      int k_slot = 0, v_slot = 1;
+      uint32_t k_phase = 0, v_phase = 0, t = 0, seg = 0;
+      uint32_t acc = 0;  // whether the pending tile adds to O
+      auto advance = [&](int &slot, uint32_t &phase) {
+        slot += 2;
+        if (slot >= SLOTS) {
+          slot -= SLOTS;
+          phase ^= 1;
+        }
+      };
+      auto pv = [&](uint32_t tile) -> bool {
+        if (!tc::mbar_wait(&ctl->full[v_slot], v_phase, abort)) return false;
+        if (!tc::mbar_wait(&ctl->p_full, tile & 1, abort)) return false;
+        tc::fence_after_sync();
+        // D = 64: the 128-row operand's second 64 rows are the first again, and
+        // accumulator lanes 64..127 are not read
+        const uint64_t vd = tc::smem_desc_sw128_mn(slots + v_slot * G::SLOT,
+                                                   D == 128 ? HALF_BYTES : 0);
+        const uint64_t pd = tc::smem_desc_sw128_mn(sp, HALF_BYTES);
+#pragma unroll
+        for (int k = 0; k < BT / 16; ++k)
+          tc::umma_bf16(tmem_o, vd + 128 * k, pd + 128 * k, idesc_o, acc | (k != 0));
+        tc::umma_commit(&ctl->empty[v_slot]);
+        tc::umma_commit(&ctl->pv_done);
+        advance(v_slot, v_phase);
+        return true;
+      };
+      bool ok = true;
+      while (ok && walk.next(s)) {
+        if (!tc::mbar_wait(&ctl->q_full, seg & 1, abort)) break;
+        ++seg;
+        for (int tile = s.tb; tile < s.te; ++tile) {
+          const uint32_t b = t & 1;
+          if (!tc::mbar_wait(&ctl->full[k_slot], k_phase, abort) ||
+              !tc::mbar_wait(&ctl->s_empty[b], ((t >> 1) & 1) ^ 1, abort)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t kd =
+                tc::smem_desc_sw128(slots + k_slot * G::SLOT + (k / 4) * HALF_BYTES);
+            const uint64_t qd = tc::smem_desc_sw128(sq + (k / 4) * NT * 128);
+            tc::umma_bf16(tmem + b * NT, kd + 2 * (k & 3), qd + 2 * (k & 3), idesc_s, k != 0);
+          }
+          tc::umma_commit(&ctl->empty[k_slot]);
+          tc::umma_commit(&ctl->s_full[b]);
+          advance(k_slot, k_phase);
+          if (t > 0 && !pv(t - 1)) {
+            ok = false;
+            break;
+          }
+          acc = tile != s.tb;
+          ++t;
+        }
+      }
+      if (ok && t > 0 && u0 < u1) pv(t - 1);
+      tc::umma_commit(&ctl->drain);  // all MMAs issued have finished
+      volatile int never = 0;
+      tc::mbar_wait(&ctl->drain, 0, &never);
+    }
+    __syncwarp();
+  } else if (warp < 2 + G::SW) {
+    // ----------------------------------------------------------- softmax ----
+    const int quarter = warp & 3, cg = (warp - 2) >> 2, bar = 1 + cg;
+    const int token = quarter * 32 + lane, c0 = cg * CW;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const bool leader = warp == 2 && lane == 0;
+    // P[token][column]: 64-column halves; 16-byte chunk c of a row lies at
+    // c ^ (token & 7)
+    const int p_chunk = (c0 % 64) / 8;
+    auto p_at = [&](int col) -> uint4 * {
+      return reinterpret_cast<uint4 *>(sp + (col / 64) * HALF_BYTES + token * 128 +
+                                       (((col % 64) / 8) ^ (token & 7)) * 16);
+    };
+    // the column sums' meeting place: this group's own chunks of P rows 0, 8, ..
+    auto sum_slot = [&](int q, int j) -> float * {
+      return reinterpret_cast<float *>(sp + (c0 / 64) * HALF_BYTES + 8 * (q * 2 + j / 16) * 128 +
+                                       p_chunk * 16) + j % 16;
+    };
+    auto load_q = [&](const Segment &n) {
+      const int box_bytes = nodes_tile * a.group * 128;
+      tc::mbar_expect_tx(&ctl->q_full, HALVES * box_bytes);
+      for (int c = 0; c < HALVES; ++c)
+        tc::tma_load_3d(sq + c * NT * 128, &tma_q, c * 64, n.h * a.group, n.row0 + n.node0,
+                        &ctl->q_full, tc::policy_evict_normal());
+    };
+    if (leader) a.desc[cta * 8] = 0;
+    bool have = walk.next(s);
+    if (have && leader) load_q(s);
+    uint32_t t = 0, seg = 0, v_slot = 1, v_phase = 0, q_loads = have;
+    bool ok = true, gone = false;
+    while (have) {
+      Segment nx = s;
+      bool more = false;
+      const float ks = a.k_scale ? a.k_scale[s.h] : 1.0f, vs = a.v_scale ? a.v_scale[s.h] : 1.0f;
+      const float c = a.scale * ks * LOG2E;
+      const int count = min(max(s.nodes * a.group - c0, 0), CW);  // this group's columns in use
+      // lane j: the ancestor mask of column c0 + j
+      unsigned long long word = 0;
+      if (lane < count) {
+        const int node = s.node0 + (c0 + lane) / a.group;
+        word = a.anc ? a.anc[s.row0 + node] : (2ull << node) - 1;
+        if (s.n < 64) word &= (1ull << s.n) - 1;
+      }
+      if (quarter == 0 && lane < CW) {
+        // a column that no row uses never calls for a higher reference
+        ctl->nm[c0 + lane] = lane < count ? INFINITY : -INFINITY;
+        ctl->top[c0 + lane] = order_key(-INFINITY);
+      }
+      if (leader) ctl->odd[(seg + 1) % 3] = 0;
+      group_sync(bar);
+      float l[CW];
+#pragma unroll
+      for (int j = 0; j < CW; ++j) l[j] = 0.0f;
+      bool force = true;  // some column has no reference yet
+
+      for (int tile = s.tb; tile < s.te; ++tile, ++t) {
+        const uint32_t b = t & 1;
+        ok = ok && warp_wait(&ctl->s_full[b], (t >> 1) & 1, abort);
+        if (tile == s.te - 1) {  // the segment's last use of Q is behind
+          more = walk.next(nx);
+          if (ok && more) {
+            if (leader) load_q(nx);
+            ++q_loads;
+          }
+        }
+        const int pos = tile * BT + token;
+        const bool edge = tile * BT + BT > s.ctx;  // some token is a node or past the end
+        uint32_t sr[CW];
+        float e[CW];
+        tc::fence_after_sync();
+        auto scores = [&](bool shifted) {  // e = c * S (- reference), masked
+          tc::tmem_ld(tmem + lanes + b * NT + c0, sr);
+          tc::tmem_wait_ld();
+          tc::reg_fence(sr);
+#pragma unroll
+          for (int j = 0; j < CW; j += 4) {
+            float4 nm = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (shifted) nm = *reinterpret_cast<const float4 *>(&ctl->nm[c0 + j]);
+            e[j] = fmaf(__uint_as_float(sr[j]), c, nm.x);
+            e[j + 1] = fmaf(__uint_as_float(sr[j + 1]), c, nm.y);
+            e[j + 2] = fmaf(__uint_as_float(sr[j + 2]), c, nm.z);
+            e[j + 3] = fmaf(__uint_as_float(sr[j + 3]), c, nm.w);
+          }
+          if (edge) {
+            const int node = pos - s.ctx;
+            const bool ctx_token = node < 0, end = pos >= s.total;
+#pragma unroll
+            for (int j = 0; j < CW; ++j) {
+              const unsigned long long w = __shfl_sync(0xffffffffu, word, j);
+              const bool seen = ctx_token || (!end && (w >> (node & 63) & 1));
+              e[j] = seen ? e[j] : -INFINITY;
+            }
+          }
+        };
+        float most = -INFINITY;
+        if (ok) {
+          scores(true);
+#pragma unroll
+          for (int j = 0; j < CW; j += 8)
+            if (j < count) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) most = fmaxf(most, e[j + i]);
+            }
+        }
+        bool waited = t == 0;
+        if (group_any(bar, force || most > RAISE || !ok)) {
+          if (group_any(bar, !ok)) {
+            gone = true;
+            break;
+          }
+          // raise the references to the columns' maxima
+          scores(false);
+          int key = order_key(-INFINITY);
+#pragma unroll
+          for (int j = 0; j < CW; ++j) {
+            const int m = __reduce_max_sync(0xffffffffu, order_key(e[j]));
+            if (lane == j) key = m;
+          }
+          if (lane < CW) atomicMax(&ctl->top[c0 + lane], key);
+          group_sync(bar);
+          if (!waited) ok = warp_wait(&ctl->pv_done, (t - 1) & 1, abort);
+          waited = true;
+          tc::fence_after_sync();
+          force = false;
+          const bool scale_o = tile != s.tb && ok;
+#pragma unroll
+          for (int j = 0; j < CW; j += 16) {
+            float keep[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float top = order_value(ctl->top[c0 + j + i]), old = -ctl->nm[c0 + j + i];
+              force = force || (top == -INFINITY && j + i < count);
+              // no reference before: nothing to keep
+              keep[i] = old == -INFINITY ? 0.0f : ex2_fast(old - top);
+              l[j + i] *= keep[i];
+              e[j + i] -= top == -INFINITY ? 0.0f : top;
+            }
+            if (scale_o) {
+#pragma unroll
+              for (int part = 0; part < 2; ++part) {
+                uint32_t o[16];
+                tc::tmem_ld16(tmem_o + lanes + part * NT + c0 + j, o);
+                tc::tmem_wait_ld();
+                tc::reg_fence(o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  o[i] = __float_as_uint(__uint_as_float(o[i]) * keep[i]);
+                tc::tmem_st16(tmem_o + lanes + part * NT + c0 + j, o);
+              }
+            }
+          }
+          if (scale_o) tc::tmem_wait_st();
+          group_sync(bar);
+          if (quarter == 0 && lane < count) ctl->nm[c0 + lane] = -order_value(ctl->top[c0 + lane]);
+          group_sync(bar);
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ctl->s_empty[b]);
+        if (!waited) ok = warp_wait(&ctl->pv_done, (t - 1) & 1, abort);  // P is free
+#pragma unroll
+        for (int j = 0; j < CW; j += 8)
+          if (j < count) {
+            float w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              w[i] = ex2_fast(e[j + i]);
+              l[j + i] += w[i];
+            }
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              hi[i] = pack_bf16(w[2 * i], w[2 * i + 1]);
+              lo[i] = pack_bf16(w[2 * i] - bf16_lo(hi[i]), w[2 * i + 1] - bf16_hi(hi[i]));
+            }
+            *p_at(c0 + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *p_at(NT + c0 + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        if (edge) {
+          // What a row does not see must not meet its zero weight as infinity or
+          // NaN: V past the end is cleared, and so are the nodes' non-finite
+          // values, which the epilogue gives to the rows that do see them.
+          ok = ok && warp_wait(&ctl->full[v_slot], v_phase, abort);
+          uint8_t *row = slots + v_slot * G::SLOT + token * 128;
+          if (ok && pos >= s.ctx) {
+            for (int i = cg; i < HALVES * 8; i += CG) {
+              uint4 *x = reinterpret_cast<uint4 *>(row + (i / 8) * HALF_BYTES + (i % 8) * 16);
+              if (pos >= s.total) {
+                *x = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              uint4 y = *x;
+              uint32_t *w = reinterpret_cast<uint32_t *>(&y);
+              bool odd = false;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u, odd = true;
+                if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0xffffu, odd = true;
+              }
+              if (odd) {
+                *x = y;
+                atomicOr(&ctl->odd[seg % 3], 1ull << (pos - s.ctx));
+              }
+            }
+          }
+        }
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ctl->p_full);
+        v_slot += 2;
+        if (v_slot >= SLOTS) {
+          v_slot -= SLOTS;
+          v_phase ^= 1;
+        }
+      }
+      if (gone) break;
+
+      // ------------------------------------------------- end of a segment ----
+      ok = ok && warp_wait(&ctl->pv_done, (t - 1) & 1, abort);
+      const float part = column_sums<CW>(l, lane);
+      if (ok && lane < CW) *sum_slot(quarter, lane) = part;
+      if (group_any(bar, !ok)) {
+        gone = true;
+        break;
+      }
+      tc::fence_after_sync();
+      float sum = 0.0f, top = 0.0f;
+      if (lane < CW) {
+        sum = (*sum_slot(0, lane) + *sum_slot(1, lane)) + (*sum_slot(2, lane) + *sum_slot(3, lane));
+        top = order_value(ctl->top[c0 + lane]);
+      }
+      const unsigned long long odd = ctl->odd[seg % 3];
+      const bool whole = s.tb == 0 && s.te == s.tiles;
+      const int piece = s.tb == 0 ? 1 : 0;
+      const int d = token;  // accumulator lane = column of the head
+      const bool sees = s.ctx > 0 || word != 0;
+      const float inv = sees ? vs / sum : 0.0f;
+      const int col = c0 + lane, node = s.node0 + col / a.group;
+      const int head = s.h * a.group + col % a.group;
+      if (quarter == 0 && lane < count) {
+        if (!whole) {
+          float *ml = a.part_ml + (size_t)(cta * 2 + piece) * 2 * NT + col;
+          ml[0] = top;
+          ml[NT] = sum;
+        } else if (a.lse) {
+          a.lse[(size_t)(s.row0 + node) * a.heads * a.group + head] =
+              sees ? (top + log2f(sum)) * LN2 : -INFINITY;
+        }
+      }
+      if (quarter * 32 < D) {
+#pragma unroll 1
+        for (int j = 0; j < CW; j += 16) {
+          if (j >= count) break;
+          uint32_t o[16], o_lo[16];
+          tc::tmem_ld16(tmem_o + lanes + c0 + j, o);
+          tc::tmem_ld16(tmem_o + lanes + NT + c0 + j, o_lo);
+          tc::tmem_wait_ld();
+          tc::reg_fence(o);
+          tc::reg_fence(o_lo);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(o_lo[i]));
+          for (unsigned long long m = odd; m; m &= m - 1) {
+            const int at = __ffsll((long long)m) - 1, pos = s.ctx + at;
+            const int page = a.block_table[(size_t)s.r * a.max_pages + (pos >> a.page_shift)];
+            float x = 0.0f;
+            if (page >= 0 && page < a.n_pages) {
+              const uint8_t *v = a.v + page * a.page_bytes +
+                                 (pos & ((1 << a.page_shift) - 1)) * a.token_bytes +
+                                 s.h * a.head_bytes;
+              if constexpr (G::FP8)
+                x = __uint_as_float(widen_e4m3x2(v[d]) << 16);
+              else
+                x = __bfloat162float(reinterpret_cast<const bf16 *>(v)[d]);
+            }
+            const bool finite = fabsf(x) < INFINITY;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const unsigned long long w = __shfl_sync(0xffffffffu, word, j + i);
+              if (!finite && (w >> at & 1)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
+            }
+          }
+          float *po = a.part_o + ((size_t)(cta * 2 + piece) * NT + c0 + j) * D + d;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float f = __shfl_sync(0xffffffffu, inv, j + i);
+            const int row = __shfl_sync(0xffffffffu, s.row0 + node, j + i);
+            const int hd = __shfl_sync(0xffffffffu, head, j + i);
+            if (j + i < count) {
+              if (whole)
+                a.out[row * a.out_row + hd * a.out_head + d] =
+                    __float2bfloat16_rn(__uint_as_float(o[i]) * f);
+              else
+                po[i * D] = __uint_as_float(o[i]);
+            }
+          }
+        }
+      }
+      if (leader && !whole && piece == 1) {
+        // the item goes on in the CTAs up to the one that holds its last unit
+        const long long end = u1 + (s.tiles - s.te);
+        int *desc = a.desc + cta * 8;
+        desc[1] = s.row0;
+        desc[2] = s.node0;
+        desc[3] = s.nodes;
+        desc[4] = s.h;
+        desc[0] = (int)((end * shares - 1) / units) - cta + 1;
+      }
+      s = nx;
+      have = more;
+      ++seg;
+    }
+    if (leader && q_loads) {  // a Q copy still in flight lands before the CTA ends
+      volatile int never = 0;
+      tc::mbar_wait(&ctl->q_full, (q_loads - 1) & 1, &never);
+    }
+    __syncwarp();
+  } else if constexpr (G::FP8) {
+    // --------------------------------------- 8-bit tiles widened to bf16 ----
+    const int w = warp - 2 - G::SW;
+    int slot = 0, raw = 0;
+    uint32_t phase = 0, raw_phase = 0;
+    constexpr int PARTS = D / 16;  // 16-byte parts of a raw row
+    for (long long f = 0; f < 2 * (u1 - u0); ++f) {
+      if (!warp_wait(&ctl->rfull[raw], raw_phase, abort) ||
+          !warp_wait(&ctl->empty[slot], phase ^ 1, abort))
+        break;
+      const uint8_t *src = raws + raw * G::RAW;
+      uint8_t *dst = slots + slot * G::SLOT;
+      // eight lanes take eight tokens: the swizzles spread both sides over all banks
+      const int token = w * 32 + lane;
+      // raw rows of 128 bytes are swizzled by token & 7, of 64 bytes by (token >> 1) & 3
+      const int raw_x = D == 128 ? token & 7 : (token >> 1) & 3;
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(src + token * D + ((p ^ raw_x) * 16));
+        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[2 * i] = widen_e4m3x2(v[i] & 0xffffu);
+          o[2 * i + 1] = widen_e4m3x2(v[i] >> 16);
+        }
+        uint8_t *row = dst + (p / 4) * HALF_BYTES + token * 128;
+        const int c = (2 * p) % 8;
+        *reinterpret_cast<uint4 *>(row + ((c ^ (token & 7)) * 16)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(row + (((c + 1) ^ (token & 7)) * 16)) =
+            make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&ctl->full[slot]);
+        tc::mbar_arrive(&ctl->rempty[raw]);
+      }
+      if (++slot == SLOTS) {
+        slot = 0;
+        phase ^= 1;
+      }
+      if (++raw == RAWS) {
+        raw = 0;
+        raw_phase ^= 1;
+      }
+    }
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (ctl->abort && threadIdx.x == 0) dspark_set_status(DSPARK_ERR_TIMEOUT);
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, G::TMEM_COLS);
+  }
+}
+
+// The cut items: block (c, y) joins the pieces of the item that CTA c began and
+// could not finish, a warp taking one row, its own pieces in order.
+template <int D>
+__global__ void __launch_bounds__(128) tree_attention_join(const Args a, int nt) {
+  constexpr int E = D / 32;
+  pdl_trigger();
+  pdl_wait();
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const int *desc = a.desc + c * 8;
+  const int pieces = desc[0], col = blockIdx.y * 4 + (threadIdx.x >> 5);
+  if (pieces == 0 || col >= desc[3] * a.group) return;
+  // piece 0 is CTA c's last one, piece k > 0 CTA (c + k)'s first
+  auto at = [&](int k) -> size_t { return (size_t)(k ? 2 * (c + k) : 2 * c + 1) * nt; };
+  float top = -INFINITY, sum = 0.0f;
+  for (int k = lane; k < pieces; k += 32) top = fmaxf(top, a.part_ml[2 * at(k) + col]);
+  top = warp_max(top);
+  for (int k = lane; k < pieces; k += 32) {
+    const float m = a.part_ml[2 * at(k) + col];
+    sum += m == -INFINITY ? 0.0f : ex2_fast(m - top) * a.part_ml[2 * at(k) + nt + col];
+  }
+  sum = warp_sum(sum);
+  float o[E] = {};
+  for (int k = 0; k < pieces; ++k) {
+    const float m = a.part_ml[2 * at(k) + col], w = m == -INFINITY ? 0.0f : ex2_fast(m - top);
+    const float *src = a.part_o + (at(k) + col) * D + lane * E;
+#pragma unroll
+    for (int i = 0; i < E; ++i) o[i] = fmaf(w, src[i], o[i]);
+  }
+  const int row = desc[1] + desc[2] + col / a.group, h = desc[4];
+  const int head = h * a.group + col % a.group;
+  const float f = (a.v_scale ? a.v_scale[h] : 1.0f) / sum;
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    a.out[row * a.out_row + head * a.out_head + lane * E + i] = __float2bfloat16_rn(o[i] * f);
+  if (a.lse && lane == 0)
+    a.lse[(size_t)row * a.heads * a.group + head] = (top + log2f(sum)) * LN2;
+}
+
+}  // namespace attn
