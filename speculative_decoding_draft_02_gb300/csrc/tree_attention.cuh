@@ -14,7 +14,7 @@
 // Here a thread owns one token (TMEM lane) and the rows run along registers.  Its
 // price is the maximum over tokens, which lies across lanes; it is paid only when
 // it matters: the exponent's reference is kept from tile to tile and raised (with
-// O rescaled) only when some score exceeds it by 2^8.
+// O rescaled) only when some weight would exceed 2^RAISE.
 //
 // A weight meets V as the sum of two bf16 numbers, its rounding and what that
 // left out (columns j and NT + j of P, and two parts of O added at the end):
@@ -30,8 +30,9 @@
 // from call to call).
 //
 // One CTA per SM: warp 0 loads (TMA, one copy per page and 64 columns), warp 1
-// issues the MMAs, 4 * CG warps do the softmax (a group of four per 32 columns),
-// and for an 8-bit cache four more widen the tiles to bf16 between two rings.
+// issues the MMAs, one or two groups of four warps do the softmax (a warp for each
+// 32 tokens, CH chunks of 32 columns one after the other), and for an 8-bit cache
+// eight more widen the tiles to bf16 between two rings.
 // Every wait is bounded; on expiry the CTA raises DSPARK_ERR_TIMEOUT, drains its
 // own copies and MMAs, frees TMEM and exits.
 #pragma once
@@ -44,9 +45,14 @@ namespace attn {
 
 constexpr int BT = 128;                 // tokens of a tile
 constexpr int SMEM_LIMIT = 232448;      // 227 KB
-constexpr int CTL_BYTES = 2048;
+constexpr int CTL_BYTES = 2560;
 constexpr int MAX_SLOTS = 12;
-constexpr float RAISE = 8.0f;           // log2: how far scores may pass the reference
+// What beginning and ending an item costs a CTA, in tiles (measured: about one
+// tile's time at 32 columns); counted so that short contexts balance too.
+constexpr int ITEM_UNITS = 1;
+// log2: how far scores may pass the reference.  Weights, their sum and O are
+// floating-point numbers of f32's range, so nothing is lost below 2^32.
+constexpr float RAISE = 32.0f;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 struct Args {
@@ -69,9 +75,12 @@ template <int TYPE, int D, int NT>
 struct Geo {
   static constexpr bool FP8 = TYPE == DSPARK_KV_E4M3;
   static constexpr int CW = NT < 32 ? NT : 32;  // columns of a softmax thread
-  static constexpr int CG = NT / CW;
+  // groups of softmax warps: one beside the warps that widen, so that a thread
+  // keeps its columns' sums in registers
+  static constexpr int CG = !FP8 && NT >= 64 ? 2 : 1;
+  static constexpr int CH = NT / (CW * CG);     // chunks of columns of a thread
   static constexpr int SW = 4 * CG;
-  static constexpr int CV = FP8 ? 4 : 0;
+  static constexpr int CV = FP8 ? 8 : 0;
   static constexpr int THREADS = 32 * (2 + SW + CV);
   static constexpr int SLOT = BT * D * 2;
   static constexpr int Q_BYTES = NT * D * 2;
@@ -87,20 +96,6 @@ struct Geo {
   static constexpr uint32_t TMEM_COLS = 4 * NT;  // two tiles of S, and O's two parts
   static_assert(SLOTS >= 3 && (!FP8 || RAWS >= 3) && SMEM_BYTES <= SMEM_LIMIT, "shared memory");
 };
-
-struct Ctl {
-  uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], rfull[MAX_SLOTS], rempty[MAX_SLOTS];
-  uint64_t q_full, s_full[2], s_empty[2], p_full, pv_done, drain;
-  alignas(16) float nm[128];  // minus each column's reference exponent (log2); +inf: none yet
-  int top[128];           // its maximum score so far, as an ordered key
-  long long sums[32];
-  unsigned long long odd[3];  // nodes with non-finite V, by segment mod 3
-  long long start_off;
-  int start_r;
-  int abort;
-  uint32_t tmem;
-};
-static_assert(sizeof(Ctl) <= CTL_BYTES, "control block");
 
 // f32 as an int of the same order (-0 below +0; NaN outside the numbers).
 __device__ __forceinline__ int order_key(float x) {
@@ -136,7 +131,7 @@ struct Request {
     return ok || n == 0;
   }
   __device__ __forceinline__ long long units(const Args &a) const {
-    return (long long)tiles * row_tiles * a.heads;
+    return n ? (long long)(tiles + ITEM_UNITS) * row_tiles * a.heads : 0;
   }
 };
 
@@ -148,31 +143,36 @@ struct Segment {
 // Walks a CTA's share of the list of units.  The next request's lengths are read
 // one request ahead.
 struct Walker {
-  const Args &a;
-  int nodes_tile, r, h, rt, tile, next_ctx, next_end, end;
+  int nodes_tile, r, h, rt, tile, over, next_ctx, next_end, end;
   long long pos, last;  // the next unit, and the end of the share
   Request q;
-  __device__ Walker(const Args &args, int nt) : a(args), nodes_tile(nt) {}
-  __device__ __forceinline__ void ahead() {
+  __device__ __forceinline__ void ahead(const Args &a) {
     if (r + 1 < a.R) {
       next_ctx = a.ctx[r + 1];
       next_end = a.row_start[r + 2];
     }
   }
-  __device__ __forceinline__ void begin(int r0, long long off, long long u0, long long u1) {
+  __device__ __forceinline__ void begin(const Args &a, int nt, int r0, long long off, long long u0,
+                                        long long u1) {
+    nodes_tile = nt;
     pos = u0;
     last = u1;
-    if (u0 >= u1) return;
+    over = 0;
+    if (u0 >= u1) return;  // nothing else is read then
     r = r0;
     end = a.row_start[r + 1];
     q.set(a, nodes_tile, a.ctx[r], a.row_start[r], end);
-    const long long item = off / q.tiles;
-    tile = (int)(off - item * q.tiles);
+    const int each = q.tiles + ITEM_UNITS;
+    const long long item = off / each;
+    const int rest = (int)(off - item * each);
+    over = max(ITEM_UNITS - rest, 0);  // of the item's own units before its tiles
+    tile = max(rest - ITEM_UNITS, 0);
     h = (int)(item / q.row_tiles);
     rt = (int)(item - (long long)h * q.row_tiles);
-    ahead();
+    ahead(a);
   }
-  __device__ __forceinline__ bool next(Segment &s) {
+  __device__ __forceinline__ bool next(const Args &a, Segment &s) {
+    pos += over;
     if (pos >= last) return false;
     if (h == a.heads) {
       h = 0;
@@ -184,7 +184,7 @@ struct Walker {
         const int start = end;
         end = next_end;
         q.set(a, nodes_tile, next_ctx, start, end);
-        ahead();
+        ahead(a);
       } while (q.n == 0);
     }
     s.r = r;
@@ -200,8 +200,10 @@ struct Walker {
     s.te = (int)min((long long)q.tiles, tile + (last - pos));
     pos += s.te - s.tb;
     tile = s.te;
+    over = 0;
     if (tile == q.tiles) {
       tile = 0;
+      over = ITEM_UNITS;
       if (++rt == q.row_tiles) {
         rt = 0;
         ++h;
@@ -210,6 +212,23 @@ struct Walker {
     return true;
   }
 };
+
+struct Ctl {
+  uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], rfull[MAX_SLOTS], rempty[MAX_SLOTS];
+  uint64_t q_full, s_full[2], s_empty[2], p_full, pv_done, drain;
+  alignas(16) float nm[128];  // minus each column's reference exponent (log2); +inf: none yet
+  int top[128];           // its maximum score so far, as an ordered key
+  long long sums[32];
+  Walker walk[2];         // of each softmax group, and its segments in turn
+  Segment seg[2][2];
+  int more[2][2];
+  unsigned long long odd[3];  // nodes with non-finite V, by segment mod 3
+  long long start_off;
+  int start_r;
+  int abort;
+  uint32_t tmem;
+};
+static_assert(sizeof(Ctl) <= CTL_BYTES, "control block");
 
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
   int ok = 1;
@@ -258,6 +277,25 @@ __device__ __forceinline__ float column_sums(float (&v)[CW], int lane) {
     for (int j = 0; j < o; ++j) {
       const float send = up ? v[j] : v[j + o], keep = up ? v[j + o] : v[j];
       v[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  return v[0];
+}
+
+// The columns' maxima, left the same way (a NaN counts for nothing).
+template <int CW>
+__device__ __forceinline__ float column_max(float (&v)[CW], int lane) {
+  if constexpr (CW == 16) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = fmaxf(v[j], __shfl_xor_sync(0xffffffffu, v[j], 16));
+  }
+#pragma unroll
+  for (int o = CW / 2; o; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int j = 0; j < o; ++j) {
+      const float send = up ? v[j] : v[j + o], keep = up ? v[j + o] : v[j];
+      v[j] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, o));
     }
   }
   return v[0];
@@ -361,9 +399,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
   }
   __syncthreads();
   const uint32_t tmem = ctl->tmem, tmem_o = tmem + 2 * NT;
-  Walker walk(a, nodes_tile);
-  walk.begin(ctl->start_r, ctl->start_off, u0, u1);
-  Segment s;
+  const int start_r = ctl->start_r;
+  const long long start_off = ctl->start_off;
 
   if (warp == 0) {
     // -------------------------------------------------- copies of K and V ----
@@ -376,10 +413,13 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     constexpr int RING_BYTES = G::FP8 ? G::RAW : G::SLOT;
     const int rows = min(1 << a.page_shift, BT), boxes = BT / rows;
     const uint32_t box_bytes = (uint32_t)(rows * D * (G::FP8 ? 1 : 2));
+    Walker walk;
+    Segment s;
+    walk.begin(a, nodes_tile, start_r, start_off, u0, u1);
     int slot = 0;
     uint32_t phase = 0, used = 0;
     bool ok = true;
-    while (ok && walk.next(s)) {
+    while (ok && walk.next(a, s)) {
       const int *table = a.block_table + (size_t)s.r * a.max_pages;
       // the page of box `lane` of a tile; none past the request's end
       auto page_of = [&](int tile) {
@@ -461,9 +501,20 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         advance(v_slot, v_phase);
         return true;
       };
+      Walker walk;
+      Segment s;
+      walk.begin(a, nodes_tile, start_r, start_off, u0, u1);
       bool ok = true;
-      while (ok && walk.next(s)) {
-        if (!tc::mbar_wait(&ctl->q_full, seg & 1, abort)) break;
+      while (ok && walk.next(a, s)) {
+        // a segment's last product must not wait for the next one's Q
+        if (t > 0 && !pv(t - 1)) {
+          ok = false;
+          break;
+        }
+        if (!tc::mbar_wait(&ctl->q_full, seg & 1, abort)) {
+          ok = false;
+          break;
+        }
         ++seg;
         for (int tile = s.tb; tile < s.te; ++tile) {
           const uint32_t b = t & 1;
@@ -483,7 +534,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           tc::umma_commit(&ctl->empty[k_slot]);
           tc::umma_commit(&ctl->s_full[b]);
           advance(k_slot, k_phase);
-          if (t > 0 && !pv(t - 1)) {
+          if (tile != s.tb && !pv(t - 1)) {
             ok = false;
             break;
           }
@@ -491,7 +542,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           ++t;
         }
       }
-      if (ok && t > 0 && u0 < u1) pv(t - 1);
+      if (ok && t > 0) pv(t - 1);
       tc::umma_commit(&ctl->drain);  // all MMAs issued have finished
       volatile int never = 0;
       tc::mbar_wait(&ctl->drain, 0, &never);
@@ -500,20 +551,19 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
   } else if (warp < 2 + G::SW) {
     // ----------------------------------------------------------- softmax ----
     const int quarter = warp & 3, cg = (warp - 2) >> 2, bar = 1 + cg;
-    const int token = quarter * 32 + lane, c0 = cg * CW;
+    const int token = quarter * 32 + lane, c_group = cg * G::CH * CW;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    const bool leader = warp == 2 && lane == 0;
+    const bool walker = ((warp - 2) & 3) == 0 && lane == 0, leader = warp == 2 && lane == 0;
     // P[token][column]: 64-column halves; 16-byte chunk c of a row lies at
     // c ^ (token & 7)
-    const int p_chunk = (c0 % 64) / 8;
     auto p_at = [&](int col) -> uint4 * {
       return reinterpret_cast<uint4 *>(sp + (col / 64) * HALF_BYTES + token * 128 +
                                        (((col % 64) / 8) ^ (token & 7)) * 16);
     };
-    // the column sums' meeting place: this group's own chunks of P rows 0, 8, ..
-    auto sum_slot = [&](int q, int j) -> float * {
+    // the column sums' meeting place: the columns' own chunks of P rows 0, 8, ..
+    auto sum_slot = [&](int c0, int q, int j) -> float * {
       return reinterpret_cast<float *>(sp + (c0 / 64) * HALF_BYTES + 8 * (q * 2 + j / 16) * 128 +
-                                       p_chunk * 16) + j % 16;
+                                       (c0 % 64) * 2) + j % 16;
     };
     auto load_q = [&](const Segment &n) {
       const int box_bytes = nodes_tile * a.group * 128;
@@ -522,159 +572,183 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         tc::tma_load_3d(sq + c * NT * 128, &tma_q, c * 64, n.h * a.group, n.row0 + n.node0,
                         &ctl->q_full, tc::policy_evict_normal());
     };
-    if (leader) a.desc[cta * 8] = 0;
-    bool have = walk.next(s);
-    if (have && leader) load_q(s);
-    uint32_t t = 0, seg = 0, v_slot = 1, v_phase = 0, q_loads = have;
-    bool ok = true, gone = false;
-    while (have) {
-      Segment nx = s;
-      bool more = false;
-      const float ks = a.k_scale ? a.k_scale[s.h] : 1.0f, vs = a.v_scale ? a.v_scale[s.h] : 1.0f;
-      const float c = a.scale * ks * LOG2E;
-      const int count = min(max(s.nodes * a.group - c0, 0), CW);  // this group's columns in use
-      // lane j: the ancestor mask of column c0 + j
-      unsigned long long word = 0;
-      if (lane < count) {
-        const int node = s.node0 + (c0 + lane) / a.group;
-        word = a.anc ? a.anc[s.row0 + node] : (2ull << node) - 1;
-        if (s.n < 64) word &= (1ull << s.n) - 1;
+    uint32_t t = 0, seg = 0, v_slot = 1, v_phase = 0, q_loads = 0;
+    // the group's next segment into its place of the two, and that one's Q
+    auto fetch = [&](uint32_t i) {
+      const bool more = ctl->walk[cg].next(a, ctl->seg[cg][i & 1]);
+      ctl->more[cg][i & 1] = more;
+      if (more && leader) {
+        load_q(ctl->seg[cg][i & 1]);
+        ++q_loads;
       }
-      if (quarter == 0 && lane < CW) {
-        // a column that no row uses never calls for a higher reference
-        ctl->nm[c0 + lane] = lane < count ? INFINITY : -INFINITY;
-        ctl->top[c0 + lane] = order_key(-INFINITY);
+    };
+    if (leader) a.desc[cta * 8] = 0;
+    if (walker) {
+      ctl->walk[cg].begin(a, nodes_tile, start_r, start_off, u0, u1);
+      fetch(0);
+    }
+    group_sync(bar);
+    bool ok = true, gone = false;
+    while (ctl->more[cg][seg & 1]) {
+      const Segment s = ctl->seg[cg][seg & 1];
+      const float ks = a.k_scale ? a.k_scale[s.h] : 1.0f;
+      const float c = a.scale * ks * LOG2E;
+      const int rows = s.nodes * a.group;  // columns in use
+      // lane j: the ancestor mask of each chunk's column j
+      unsigned long long word[G::CH];
+#pragma unroll
+      for (int ch = 0; ch < G::CH; ++ch) {
+        const int col = c_group + ch * CW + lane;
+        word[ch] = 0;
+        if (lane < CW && col < rows) {
+          const int node = s.node0 + col / a.group;
+          word[ch] = a.anc ? a.anc[s.row0 + node] : (2ull << node) - 1;
+          if (s.n < 64) word[ch] &= (1ull << s.n) - 1;
+        }
+        if (quarter == 0 && lane < CW) {
+          // a column that no row uses never calls for a higher reference
+          ctl->nm[col] = col < rows ? INFINITY : -INFINITY;
+          ctl->top[col] = order_key(-INFINITY);
+        }
       }
       if (leader) ctl->odd[(seg + 1) % 3] = 0;
       group_sync(bar);
-      float l[CW];
+      float l[G::CH][CW];
 #pragma unroll
-      for (int j = 0; j < CW; ++j) l[j] = 0.0f;
-      bool force = true;  // some column has no reference yet
+      for (int ch = 0; ch < G::CH; ++ch)
+#pragma unroll
+        for (int j = 0; j < CW; ++j) l[ch][j] = 0.0f;
+      uint32_t force = ~0u;  // bit ch: some column of the chunk has no reference yet
 
       for (int tile = s.tb; tile < s.te; ++tile, ++t) {
         const uint32_t b = t & 1;
         ok = ok && warp_wait(&ctl->s_full[b], (t >> 1) & 1, abort);
-        if (tile == s.te - 1) {  // the segment's last use of Q is behind
-          more = walk.next(nx);
-          if (ok && more) {
-            if (leader) load_q(nx);
-            ++q_loads;
-          }
-        }
+        if (tile == s.te - 1 && walker && ok) fetch(seg + 1);  // Q's last use is behind
         const int pos = tile * BT + token;
         const bool edge = tile * BT + BT > s.ctx;  // some token is a node or past the end
-        uint32_t sr[CW];
-        float e[CW];
+        bool waited = t == 0;
         tc::fence_after_sync();
-        auto scores = [&](bool shifted) {  // e = c * S (- reference), masked
-          tc::tmem_ld(tmem + lanes + b * NT + c0, sr);
-          tc::tmem_wait_ld();
-          tc::reg_fence(sr);
 #pragma unroll
-          for (int j = 0; j < CW; j += 4) {
-            float4 nm = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (shifted) nm = *reinterpret_cast<const float4 *>(&ctl->nm[c0 + j]);
-            e[j] = fmaf(__uint_as_float(sr[j]), c, nm.x);
-            e[j + 1] = fmaf(__uint_as_float(sr[j + 1]), c, nm.y);
-            e[j + 2] = fmaf(__uint_as_float(sr[j + 2]), c, nm.z);
-            e[j + 3] = fmaf(__uint_as_float(sr[j + 3]), c, nm.w);
-          }
+        for (int ch = 0; ch < G::CH; ++ch) {
+          const int c0 = c_group + ch * CW;
+          const int count = min(max(rows - c0, 0), CW);
+          if (ch > 0 && count == 0) break;
+          // which of the chunk's columns see this thread's token
+          uint32_t seen = 0xffffffffu;
           if (edge) {
-            const int node = pos - s.ctx;
-            const bool ctx_token = node < 0, end = pos >= s.total;
-#pragma unroll
-            for (int j = 0; j < CW; ++j) {
-              const unsigned long long w = __shfl_sync(0xffffffffu, word, j);
-              const bool seen = ctx_token || (!end && (w >> (node & 63) & 1));
-              e[j] = seen ? e[j] : -INFINITY;
+            const int node0 = tile * BT + quarter * 32 - s.ctx;  // lane 0's node
+            if (node0 + lane >= 0) seen = 0;
+            const int stop = min(s.total - s.ctx, node0 + 32);
+            for (int j = max(node0, 0); j < stop; ++j) {
+              const uint32_t by = __ballot_sync(0xffffffffu, word[ch] >> j & 1);
+              if (lane == j - node0) seen = by;
             }
           }
-        };
-        float most = -INFINITY;
-        if (ok) {
-          scores(true);
+          float e[CW];
+          auto scores = [&](bool shifted) {  // e = c * S (- reference), masked
+            uint32_t sr[CW];
+            tc::tmem_ld(tmem + lanes + b * NT + c0, sr);
+            tc::tmem_wait_ld();
+            tc::reg_fence(sr);
+#pragma unroll
+            for (int j = 0; j < CW; j += 4) {
+              float4 nm = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (shifted) nm = *reinterpret_cast<const float4 *>(&ctl->nm[c0 + j]);
+              e[j] = fmaf(__uint_as_float(sr[j]), c, nm.x);
+              e[j + 1] = fmaf(__uint_as_float(sr[j + 1]), c, nm.y);
+              e[j + 2] = fmaf(__uint_as_float(sr[j + 2]), c, nm.z);
+              e[j + 3] = fmaf(__uint_as_float(sr[j + 3]), c, nm.w);
+            }
+            if (edge) {
+#pragma unroll
+              for (int j = 0; j < CW; ++j) e[j] = seen >> j & 1 ? e[j] : -INFINITY;
+            }
+          };
+          float most = -INFINITY;
+          if (ok) {
+            scores(true);
+#pragma unroll
+            for (int j = 0; j < CW; j += 8)
+              if (j < count) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) most = fmaxf(most, e[j + i]);
+              }
+          }
+          if (group_any(bar, (force >> ch & 1) || most > RAISE || !ok)) {
+            if (group_any(bar, !ok)) {
+              gone = true;
+              break;
+            }
+            // raise the references to the columns' maxima
+            scores(false);
+            const float peak = column_max<CW>(e, lane);
+            if (lane < CW) atomicMax(&ctl->top[c0 + lane], order_key(peak));
+            group_sync(bar);
+            if (!waited) ok = warp_wait(&ctl->pv_done, (t - 1) & 1, abort);
+            waited = true;
+            tc::fence_after_sync();
+            scores(false);  // the maxima took their place
+            const bool scale_o = tile != s.tb && ok;
+            bool none = false;
+#pragma unroll
+            for (int j = 0; j < CW; j += 16) {
+              float keep[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float top = order_value(ctl->top[c0 + j + i]);
+                none = none || (top == -INFINITY && j + i < count);
+                e[j + i] -= top == -INFINITY ? 0.0f : top;
+                if (tile != s.tb) {
+                  const float old = -ctl->nm[c0 + j + i];
+                  // no reference before: nothing to keep
+                  keep[i] = old == -INFINITY ? 0.0f : ex2_fast(old - top);
+                  l[ch][j + i] *= keep[i];
+                }
+              }
+              if (scale_o) {
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                  uint32_t o[16];
+                  tc::tmem_ld16(tmem_o + lanes + part * NT + c0 + j, o);
+                  tc::tmem_wait_ld();
+                  tc::reg_fence(o);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i)
+                    o[i] = __float_as_uint(__uint_as_float(o[i]) * keep[i]);
+                  tc::tmem_st16(tmem_o + lanes + part * NT + c0 + j, o);
+                }
+              }
+            }
+            if (scale_o) tc::tmem_wait_st();
+            force = none ? force | 1u << ch : force & ~(1u << ch);
+            group_sync(bar);
+            if (quarter == 0 && lane < count) ctl->nm[c0 + lane] = -order_value(ctl->top[c0 + lane]);
+            group_sync(bar);
+          }
+          if (ch == G::CH - 1 || rows <= c0 + CW) {  // the tile's scores are read
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&ctl->s_empty[b]);
+          }
+          if (!waited) ok = warp_wait(&ctl->pv_done, (t - 1) & 1, abort);  // P is free
+          waited = true;
 #pragma unroll
           for (int j = 0; j < CW; j += 8)
             if (j < count) {
+              uint32_t hi[4], lo[4];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) most = fmaxf(most, e[j + i]);
-            }
-        }
-        bool waited = t == 0;
-        if (group_any(bar, force || most > RAISE || !ok)) {
-          if (group_any(bar, !ok)) {
-            gone = true;
-            break;
-          }
-          // raise the references to the columns' maxima
-          scores(false);
-          int key = order_key(-INFINITY);
-#pragma unroll
-          for (int j = 0; j < CW; ++j) {
-            const int m = __reduce_max_sync(0xffffffffu, order_key(e[j]));
-            if (lane == j) key = m;
-          }
-          if (lane < CW) atomicMax(&ctl->top[c0 + lane], key);
-          group_sync(bar);
-          if (!waited) ok = warp_wait(&ctl->pv_done, (t - 1) & 1, abort);
-          waited = true;
-          tc::fence_after_sync();
-          force = false;
-          const bool scale_o = tile != s.tb && ok;
-#pragma unroll
-          for (int j = 0; j < CW; j += 16) {
-            float keep[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float top = order_value(ctl->top[c0 + j + i]), old = -ctl->nm[c0 + j + i];
-              force = force || (top == -INFINITY && j + i < count);
-              // no reference before: nothing to keep
-              keep[i] = old == -INFINITY ? 0.0f : ex2_fast(old - top);
-              l[j + i] *= keep[i];
-              e[j + i] -= top == -INFINITY ? 0.0f : top;
-            }
-            if (scale_o) {
-#pragma unroll
-              for (int part = 0; part < 2; ++part) {
-                uint32_t o[16];
-                tc::tmem_ld16(tmem_o + lanes + part * NT + c0 + j, o);
-                tc::tmem_wait_ld();
-                tc::reg_fence(o);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  o[i] = __float_as_uint(__uint_as_float(o[i]) * keep[i]);
-                tc::tmem_st16(tmem_o + lanes + part * NT + c0 + j, o);
+              for (int i = 0; i < 4; ++i) {
+                const float x = ex2_fast(e[j + 2 * i]), y = ex2_fast(e[j + 2 * i + 1]);
+                l[ch][j + 2 * i] += x;
+                l[ch][j + 2 * i + 1] += y;
+                hi[i] = pack_bf16(x, y);
+                lo[i] = pack_bf16(x - bf16_lo(hi[i]), y - bf16_hi(hi[i]));
               }
+              *p_at(c0 + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *p_at(NT + c0 + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
-          }
-          if (scale_o) tc::tmem_wait_st();
-          group_sync(bar);
-          if (quarter == 0 && lane < count) ctl->nm[c0 + lane] = -order_value(ctl->top[c0 + lane]);
-          group_sync(bar);
         }
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&ctl->s_empty[b]);
-        if (!waited) ok = warp_wait(&ctl->pv_done, (t - 1) & 1, abort);  // P is free
-#pragma unroll
-        for (int j = 0; j < CW; j += 8)
-          if (j < count) {
-            float w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              w[i] = ex2_fast(e[j + i]);
-              l[j + i] += w[i];
-            }
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              hi[i] = pack_bf16(w[2 * i], w[2 * i + 1]);
-              lo[i] = pack_bf16(w[2 * i] - bf16_lo(hi[i]), w[2 * i + 1] - bf16_hi(hi[i]));
-            }
-            *p_at(c0 + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *p_at(NT + c0 + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
+        if (gone) break;
         if (edge) {
           // What a row does not see must not meet its zero weight as infinity or
           // NaN: V past the end is cleared, and so are the nodes' non-finite
@@ -716,40 +790,50 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
 
       // ------------------------------------------------- end of a segment ----
       ok = ok && warp_wait(&ctl->pv_done, (t - 1) & 1, abort);
-      const float part = column_sums<CW>(l, lane);
-      if (ok && lane < CW) *sum_slot(quarter, lane) = part;
+#pragma unroll
+      for (int ch = 0; ch < G::CH; ++ch) {
+        const float part = column_sums<CW>(l[ch], lane);
+        if (ok && lane < CW) *sum_slot(c_group + ch * CW, quarter, lane) = part;
+      }
       if (group_any(bar, !ok)) {
         gone = true;
         break;
       }
       tc::fence_after_sync();
-      float sum = 0.0f, top = 0.0f;
-      if (lane < CW) {
-        sum = (*sum_slot(0, lane) + *sum_slot(1, lane)) + (*sum_slot(2, lane) + *sum_slot(3, lane));
-        top = order_value(ctl->top[c0 + lane]);
-      }
+      const float vs = a.v_scale ? a.v_scale[s.h] : 1.0f;
       const unsigned long long odd = ctl->odd[seg % 3];
       const bool whole = s.tb == 0 && s.te == s.tiles;
       const int piece = s.tb == 0 ? 1 : 0;
       const int d = token;  // accumulator lane = column of the head
-      const bool sees = s.ctx > 0 || word != 0;
-      const float inv = sees ? vs / sum : 0.0f;
-      const int col = c0 + lane, node = s.node0 + col / a.group;
-      const int head = s.h * a.group + col % a.group;
-      if (quarter == 0 && lane < count) {
-        if (!whole) {
-          float *ml = a.part_ml + (size_t)(cta * 2 + piece) * 2 * NT + col;
-          ml[0] = top;
-          ml[NT] = sum;
-        } else if (a.lse) {
-          a.lse[(size_t)(s.row0 + node) * a.heads * a.group + head] =
-              sees ? (top + log2f(sum)) * LN2 : -INFINITY;
+#pragma unroll
+      for (int ch = 0; ch < G::CH; ++ch) {
+        const int c0 = c_group + ch * CW, count = min(rows - c0, CW);
+        if (count <= 0) break;
+        float sum = 0.0f;
+        if (lane < CW)
+          sum = (*sum_slot(c0, 0, lane) + *sum_slot(c0, 1, lane)) +
+                (*sum_slot(c0, 2, lane) + *sum_slot(c0, 3, lane));
+        const bool sees = s.ctx > 0 || word[ch] != 0;
+        const float inv = sees ? vs / sum : 0.0f;
+        if (quarter == 0 && lane < count) {
+          const float top = order_value(ctl->top[c0 + lane]);
+          const int node = (c0 + lane) / a.group, head = s.h * a.group + (c0 + lane) % a.group;
+          if (!whole) {
+            float *ml = a.part_ml + (size_t)(cta * 2 + piece) * 2 * NT + c0 + lane;
+            ml[0] = top;
+            ml[NT] = sum;
+          } else if (a.lse) {
+            a.lse[(size_t)(s.row0 + s.node0 + node) * a.heads * a.group + head] =
+                sees ? (top + log2f(sum)) * LN2 : -INFINITY;
+          }
         }
-      }
-      if (quarter * 32 < D) {
+        if (quarter * 32 >= D) continue;
+        int g = c0 % a.group;  // head of the group, and place, of column j
+        bf16 *dst = a.out + (s.row0 + s.node0 + c0 / a.group) * a.out_row +
+                    (s.h * a.group + g) * a.out_head + d;
+        float *po = a.part_o + ((size_t)(cta * 2 + piece) * NT + c0) * D + d;
 #pragma unroll 1
-        for (int j = 0; j < CW; j += 16) {
-          if (j >= count) break;
+        for (int j = 0; j < count; j += 16) {
           uint32_t o[16], o_lo[16];
           tc::tmem_ld16(tmem_o + lanes + c0 + j, o);
           tc::tmem_ld16(tmem_o + lanes + NT + c0 + j, o_lo);
@@ -773,24 +857,25 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
                 x = __bfloat162float(reinterpret_cast<const bf16 *>(v)[d]);
             }
             const bool finite = fabsf(x) < INFINITY;
+            const uint32_t by = __ballot_sync(0xffffffffu, word[ch] >> at & 1) >> j;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const unsigned long long w = __shfl_sync(0xffffffffu, word, j + i);
-              if (!finite && (w >> at & 1)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
-            }
+            for (int i = 0; i < 16; ++i)
+              if (!finite && (by >> i & 1)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
           }
-          float *po = a.part_o + ((size_t)(cta * 2 + piece) * NT + c0 + j) * D + d;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float f = __shfl_sync(0xffffffffu, inv, j + i);
-            const int row = __shfl_sync(0xffffffffu, s.row0 + node, j + i);
-            const int hd = __shfl_sync(0xffffffffu, head, j + i);
             if (j + i < count) {
               if (whole)
-                a.out[row * a.out_row + hd * a.out_head + d] =
-                    __float2bfloat16_rn(__uint_as_float(o[i]) * f);
+                *dst = __float2bfloat16_rn(__uint_as_float(o[i]) * f);
               else
-                po[i * D] = __uint_as_float(o[i]);
+                po[(j + i) * D] = __uint_as_float(o[i]);
+            }
+            ++g;
+            dst += a.out_head;
+            if (g == a.group) {
+              g = 0;
+              dst += a.out_row - a.group * a.out_head;
             }
           }
         }
@@ -805,8 +890,6 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         desc[4] = s.h;
         desc[0] = (int)((end * shares - 1) / units) - cta + 1;
       }
-      s = nx;
-      have = more;
       ++seg;
     }
     if (leader && q_loads) {  // a Q copy still in flight lands before the CTA ends
@@ -820,18 +903,24 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     int slot = 0, raw = 0;
     uint32_t phase = 0, raw_phase = 0;
     constexpr int PARTS = D / 16;  // 16-byte parts of a raw row
-    for (long long f = 0; f < 2 * (u1 - u0); ++f) {
+    Walker walk;
+    Segment s;
+    walk.begin(a, nodes_tile, start_r, start_off, u0, u1);
+    long long left = 0;  // tiles of K and V in this CTA's share
+    while (walk.next(a, s)) left += 2 * (s.te - s.tb);
+    for (; left > 0; --left) {
       if (!warp_wait(&ctl->rfull[raw], raw_phase, abort) ||
           !warp_wait(&ctl->empty[slot], phase ^ 1, abort))
         break;
       const uint8_t *src = raws + raw * G::RAW;
       uint8_t *dst = slots + slot * G::SLOT;
       // eight lanes take eight tokens: the swizzles spread both sides over all banks
-      const int token = w * 32 + lane;
+      const int token = (w & 3) * 32 + lane;
       // raw rows of 128 bytes are swizzled by token & 7, of 64 bytes by (token >> 1) & 3
       const int raw_x = D == 128 ? token & 7 : (token >> 1) & 3;
 #pragma unroll
-      for (int p = 0; p < PARTS; ++p) {
+      for (int i0 = 0; i0 < PARTS / 2; ++i0) {
+        const int p = 2 * i0 + (w >> 2);
         const uint4 x = *reinterpret_cast<const uint4 *>(src + token * D + ((p ^ raw_x) * 16));
         const uint32_t v[4] = {x.x, x.y, x.z, x.w};
         uint32_t o[8];
