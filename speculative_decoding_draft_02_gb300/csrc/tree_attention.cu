@@ -46,7 +46,8 @@ template <int TYPE, int D, int NT>
 int launch(const Launch &l) {
   using G = attn::Geo<TYPE, D, NT>;
   const dspark_kv_cache *c = l.cache;
-  const Args &a = l.a;
+  Args a = l.a;
+  a.nodes_tile = NT / a.group;
   const uint64_t size = G::FP8 ? 1 : 2;
   const uint64_t dims[4] = {(uint64_t)D, (uint64_t)c->page_size, (uint64_t)c->heads,
                             (uint64_t)c->n_pages};
@@ -60,7 +61,7 @@ int launch(const Launch &l) {
       G::FP8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   const uint64_t q_dims[3] = {(uint64_t)D, (uint64_t)(a.heads * a.group), (uint64_t)a.n_rows};
   const uint64_t q_strides[2] = {(uint64_t)l.q_head * 2, (uint64_t)l.q_row * 2};
-  const uint32_t q_box[3] = {64, (uint32_t)a.group, (uint32_t)(NT / a.group)};
+  const uint32_t q_box[3] = {64, (uint32_t)a.group, (uint32_t)a.nodes_tile};
   CUtensorMap tk, tv, tq;
   if (dspark_make_tmap(&tk, type, 4, c->k, dims, strides, box, swizzle) != 0 ||
       dspark_make_tmap(&tv, type, 4, c->v, dims, strides, box, swizzle) != 0 ||

@@ -47,6 +47,7 @@ constexpr int BT = 128;                 // tokens of a tile
 constexpr int SMEM_LIMIT = 232448;      // 227 KB
 constexpr int CTL_BYTES = 2560;
 constexpr int MAX_SLOTS = 12;
+constexpr int SEGS = 8;
 // What beginning and ending an item costs a CTA, in tiles (measured: about one
 // tile's time at 32 columns); counted so that short contexts balance too.
 constexpr int ITEM_UNITS = 1;
@@ -56,7 +57,7 @@ constexpr float RAISE = 32.0f;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 struct Args {
-  int R, heads, group, max_nodes, n_rows, max_pages, page_shift, n_pages;
+  int R, heads, group, nodes_tile, max_nodes, n_rows, max_pages, page_shift, n_pages;
   const int *ctx, *row_start, *block_table;
   const uint64_t *anc;
   const float *k_scale, *v_scale;
@@ -75,12 +76,12 @@ template <int TYPE, int D, int NT>
 struct Geo {
   static constexpr bool FP8 = TYPE == DSPARK_KV_E4M3;
   static constexpr int CW = NT < 32 ? NT : 32;  // columns of a softmax thread
-  // groups of softmax warps: one beside the warps that widen, so that a thread
-  // keeps its columns' sums in registers
-  static constexpr int CG = !FP8 && NT >= 64 ? 2 : 1;
+  static constexpr int CG = NT >= 64 ? 2 : 1;   // groups of softmax warps
   static constexpr int CH = NT / (CW * CG);     // chunks of columns of a thread
   static constexpr int SW = 4 * CG;
-  static constexpr int CV = FP8 ? 8 : 0;
+  // at most 14 warps with those that widen: a softmax thread keeps its columns'
+  // sums in registers
+  static constexpr int CV = !FP8 ? 0 : CG == 2 ? 4 : 8;
   static constexpr int THREADS = 32 * (2 + SW + CV);
   static constexpr int SLOT = BT * D * 2;
   static constexpr int Q_BYTES = NT * D * 2;
@@ -109,7 +110,7 @@ __device__ __forceinline__ float order_value(int k) {
 // A request as the kernel takes it: every later index is in bounds by this.
 struct Request {
   int row0, n, ctx, total, tiles, row_tiles;
-  __device__ __forceinline__ bool set(const Args &a, int nodes_tile, int c, int start, int end) {
+  __device__ __noinline__ bool set(const Args &a, int c, int start, int end) {
     bool ok = true;
     row0 = min(max(start, 0), a.n_rows);
     n = min(max(end, row0), a.n_rows) - row0;
@@ -127,7 +128,7 @@ struct Request {
       total = ctx + n;
     }
     tiles = n ? (total + BT - 1) / BT : 0;
-    row_tiles = (n + nodes_tile - 1) / nodes_tile;
+    row_tiles = (n + a.nodes_tile - 1) / a.nodes_tile;
     return ok || n == 0;
   }
   __device__ __forceinline__ long long units(const Args &a) const {
@@ -135,105 +136,105 @@ struct Request {
   }
 };
 
-// One CTA's consecutive tiles of one item.
+// One CTA's consecutive tiles of one item; none (tb == te): the end of its share.
 struct Segment {
-  int r, row0, n, ctx, total, tiles, h, node0, nodes, tb, te;
+  int r, row0, n, ctx, total, tiles, h, node0, nodes, tb, te, unused;
 };
 
-// Walks a CTA's share of the list of units.  The next request's lengths are read
-// one request ahead.
+// Where the copying warp stands in its CTA's share of the list of units.
 struct Walker {
-  int nodes_tile, r, h, rt, tile, over, next_ctx, next_end, end;
+  int r, h, rt, tile, over, next_ctx, next_end, end;  // over: own units of the item left
   long long pos, last;  // the next unit, and the end of the share
   Request q;
-  __device__ __forceinline__ void ahead(const Args &a) {
+  __device__ __forceinline__ void ahead(const Args &a) {  // the next request's lengths
     if (r + 1 < a.R) {
       next_ctx = a.ctx[r + 1];
       next_end = a.row_start[r + 2];
     }
   }
-  __device__ __forceinline__ void begin(const Args &a, int nt, int r0, long long off, long long u0,
-                                        long long u1) {
-    nodes_tile = nt;
-    pos = u0;
-    last = u1;
-    over = 0;
-    if (u0 >= u1) return;  // nothing else is read then
-    r = r0;
-    end = a.row_start[r + 1];
-    q.set(a, nodes_tile, a.ctx[r], a.row_start[r], end);
-    const int each = q.tiles + ITEM_UNITS;
-    const long long item = off / each;
-    const int rest = (int)(off - item * each);
-    over = max(ITEM_UNITS - rest, 0);  // of the item's own units before its tiles
-    tile = max(rest - ITEM_UNITS, 0);
-    h = (int)(item / q.row_tiles);
-    rt = (int)(item - (long long)h * q.row_tiles);
-    ahead(a);
-  }
-  __device__ __forceinline__ bool next(const Args &a, Segment &s) {
-    pos += over;
-    if (pos >= last) return false;
-    if (h == a.heads) {
-      h = 0;
-      do {
-        if (++r >= a.R) {
-          pos = last;
-          return false;
-        }
-        const int start = end;
-        end = next_end;
-        q.set(a, nodes_tile, next_ctx, start, end);
-        ahead(a);
-      } while (q.n == 0);
-    }
-    s.r = r;
-    s.row0 = q.row0;
-    s.n = q.n;
-    s.ctx = q.ctx;
-    s.total = q.total;
-    s.tiles = q.tiles;
-    s.h = h;
-    s.node0 = rt * nodes_tile;
-    s.nodes = min(nodes_tile, q.n - s.node0);
-    s.tb = tile;
-    s.te = (int)min((long long)q.tiles, tile + (last - pos));
-    pos += s.te - s.tb;
-    tile = s.te;
-    over = 0;
-    if (tile == q.tiles) {
-      tile = 0;
-      over = ITEM_UNITS;
-      if (++rt == q.row_tiles) {
-        rt = 0;
-        ++h;
-      }
-    }
-    return true;
-  }
 };
+
+__device__ __forceinline__ bool next_segment(Walker *w, Segment *s, const Args *a) {
+  w->pos += w->over;
+  w->over = 0;
+  if (w->pos >= w->last) return false;
+  if (w->h == a->heads) {
+    w->h = 0;
+    do {
+      if (++w->r >= a->R) {
+        w->pos = w->last;
+        return false;
+      }
+      const int start = w->end;
+      w->end = w->next_end;
+      w->q.set(*a, w->next_ctx, start, w->end);
+      w->ahead(*a);
+    } while (w->q.n == 0);
+  }
+  const Request q = w->q;
+  s->r = w->r;
+  s->row0 = q.row0;
+  s->n = q.n;
+  s->ctx = q.ctx;
+  s->total = q.total;
+  s->tiles = q.tiles;
+  s->h = w->h;
+  s->node0 = w->rt * a->nodes_tile;
+  s->nodes = min(a->nodes_tile, q.n - s->node0);
+  const int tb = w->tile, te = (int)min((long long)q.tiles, tb + (w->last - w->pos));
+  s->tb = tb;
+  s->te = te;
+  w->pos += te - tb;
+  w->tile = te;
+  if (te == q.tiles) {
+    w->tile = 0;
+    w->over = ITEM_UNITS;
+    if (++w->rt == q.row_tiles) {
+      w->rt = 0;
+      ++w->h;
+    }
+  }
+  return true;
+}
+
+// A quotient of two non-negative 64-bit numbers: a call, for its size.
+__device__ __noinline__ long long divide(long long x, long long y) {
+  return (long long)((unsigned long long)x / (unsigned long long)y);
+}
 
 struct Ctl {
   uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], rfull[MAX_SLOTS], rempty[MAX_SLOTS];
   uint64_t q_full, s_full[2], s_empty[2], p_full, pv_done, drain;
-  alignas(16) float nm[128];  // minus each column's reference exponent (log2); +inf: none yet
-  int top[128];           // its maximum score so far, as an ordered key
+  alignas(16) float nm[128];  // minus each column's reference exponent (log2)
+  int top[128];           // how far a tile's scores pass it, as an ordered key
   long long sums[32];
-  Walker walk[2];         // of each softmax group, and its segments in turn
-  Segment seg[2][2];
-  int more[2][2];
+  Walker walk;
+  // The share's segments as the copying warp comes to them, for the other roles.
+  alignas(16) Segment seg[SEGS];
+  uint64_t seg_full[SEGS], seg_empty[SEGS];
+  int raw_end;            // 8-bit: fills of the raw ring
   unsigned long long odd[3];  // nodes with non-finite V, by segment mod 3
-  long long start_off;
-  int start_r;
   int abort;
   uint32_t tmem;
 };
 static_assert(sizeof(Ctl) <= CTL_BYTES, "control block");
 
+// The library's bounded wait in few instructions, as many places have one; the
+// clock, which is slow to read, is looked at once in 64 tries.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  uint64_t t0 = 0;
+  for (uint32_t tries = 1; !tc::mbar_try_wait_sleep(bar, parity); ++tries) {
+    if (tries & 63) continue;
+    const uint64_t now = tc::globaltimer();
+    if (t0 == 0) t0 = now;
+    if (*abort) return false;
+    if (now - t0 > tc::WAIT_LIMIT_NS) *abort = 1;
+  }
+  return true;
+}
+// By every lane of a warp; one answer for all.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = tc::mbar_wait(bar, parity, abort) ? 1 : 0;
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+  return __all_sync(0xffffffffu, wait(bar, parity, abort));
 }
 
 __device__ __forceinline__ void group_sync(int id) {
@@ -305,7 +306,8 @@ template <int TYPE, int D, int NT>
 __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     tree_attention_kernel(const __grid_constant__ CUtensorMap tma_k,
                           const __grid_constant__ CUtensorMap tma_v,
-                          const __grid_constant__ CUtensorMap tma_q, const Args a) {
+                          const __grid_constant__ CUtensorMap tma_q,
+                          const __grid_constant__ Args a) {
   using G = Geo<TYPE, D, NT>;
   constexpr int CW = G::CW, CG = G::CG, SLOTS = G::SLOTS, RAWS = G::RAWS;
   constexpr int HALVES = D / 64;            // 64-column halves of a head
@@ -319,13 +321,14 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
   volatile int *abort = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
-  const int nodes_tile = NT / a.group;
 
   if (threadIdx.x == 0) {
+#pragma unroll 1
     for (int s = 0; s < SLOTS; ++s) {
       tc::mbar_init(&ctl->full[s], G::FP8 ? G::CV : 1);
       tc::mbar_init(&ctl->empty[s], 1);
     }
+#pragma unroll 1
     for (int s = 0; s < RAWS; ++s) {
       tc::mbar_init(&ctl->rfull[s], 1);
       tc::mbar_init(&ctl->rempty[s], G::CV);
@@ -340,6 +343,12 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     tc::mbar_init(&ctl->drain, 1);
     for (int i = 0; i < 3; ++i) ctl->odd[i] = 0;
     ctl->abort = 0;
+    ctl->raw_end = -1;
+#pragma unroll 1
+    for (int i = 0; i < SEGS; ++i) {
+      tc::mbar_init(&ctl->seg_full[i], 1);
+      tc::mbar_init(&ctl->seg_empty[i], 1 + CG);  // the MMA issuer, each softmax group
+    }
     tc::fence_barrier_init();
     tc::tma_prefetch_desc(&tma_k);
     tc::tma_prefetch_desc(&tma_v);
@@ -353,9 +362,10 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
   const int per = (a.R + G::THREADS - 1) / G::THREADS;
   const int r_lo = min((int)threadIdx.x * per, a.R), r_hi = min(r_lo + per, a.R);
   long long mine = 0;
+#pragma unroll 1
   for (int r = r_lo; r < r_hi; ++r) {
     Request q;
-    if (!q.set(a, nodes_tile, a.ctx[r], a.row_start[r], a.row_start[r + 1]) && cta == 0)
+    if (!q.set(a, a.ctx[r], a.row_start[r], a.row_start[r + 1]) && cta == 0)
       dspark_set_status(DSPARK_ERR_LENGTH);
     mine += q.units(a);
   }
@@ -369,57 +379,84 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  long long all = lane < G::THREADS / 32 ? ctl->sums[lane] : 0;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, all, o);
-    if (lane >= o) all += t;
+  long long units = 0, first = upto - mine;  // of all requests, and before this thread's
+#pragma unroll 1
+  for (int w = 0; w < G::THREADS / 32; ++w) {
+    const long long t = ctl->sums[w];
+    units += t;
+    if (w < warp) first += t;
   }
-  const long long before_warp = warp ? __shfl_sync(0xffffffffu, all, warp - 1) : 0;
-  const long long units = __shfl_sync(0xffffffffu, all, 31);
-  // with fewer units than CTAs the first ones take one each: an item's pieces lie
-  // in consecutive CTAs
-  const long long shares = min((long long)gridDim.x, units);
-  const long long u0 = cta < shares ? units * cta / shares : units;
-  const long long u1 = cta < shares ? units * (cta + 1) / shares : units;
-  const long long first = before_warp + upto - mine;
-  if (mine > 0 && first <= u0 && u0 < first + mine) {
-    long long at = first;
-    for (int r = r_lo; r < r_hi; ++r) {
-      Request q;
-      q.set(a, nodes_tile, a.ctx[r], a.row_start[r], a.row_start[r + 1]);
-      const long long m = q.units(a);
-      if (u0 < at + m) {
-        ctl->start_r = r;
-        ctl->start_off = u0 - at;
-        break;
-      }
-      at += m;
+  // equal shares, the first ones a unit longer; with fewer units than CTAs the
+  // first take one each, so that an item's pieces lie in consecutive CTAs
+  const int shares = (int)min((long long)gridDim.x, max(units, 1ll));
+  const long long share = divide(units, shares), longer = units - share * shares;
+  const long long u0 = cta < shares ? cta * share + min((long long)cta, longer) : units;
+  const long long u1 = cta < shares ? u0 + share + (cta < longer) : units;
+  Walker *walk0 = &ctl->walk;
+  if (u0 == u1) {
+    if (threadIdx.x == 0) {
+      walk0->pos = walk0->last = units;
+      walk0->over = 0;
     }
+  } else if (mine > 0 && first <= u0 && u0 < first + mine) {
+    long long off = u0 - first;
+    int r = r_lo;
+    Request q;
+#pragma unroll 1
+    for (;; ++r) {
+      q.set(a, a.ctx[r], a.row_start[r], a.row_start[r + 1]);
+      const long long m = q.units(a);
+      if (off < m) break;
+      off -= m;
+    }
+    const int each = q.tiles + ITEM_UNITS;
+    const int item = (int)divide(off, each), rest = (int)(off - (long long)item * each);
+    walk0->over = max(ITEM_UNITS - rest, 0);
+    walk0->tile = max(rest - ITEM_UNITS, 0);
+    walk0->h = item / q.row_tiles;
+    walk0->rt = item % q.row_tiles;
+    walk0->r = r;
+    walk0->q = q;
+    walk0->end = a.row_start[r + 1];
+    walk0->pos = u0;
+    walk0->last = u1;
+    walk0->ahead(a);
   }
   __syncthreads();
   const uint32_t tmem = ctl->tmem, tmem_o = tmem + 2 * NT;
-  const int start_r = ctl->start_r;
-  const long long start_off = ctl->start_off;
 
   if (warp == 0) {
     // -------------------------------------------------- copies of K and V ----
     // Row tiles of one item read the same K and V: keep them in L2 for the next.
     const uint64_t pol =
-        a.max_nodes > nodes_tile ? tc::policy_evict_normal() : tc::policy_evict_first();
+        a.max_nodes > a.nodes_tile ? tc::policy_evict_normal() : tc::policy_evict_first();
     constexpr int RING = G::FP8 ? RAWS : SLOTS;
     uint64_t *full = G::FP8 ? ctl->rfull : ctl->full, *empty = G::FP8 ? ctl->rempty : ctl->empty;
     uint8_t *ring = G::FP8 ? raws : slots;
     constexpr int RING_BYTES = G::FP8 ? G::RAW : G::SLOT;
     const int rows = min(1 << a.page_shift, BT), boxes = BT / rows;
     const uint32_t box_bytes = (uint32_t)(rows * D * (G::FP8 ? 1 : 2));
-    Walker walk;
-    Segment s;
-    walk.begin(a, nodes_tile, start_r, start_off, u0, u1);
-    int slot = 0;
+    int slot = 0, fills = 0;
     uint32_t phase = 0, used = 0;
     bool ok = true;
-    while (ok && walk.next(a, s)) {
+    // Segments are published one ahead of the copies, so that a role that needs the
+    // next one never waits for room in the ring.
+    int published = 0;
+    auto publish = [&]() {
+      const int i = published % SEGS;
+      ok = ok && warp_wait(&ctl->seg_empty[i], ((published / SEGS) & 1) ^ 1, abort);
+      if (ok && lane == 0) {
+        if (!next_segment(&ctl->walk, &ctl->seg[i], &a)) ctl->seg[i].tb = ctl->seg[i].te = 0;
+        tc::mbar_arrive(&ctl->seg_full[i]);
+      }
+      __syncwarp();
+      ++published;
+    };
+    while (ok) {
+#pragma unroll 1
+      for (int k = published ? 1 : 2; k; --k) publish();
+      const Segment s = ctl->seg[(published - 2) % SEGS];
+      if (s.tb == s.te) break;
       const int *table = a.block_table + (size_t)s.r * a.max_pages;
       // the page of box `lane` of a tile; none past the request's end
       auto page_of = [&](int tile) {
@@ -457,6 +494,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
             }
           }
           used |= 1u << slot;
+          ++fills;
           if (++slot == RING) {
             slot = 0;
             phase ^= 1;
@@ -467,15 +505,21 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     // drain: every copy issued has landed (a slot's last fill is of this pass of
     // the ring before `slot`, of the last pass from it on)
     volatile int never = 0;
+#pragma unroll 1
     for (int i = 0; i < RING; ++i)
       if (used >> i & 1) warp_wait(&full[i], i < slot ? phase : phase ^ 1, &never);
+    if (G::FP8 && ok && warp_wait(&empty[slot], phase ^ 1, abort) && lane == 0) {
+      // one fill more without data: the end
+      *(volatile int *)&ctl->raw_end = fills;
+      tc::mbar_arrive(&full[slot]);
+    }
   } else if (warp == 1) {
     // -------------------------------------------------------- MMA issuer ----
     if (lane == 0) {
       constexpr uint32_t idesc_s = tc::idesc_bf16(BT, NT);
       constexpr uint32_t idesc_o = tc::idesc_bf16(128, 2 * NT) | tc::IDESC_A_MN | tc::IDESC_B_MN;
       int k_slot = 0, v_slot = 1;
-      uint32_t k_phase = 0, v_phase = 0, t = 0, seg = 0;
+      uint32_t k_phase = 0, v_phase = 0, t = 0, pv = 0, seg = 0;
       uint32_t acc = 0;  // whether the pending tile adds to O
       auto advance = [&](int &slot, uint32_t &phase) {
         slot += 2;
@@ -484,65 +528,71 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           phase ^= 1;
         }
       };
-      auto pv = [&](uint32_t tile) -> bool {
-        if (!tc::mbar_wait(&ctl->full[v_slot], v_phase, abort)) return false;
-        if (!tc::mbar_wait(&ctl->p_full, tile & 1, abort)) return false;
-        tc::fence_after_sync();
-        // D = 64: the 128-row operand's second 64 rows are the first again, and
-        // accumulator lanes 64..127 are not read
-        const uint64_t vd = tc::smem_desc_sw128_mn(slots + v_slot * G::SLOT,
-                                                   D == 128 ? HALF_BYTES : 0);
-        const uint64_t pd = tc::smem_desc_sw128_mn(sp, HALF_BYTES);
-#pragma unroll
-        for (int k = 0; k < BT / 16; ++k)
-          tc::umma_bf16(tmem_o, vd + 128 * k, pd + 128 * k, idesc_o, acc | (k != 0));
-        tc::umma_commit(&ctl->empty[v_slot]);
-        tc::umma_commit(&ctl->pv_done);
-        advance(v_slot, v_phase);
-        return true;
-      };
-      Walker walk;
-      Segment s;
-      walk.begin(a, nodes_tile, start_r, start_off, u0, u1);
-      bool ok = true;
-      while (ok && walk.next(a, s)) {
-        // a segment's last product must not wait for the next one's Q
-        if (t > 0 && !pv(t - 1)) {
-          ok = false;
-          break;
+      // Tile t's S, then tile t - 1's O: the tensor cores work on the one while the
+      // softmax has the other.  Between two segments the order turns: a segment's
+      // last product must not wait for the next one's Q.
+      bool ok = true, first = true, more = true;
+      int tile = 0, te = 0;
+      for (bool pending = false; ok && (more || pending);) {
+        if (more && first && !pending) {  // the next segment
+          const int i = seg % SEGS;
+          ok = wait(&ctl->seg_full[i], (seg / SEGS) & 1, abort);
+          if (!ok) break;
+          tile = ctl->seg[i].tb;
+          te = ctl->seg[i].te;
+          tc::mbar_arrive(&ctl->seg_empty[i]);
+          more = tile < te;
+          if (!more) break;
         }
-        if (!tc::mbar_wait(&ctl->q_full, seg & 1, abort)) {
-          ok = false;
-          break;
-        }
-        ++seg;
-        for (int tile = s.tb; tile < s.te; ++tile) {
+        if (more && (!first || !pending)) {
           const uint32_t b = t & 1;
-          if (!tc::mbar_wait(&ctl->full[k_slot], k_phase, abort) ||
-              !tc::mbar_wait(&ctl->s_empty[b], ((t >> 1) & 1) ^ 1, abort)) {
-            ok = false;
-            break;
-          }
+          ok = (!first || wait(&ctl->q_full, seg & 1, abort)) &&
+               wait(&ctl->full[k_slot], k_phase, abort) &&
+               wait(&ctl->s_empty[b], ((t >> 1) & 1) ^ 1, abort);
+          if (!ok) break;
           tc::fence_after_sync();
+          const uint64_t kd = tc::smem_desc_sw128(slots + k_slot * G::SLOT);
+          const uint64_t qd = tc::smem_desc_sw128(sq);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t kd =
-                tc::smem_desc_sw128(slots + k_slot * G::SLOT + (k / 4) * HALF_BYTES);
-            const uint64_t qd = tc::smem_desc_sw128(sq + (k / 4) * NT * 128);
-            tc::umma_bf16(tmem + b * NT, kd + 2 * (k & 3), qd + 2 * (k & 3), idesc_s, k != 0);
-          }
+          for (int k = 0; k < D / 16; ++k)
+            tc::umma_bf16(tmem + b * NT, kd + (k / 4) * (HALF_BYTES / 16) + 2 * (k & 3),
+                          qd + (k / 4) * (NT * 128 / 16) + 2 * (k & 3), idesc_s, k != 0);
           tc::umma_commit(&ctl->empty[k_slot]);
           tc::umma_commit(&ctl->s_full[b]);
           advance(k_slot, k_phase);
-          if (tile != s.tb && !pv(t - 1)) {
-            ok = false;
-            break;
-          }
-          acc = tile != s.tb;
           ++t;
         }
+        // the product before: of this tile where a segment begins or all is done
+        const bool issued = more && (!first || !pending);
+        if (pending) {
+          ok = wait(&ctl->full[v_slot], v_phase, abort) &&
+               wait(&ctl->p_full, pv & 1, abort);
+          if (!ok) break;
+          tc::fence_after_sync();
+          // D = 64: the 128-row operand's second 64 rows are the first again, and
+          // accumulator lanes 64..127 are not read
+          const uint64_t vd = tc::smem_desc_sw128_mn(slots + v_slot * G::SLOT,
+                                                     D == 128 ? HALF_BYTES : 0);
+          const uint64_t pd = tc::smem_desc_sw128_mn(sp, HALF_BYTES);
+#pragma unroll
+          for (int k = 0; k < BT / 16; ++k)
+            tc::umma_bf16(tmem_o, vd + 128 * k, pd + 128 * k, idesc_o, acc | (k != 0));
+          tc::umma_commit(&ctl->empty[v_slot]);
+          tc::umma_commit(&ctl->pv_done);
+          advance(v_slot, v_phase);
+          ++pv;
+          pending = false;
+        }
+        if (issued) {
+          pending = true;
+          acc = !first;
+          first = false;
+          if (++tile == te) {
+            ++seg;
+            first = true;
+          }
+        }
       }
-      if (ok && t > 0) pv(t - 1);
       tc::umma_commit(&ctl->drain);  // all MMAs issued have finished
       volatile int never = 0;
       tc::mbar_wait(&ctl->drain, 0, &never);
@@ -553,7 +603,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     const int quarter = warp & 3, cg = (warp - 2) >> 2, bar = 1 + cg;
     const int token = quarter * 32 + lane, c_group = cg * G::CH * CW;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    const bool walker = ((warp - 2) & 3) == 0 && lane == 0, leader = warp == 2 && lane == 0;
+    const bool leader = warp == 2 && lane == 0;
     // P[token][column]: 64-column halves; 16-byte chunk c of a row lies at
     // c ^ (token & 7)
     auto p_at = [&](int col) -> uint4 * {
@@ -565,32 +615,33 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       return reinterpret_cast<float *>(sp + (c0 / 64) * HALF_BYTES + 8 * (q * 2 + j / 16) * 128 +
                                        (c0 % 64) * 2) + j % 16;
     };
-    auto load_q = [&](const Segment &n) {
-      const int box_bytes = nodes_tile * a.group * 128;
-      tc::mbar_expect_tx(&ctl->q_full, HALVES * box_bytes);
-      for (int c = 0; c < HALVES; ++c)
-        tc::tma_load_3d(sq + c * NT * 128, &tma_q, c * 64, n.h * a.group, n.row0 + n.node0,
-                        &ctl->q_full, tc::policy_evict_normal());
-    };
     uint32_t t = 0, seg = 0, v_slot = 1, v_phase = 0, q_loads = 0;
-    // the group's next segment into its place of the two, and that one's Q
-    auto fetch = [&](uint32_t i) {
-      const bool more = ctl->walk[cg].next(a, ctl->seg[cg][i & 1]);
-      ctl->more[cg][i & 1] = more;
-      if (more && leader) {
-        load_q(ctl->seg[cg][i & 1]);
-        ++q_loads;
-      }
-    };
-    if (leader) a.desc[cta * 8] = 0;
-    if (walker) {
-      ctl->walk[cg].begin(a, nodes_tile, start_r, start_off, u0, u1);
-      fetch(0);
-    }
-    group_sync(bar);
     bool ok = true, gone = false;
-    while (ctl->more[cg][seg & 1]) {
-      const Segment s = ctl->seg[cg][seg & 1];
+    auto segment_here = [&](uint32_t i) {
+      return wait(&ctl->seg_full[i % SEGS], (i / SEGS) & 1, abort);
+    };
+    // Q of segment i, by the leader: its place is free once the products with the
+    // last one's are done
+    auto load_q = [&](uint32_t i) {
+      if (!segment_here(i)) return;
+      const Segment *n = &ctl->seg[i % SEGS];
+      if (n->tb == n->te) return;
+      tc::mbar_expect_tx(&ctl->q_full, HALVES * a.nodes_tile * a.group * 128);
+      for (int c = 0; c < HALVES; ++c)
+        tc::tma_load_3d(sq + c * NT * 128, &tma_q, c * 64, n->h * a.group, n->row0 + n->node0,
+                        &ctl->q_full, tc::policy_evict_normal());
+      ++q_loads;
+    };
+    if (leader) {
+      a.desc[cta * 8] = 0;
+      load_q(0);
+    }
+    __syncwarp();
+    for (;;) {
+      ok = ok && __all_sync(0xffffffffu, segment_here(seg));
+      if (group_any(bar, !ok)) break;
+      const Segment s = ctl->seg[seg % SEGS];
+      if (s.tb == s.te) break;
       const float ks = a.k_scale ? a.k_scale[s.h] : 1.0f;
       const float c = a.scale * ks * LOG2E;
       const int rows = s.nodes * a.group;  // columns in use
@@ -606,8 +657,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           if (s.n < 64) word[ch] &= (1ull << s.n) - 1;
         }
         if (quarter == 0 && lane < CW) {
-          // a column that no row uses never calls for a higher reference
-          ctl->nm[col] = col < rows ? INFINITY : -INFINITY;
+          ctl->nm[col] = 0.0f;
           ctl->top[col] = order_key(-INFINITY);
         }
       }
@@ -618,12 +668,18 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       for (int ch = 0; ch < G::CH; ++ch)
 #pragma unroll
         for (int j = 0; j < CW; ++j) l[ch][j] = 0.0f;
-      uint32_t force = ~0u;  // bit ch: some column of the chunk has no reference yet
+      // bit j: column j of the chunk has no reference yet (its rows have seen nothing)
+      uint32_t unset[G::CH];
+#pragma unroll
+      for (int ch = 0; ch < G::CH; ++ch) {
+        const int n = min(max(rows - c_group - ch * CW, 0), CW);
+        unset[ch] = n == 32 ? ~0u : (1u << n) - 1;
+      }
 
       for (int tile = s.tb; tile < s.te; ++tile, ++t) {
         const uint32_t b = t & 1;
         ok = ok && warp_wait(&ctl->s_full[b], (t >> 1) & 1, abort);
-        if (tile == s.te - 1 && walker && ok) fetch(seg + 1);  // Q's last use is behind
+        if (tile == s.te - 1 && leader && ok) load_q(seg + 1);
         const int pos = tile * BT + token;
         const bool edge = tile * BT + BT > s.ctx;  // some token is a node or past the end
         bool waited = t == 0;
@@ -639,92 +695,85 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
             const int node0 = tile * BT + quarter * 32 - s.ctx;  // lane 0's node
             if (node0 + lane >= 0) seen = 0;
             const int stop = min(s.total - s.ctx, node0 + 32);
+#pragma unroll 1
             for (int j = max(node0, 0); j < stop; ++j) {
               const uint32_t by = __ballot_sync(0xffffffffu, word[ch] >> j & 1);
               if (lane == j - node0) seen = by;
             }
           }
+          // e = c * S - reference, masked; again where the references are raised
           float e[CW];
-          auto scores = [&](bool shifted) {  // e = c * S (- reference), masked
-            uint32_t sr[CW];
-            tc::tmem_ld(tmem + lanes + b * NT + c0, sr);
-            tc::tmem_wait_ld();
-            tc::reg_fence(sr);
+          for (bool again = false;; again = true) {
+            float most = -INFINITY;
+            if (ok) {
 #pragma unroll
-            for (int j = 0; j < CW; j += 4) {
-              float4 nm = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if (shifted) nm = *reinterpret_cast<const float4 *>(&ctl->nm[c0 + j]);
-              e[j] = fmaf(__uint_as_float(sr[j]), c, nm.x);
-              e[j + 1] = fmaf(__uint_as_float(sr[j + 1]), c, nm.y);
-              e[j + 2] = fmaf(__uint_as_float(sr[j + 2]), c, nm.z);
-              e[j + 3] = fmaf(__uint_as_float(sr[j + 3]), c, nm.w);
-            }
-            if (edge) {
+              for (int h = 0; h < CW; h += 16) {
+                uint32_t sr[16];
+                tc::tmem_ld16(tmem + lanes + b * NT + c0 + h, sr);
+                tc::tmem_wait_ld();
+                tc::reg_fence(sr);
 #pragma unroll
-              for (int j = 0; j < CW; ++j) e[j] = seen >> j & 1 ? e[j] : -INFINITY;
-            }
-          };
-          float most = -INFINITY;
-          if (ok) {
-            scores(true);
-#pragma unroll
-            for (int j = 0; j < CW; j += 8)
-              if (j < count) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) most = fmaxf(most, e[j + i]);
+                for (int j = 0; j < 16; j += 4) {
+                  const float4 nm = *reinterpret_cast<const float4 *>(&ctl->nm[c0 + h + j]);
+                  e[h + j] = fmaf(__uint_as_float(sr[j]), c, nm.x);
+                  e[h + j + 1] = fmaf(__uint_as_float(sr[j + 1]), c, nm.y);
+                  e[h + j + 2] = fmaf(__uint_as_float(sr[j + 2]), c, nm.z);
+                  e[h + j + 3] = fmaf(__uint_as_float(sr[j + 3]), c, nm.w);
+                }
               }
-          }
-          if (group_any(bar, (force >> ch & 1) || most > RAISE || !ok)) {
+              if (edge) {
+#pragma unroll
+                for (int j = 0; j < CW; ++j) e[j] = seen >> j & 1 ? e[j] : -INFINITY;
+              }
+              // columns that no row uses call for nothing
+#pragma unroll
+              for (int j = 0; j < CW; ++j)
+                if (j < count) most = fmaxf(most, e[j]);
+            }
+            if (again || !group_any(bar, unset[ch] != 0 || most > RAISE || !ok)) break;
             if (group_any(bar, !ok)) {
               gone = true;
               break;
             }
-            // raise the references to the columns' maxima
-            scores(false);
+            // by how much the tile passes each reference: lane j for column j
             const float peak = column_max<CW>(e, lane);
             if (lane < CW) atomicMax(&ctl->top[c0 + lane], order_key(peak));
-            group_sync(bar);
             if (!waited) ok = warp_wait(&ctl->pv_done, (t - 1) & 1, abort);
             waited = true;
-            tc::fence_after_sync();
-            scores(false);  // the maxima took their place
-            const bool scale_o = tile != s.tb && ok;
-            bool none = false;
-#pragma unroll
-            for (int j = 0; j < CW; j += 16) {
-              float keep[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float top = order_value(ctl->top[c0 + j + i]);
-                none = none || (top == -INFINITY && j + i < count);
-                e[j + i] -= top == -INFINITY ? 0.0f : top;
-                if (tile != s.tb) {
-                  const float old = -ctl->nm[c0 + j + i];
-                  // no reference before: nothing to keep
-                  keep[i] = old == -INFINITY ? 0.0f : ex2_fast(old - top);
-                  l[ch][j + i] *= keep[i];
-                }
-              }
-              if (scale_o) {
-#pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                  uint32_t o[16];
-                  tc::tmem_ld16(tmem_o + lanes + part * NT + c0 + j, o);
-                  tc::tmem_wait_ld();
-                  tc::reg_fence(o);
-#pragma unroll
-                  for (int i = 0; i < 16; ++i)
-                    o[i] = __float_as_uint(__uint_as_float(o[i]) * keep[i]);
-                  tc::tmem_st16(tmem_o + lanes + part * NT + c0 + j, o);
-                }
-              }
-            }
-            if (scale_o) tc::tmem_wait_st();
-            force = none ? force | 1u << ch : force & ~(1u << ch);
             group_sync(bar);
-            if (quarter == 0 && lane < count) ctl->nm[c0 + lane] = -order_value(ctl->top[c0 + lane]);
+            float raise = order_value(ctl->top[c0 + lane % CW]);
+            const bool fresh = unset[ch] >> (lane % CW) & 1;
+            if (!(raise > -INFINITY) || (!fresh && raise < 0.0f)) raise = 0.0f;
+            unset[ch] &= __ballot_sync(0xffffffffu, lane < CW && ctl->top[c0 + lane % CW] ==
+                                                                     order_key(-INFINITY));
+            if (tile != s.tb && ok) {  // what is summed so far, to the new references
+              tc::fence_after_sync();
+              const float keep = fresh ? 1.0f : ex2_fast(-raise);
+#pragma unroll
+              for (int j = 0; j < CW; ++j) l[ch][j] *= __shfl_sync(0xffffffffu, keep, j);
+#pragma unroll 1
+              for (int h = 0; h < 2 * CW; h += 16) {
+                const uint32_t at = tmem_o + lanes + (h < CW ? 0 : NT - CW) + c0 + h;
+                uint32_t o[16];
+                tc::tmem_ld16(at, o);
+                tc::tmem_wait_ld();
+                tc::reg_fence(o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  o[i] = __float_as_uint(__uint_as_float(o[i]) *
+                                         __shfl_sync(0xffffffffu, keep, (h + i) % CW));
+                tc::tmem_st16(at, o);
+              }
+              tc::tmem_wait_st();
+            }
+            group_sync(bar);
+            if (quarter == 0 && lane < CW) {
+              ctl->nm[c0 + lane] -= raise;
+              ctl->top[c0 + lane] = order_key(-INFINITY);
+            }
             group_sync(bar);
           }
+          if (gone) break;
           if (ch == G::CH - 1 || rows <= c0 + CW) {  // the tile's scores are read
             tc::fence_before_sync();
             __syncwarp();
@@ -756,6 +805,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           ok = ok && warp_wait(&ctl->full[v_slot], v_phase, abort);
           uint8_t *row = slots + v_slot * G::SLOT + token * 128;
           if (ok && pos >= s.ctx) {
+#pragma unroll 1
             for (int i = cg; i < HALVES * 8; i += CG) {
               uint4 *x = reinterpret_cast<uint4 *>(row + (i / 8) * HALF_BYTES + (i % 8) * 16);
               if (pos >= s.total) {
@@ -804,80 +854,109 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       const unsigned long long odd = ctl->odd[seg % 3];
       const bool whole = s.tb == 0 && s.te == s.tiles;
       const int piece = s.tb == 0 ? 1 : 0;
-      const int d = token;  // accumulator lane = column of the head
+      const int here = min(max(rows - c_group, 0), G::CH * CW);  // the group's columns in use
+      float sum[G::CH];
 #pragma unroll
       for (int ch = 0; ch < G::CH; ++ch) {
-        const int c0 = c_group + ch * CW, count = min(rows - c0, CW);
-        if (count <= 0) break;
-        float sum = 0.0f;
+        const int c0 = c_group + ch * CW;
+        sum[ch] = 0.0f;
         if (lane < CW)
-          sum = (*sum_slot(c0, 0, lane) + *sum_slot(c0, 1, lane)) +
-                (*sum_slot(c0, 2, lane) + *sum_slot(c0, 3, lane));
-        const bool sees = s.ctx > 0 || word[ch] != 0;
-        const float inv = sees ? vs / sum : 0.0f;
-        if (quarter == 0 && lane < count) {
-          const float top = order_value(ctl->top[c0 + lane]);
-          const int node = (c0 + lane) / a.group, head = s.h * a.group + (c0 + lane) % a.group;
-          if (!whole) {
-            float *ml = a.part_ml + (size_t)(cta * 2 + piece) * 2 * NT + c0 + lane;
-            ml[0] = top;
-            ml[NT] = sum;
-          } else if (a.lse) {
-            a.lse[(size_t)(s.row0 + s.node0 + node) * a.heads * a.group + head] =
-                sees ? (top + log2f(sum)) * LN2 : -INFINITY;
-          }
-        }
-        if (quarter * 32 >= D) continue;
-        int g = c0 % a.group;  // head of the group, and place, of column j
-        bf16 *dst = a.out + (s.row0 + s.node0 + c0 / a.group) * a.out_row +
-                    (s.h * a.group + g) * a.out_head + d;
-        float *po = a.part_o + ((size_t)(cta * 2 + piece) * NT + c0) * D + d;
+          sum[ch] = (*sum_slot(c0, 0, lane) + *sum_slot(c0, 1, lane)) +
+                    (*sum_slot(c0, 2, lane) + *sum_slot(c0, 3, lane));
+      }
+      group_sync(bar);  // the sums are read: P's columns become O's way out
+      // O[column][d] through shared memory: this thread has row d of it, and the
+      // group's own chunks of P's row d take it, 4 columns to a chunk (the first
+      // half of a chunk of columns where the weights' roundings lay, the second
+      // where their rests did)
+      constexpr int HW = CW / 2;
+      auto o_at = [&](int row, int j) -> float * {
+        const int c = (j % CW < HW ? 0 : NT) + c_group + j / CW * CW + j % HW / 4 * 8;
+        return reinterpret_cast<float *>(sp + (c / 64) * HALF_BYTES + row * 128 +
+                                         (((c % 64) / 8) ^ (row & 7)) * 16) + j % 4;
+      };
+      if (quarter * 32 < D) {
+        const int d = token;  // accumulator lane = column of the head
 #pragma unroll 1
-        for (int j = 0; j < count; j += 16) {
+        for (int j = 0; j < here; j += 16) {
           uint32_t o[16], o_lo[16];
-          tc::tmem_ld16(tmem_o + lanes + c0 + j, o);
-          tc::tmem_ld16(tmem_o + lanes + NT + c0 + j, o_lo);
+          tc::tmem_ld16(tmem_o + lanes + c_group + j, o);
+          tc::tmem_ld16(tmem_o + lanes + NT + c_group + j, o_lo);
           tc::tmem_wait_ld();
           tc::reg_fence(o);
           tc::reg_fence(o_lo);
+          float x[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(o_lo[i]));
+          for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(o[i]) + __uint_as_float(o_lo[i]);
+#pragma unroll 1
           for (unsigned long long m = odd; m; m &= m - 1) {
             const int at = __ffsll((long long)m) - 1, pos = s.ctx + at;
             const int page = a.block_table[(size_t)s.r * a.max_pages + (pos >> a.page_shift)];
-            float x = 0.0f;
+            float v = 0.0f;
             if (page >= 0 && page < a.n_pages) {
-              const uint8_t *v = a.v + page * a.page_bytes +
-                                 (pos & ((1 << a.page_shift) - 1)) * a.token_bytes +
-                                 s.h * a.head_bytes;
+              const uint8_t *src = a.v + page * a.page_bytes +
+                                   (pos & ((1 << a.page_shift) - 1)) * a.token_bytes +
+                                   s.h * a.head_bytes;
               if constexpr (G::FP8)
-                x = __uint_as_float(widen_e4m3x2(v[d]) << 16);
+                v = __uint_as_float(widen_e4m3x2(src[d]) << 16);
               else
-                x = __bfloat162float(reinterpret_cast<const bf16 *>(v)[d]);
+                v = __bfloat162float(reinterpret_cast<const bf16 *>(src)[d]);
             }
-            const bool finite = fabsf(x) < INFINITY;
-            const uint32_t by = __ballot_sync(0xffffffffu, word[ch] >> at & 1) >> j;
+            const bool finite = fabsf(v) < INFINITY;
+            uint32_t by = 0;
+#pragma unroll
+            for (int ch = 0; ch < G::CH; ++ch) {
+              const uint32_t all = __ballot_sync(0xffffffffu, word[ch] >> at & 1);
+              if (j / CW == ch) by = all >> (j % CW);
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              if (!finite && (by >> i & 1)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
+              if (!finite && (by >> i & 1)) x[i] += v;
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float f = __shfl_sync(0xffffffffu, inv, j + i);
-            if (j + i < count) {
-              if (whole)
-                *dst = __float2bfloat16_rn(__uint_as_float(o[i]) * f);
-              else
-                po[(j + i) * D] = __uint_as_float(o[i]);
-            }
-            ++g;
-            dst += a.out_head;
-            if (g == a.group) {
-              g = 0;
-              dst += a.out_row - a.group * a.out_head;
-            }
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<float4 *>(o_at(d, j + i)) =
+                make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        }
+      }
+      if (quarter == 0 && lane < CW) {
+#pragma unroll
+        for (int ch = 0; ch < G::CH; ++ch) {
+          const int col = c_group + ch * CW + lane;
+          if (col >= rows) continue;
+          const bool sees = s.ctx > 0 || word[ch] != 0;
+          const float ref = unset[ch] >> lane & 1 ? -INFINITY : -ctl->nm[col];
+          if (!whole) {
+            float *ml = a.part_ml + (size_t)(cta * 2 + piece) * 2 * NT + col;
+            ml[0] = ref;
+            ml[NT] = sum[ch];
+          } else if (a.lse) {
+            const int node = col / a.group, head = s.h * a.group + col - node * a.group;
+            a.lse[(size_t)(s.row0 + s.node0 + node) * a.heads * a.group + head] =
+                sees ? (ref + log2f(sum[ch])) * LN2 : -INFINITY;
           }
+          ctl->nm[col] = sees ? vs / sum[ch] : 0.0f;  // the rows' factors
+        }
+      }
+      group_sync(bar);
+      // a warp takes every fourth column, a lane 32 apart of its elements
+      int g = (c_group + quarter) % a.group, node = (c_group + quarter) / a.group;
+#pragma unroll 1
+      for (int j = quarter; j < here; j += 4) {
+        const float f = ctl->nm[c_group + j];
+        bf16 *dst = a.out + (s.row0 + s.node0 + node) * a.out_row +
+                    (s.h * a.group + g) * a.out_head + lane;
+        float *po = a.part_o + ((size_t)(cta * 2 + piece) * NT + c_group + j) * D + lane;
+#pragma unroll
+        for (int k = 0; k < D; k += 32) {
+          const float x = *o_at(lane + k, j);
+          if (whole) dst[k] = __float2bfloat16_rn(x * f);
+          else po[k] = x;
+        }
+        g += 4;
+        while (g >= a.group) {
+          g -= a.group;
+          ++node;
         }
       }
       if (leader && !whole && piece == 1) {
@@ -888,8 +967,12 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         desc[2] = s.node0;
         desc[3] = s.nodes;
         desc[4] = s.h;
-        desc[0] = (int)((end * shares - 1) / units) - cta + 1;
+        const long long u = end - 1, split = longer * (share + 1);
+        desc[0] = (int)(u < split ? divide(u, share + 1) : longer + divide(u - split, share)) -
+                  cta + 1;
       }
+      __syncwarp();
+      if (quarter == 0 && lane == 0) tc::mbar_arrive(&ctl->seg_empty[seg % SEGS]);
       ++seg;
     }
     if (leader && q_loads) {  // a Q copy still in flight lands before the CTA ends
@@ -903,24 +986,19 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     int slot = 0, raw = 0;
     uint32_t phase = 0, raw_phase = 0;
     constexpr int PARTS = D / 16;  // 16-byte parts of a raw row
-    Walker walk;
-    Segment s;
-    walk.begin(a, nodes_tile, start_r, start_off, u0, u1);
-    long long left = 0;  // tiles of K and V in this CTA's share
-    while (walk.next(a, s)) left += 2 * (s.te - s.tb);
-    for (; left > 0; --left) {
+    for (int f = 0;; ++f) {
       if (!warp_wait(&ctl->rfull[raw], raw_phase, abort) ||
-          !warp_wait(&ctl->empty[slot], phase ^ 1, abort))
+          f == *(volatile int *)&ctl->raw_end || !warp_wait(&ctl->empty[slot], phase ^ 1, abort))
         break;
       const uint8_t *src = raws + raw * G::RAW;
       uint8_t *dst = slots + slot * G::SLOT;
       // eight lanes take eight tokens: the swizzles spread both sides over all banks
-      const int token = (w & 3) * 32 + lane;
+      const int token = (w & 3) * 32 + lane;  // eight warps: two for a token's parts
       // raw rows of 128 bytes are swizzled by token & 7, of 64 bytes by (token >> 1) & 3
       const int raw_x = D == 128 ? token & 7 : (token >> 1) & 3;
 #pragma unroll
-      for (int i0 = 0; i0 < PARTS / 2; ++i0) {
-        const int p = 2 * i0 + (w >> 2);
+      for (int i0 = 0; i0 < PARTS * 4 / G::CV; ++i0) {
+        const int p = (G::CV / 4) * i0 + (w >> 2);
         const uint4 x = *reinterpret_cast<const uint4 *>(src + token * D + ((p ^ raw_x) * 16));
         const uint32_t v[4] = {x.x, x.y, x.z, x.w};
         uint32_t o[8];
@@ -965,7 +1043,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
 // The cut items: block (c, y) joins the pieces of the item that CTA c began and
 // could not finish, a warp taking one row, its own pieces in order.
 template <int D>
-__global__ void __launch_bounds__(128) tree_attention_join(const Args a, int nt) {
+__global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant__ Args a, int nt) {
   constexpr int E = D / 32;
   pdl_trigger();
   pdl_wait();
@@ -975,27 +1053,25 @@ __global__ void __launch_bounds__(128) tree_attention_join(const Args a, int nt)
   if (pieces == 0 || col >= desc[3] * a.group) return;
   // piece 0 is CTA c's last one, piece k > 0 CTA (c + k)'s first
   auto at = [&](int k) -> size_t { return (size_t)(k ? 2 * (c + k) : 2 * c + 1) * nt; };
-  float top = -INFINITY, sum = 0.0f;
+  float top = -INFINITY;
+#pragma unroll 1
   for (int k = lane; k < pieces; k += 32) top = fmaxf(top, a.part_ml[2 * at(k) + col]);
   top = warp_max(top);
-  for (int k = lane; k < pieces; k += 32) {
-    const float m = a.part_ml[2 * at(k) + col];
-    sum += m == -INFINITY ? 0.0f : ex2_fast(m - top) * a.part_ml[2 * at(k) + nt + col];
-  }
-  sum = warp_sum(sum);
-  float o[E] = {};
+  float sum = 0.0f, o[E] = {};
+#pragma unroll 4
   for (int k = 0; k < pieces; ++k) {
     const float m = a.part_ml[2 * at(k) + col], w = m == -INFINITY ? 0.0f : ex2_fast(m - top);
-    const float *src = a.part_o + (at(k) + col) * D + lane * E;
+    const float *src = a.part_o + (at(k) + col) * D + lane;
+    sum = fmaf(w, a.part_ml[2 * at(k) + nt + col], sum);
 #pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = fmaf(w, src[i], o[i]);
+    for (int i = 0; i < E; ++i) o[i] = fmaf(w, src[32 * i], o[i]);
   }
   const int row = desc[1] + desc[2] + col / a.group, h = desc[4];
   const int head = h * a.group + col % a.group;
   const float f = (a.v_scale ? a.v_scale[h] : 1.0f) / sum;
+  bf16 *dst = a.out + row * a.out_row + head * a.out_head + lane;
 #pragma unroll
-  for (int i = 0; i < E; ++i)
-    a.out[row * a.out_row + head * a.out_head + lane * E + i] = __float2bfloat16_rn(o[i] * f);
+  for (int i = 0; i < E; ++i) dst[32 * i] = __float2bfloat16_rn(o[i] * f);
   if (a.lse && lane == 0)
     a.lse[(size_t)row * a.heads * a.group + head] = (top + log2f(sum)) * LN2;
 }
