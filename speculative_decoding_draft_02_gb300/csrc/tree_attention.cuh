@@ -199,6 +199,7 @@ __device__ __forceinline__ bool next_segment(Walker *w, Segment *s, const Args *
 
 // A quotient of two non-negative 64-bit numbers: a call, for its size.
 __device__ __noinline__ long long divide(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
   return (long long)((unsigned long long)x / (unsigned long long)y);
 }
 
@@ -657,7 +658,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           if (s.n < 64) word[ch] &= (1ull << s.n) - 1;
         }
         if (quarter == 0 && lane < CW) {
-          ctl->nm[col] = 0.0f;
+          // a column that no row uses has no weight and calls for nothing
+          ctl->nm[col] = col < rows ? 0.0f : -INFINITY;
           ctl->top[col] = order_key(-INFINITY);
         }
       }
@@ -687,8 +689,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
 #pragma unroll
         for (int ch = 0; ch < G::CH; ++ch) {
           const int c0 = c_group + ch * CW;
-          const int count = min(max(rows - c0, 0), CW);
-          if (ch > 0 && count == 0) break;
+          if (ch > 0 && c0 >= rows) break;
           // which of the chunk's columns see this thread's token
           uint32_t seen = 0xffffffffu;
           if (edge) {
@@ -725,10 +726,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
 #pragma unroll
                 for (int j = 0; j < CW; ++j) e[j] = seen >> j & 1 ? e[j] : -INFINITY;
               }
-              // columns that no row uses call for nothing
 #pragma unroll
-              for (int j = 0; j < CW; ++j)
-                if (j < count) most = fmaxf(most, e[j]);
+              for (int j = 0; j < CW; ++j) most = fmaxf(most, e[j]);
             }
             if (again || !group_any(bar, unset[ch] != 0 || most > RAISE || !ok)) break;
             if (group_any(bar, !ok)) {
@@ -779,23 +778,26 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&ctl->s_empty[b]);
           }
+          // e's place is taken by the weights: roundings below, rests above
+#pragma unroll
+          for (int j = 0; j < CW; j += 2) {
+            const float x = ex2_fast(e[j]), y = ex2_fast(e[j + 1]);
+            l[ch][j] += x;
+            l[ch][j + 1] += y;
+            const uint32_t hi = pack_bf16(x, y);
+            e[j] = __uint_as_float(hi);
+            e[j + 1] = __uint_as_float(pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi)));
+          }
           if (!waited) ok = warp_wait(&ctl->pv_done, (t - 1) & 1, abort);  // P is free
           waited = true;
 #pragma unroll
-          for (int j = 0; j < CW; j += 8)
-            if (j < count) {
-              uint32_t hi[4], lo[4];
+          for (int j = 0; j < CW; j += 8) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float x = ex2_fast(e[j + 2 * i]), y = ex2_fast(e[j + 2 * i + 1]);
-                l[ch][j + 2 * i] += x;
-                l[ch][j + 2 * i + 1] += y;
-                hi[i] = pack_bf16(x, y);
-                lo[i] = pack_bf16(x - bf16_lo(hi[i]), y - bf16_hi(hi[i]));
-              }
-              *p_at(c0 + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              *p_at(NT + c0 + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            }
+            for (int part = 0; part < 2; ++part)
+              *p_at(part * NT + c0 + j) = make_uint4(
+                  __float_as_uint(e[j + part]), __float_as_uint(e[j + 2 + part]),
+                  __float_as_uint(e[j + 4 + part]), __float_as_uint(e[j + 6 + part]));
+          }
         }
         if (gone) break;
         if (edge) {
@@ -864,19 +866,33 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           sum[ch] = (*sum_slot(c0, 0, lane) + *sum_slot(c0, 1, lane)) +
                     (*sum_slot(c0, 2, lane) + *sum_slot(c0, 3, lane));
       }
-      group_sync(bar);  // the sums are read: P's columns become O's way out
-      // O[column][d] through shared memory: this thread has row d of it, and the
-      // group's own chunks of P's row d take it, 4 columns to a chunk (the first
-      // half of a chunk of columns where the weights' roundings lay, the second
-      // where their rests did)
-      constexpr int HW = CW / 2;
-      auto o_at = [&](int row, int j) -> float * {
-        const int c = (j % CW < HW ? 0 : NT) + c_group + j / CW * CW + j % HW / 4 * 8;
-        return reinterpret_cast<float *>(sp + (c / 64) * HALF_BYTES + row * 128 +
-                                         (((c % 64) / 8) ^ (row & 7)) * 16) + j % 4;
-      };
+      if (quarter == 0 && lane < CW) {
+#pragma unroll
+        for (int ch = 0; ch < G::CH; ++ch) {
+          const int col = c_group + ch * CW + lane;
+          if (col >= rows) continue;
+          const bool sees = s.ctx > 0 || word[ch] != 0;
+          const float ref = unset[ch] >> lane & 1 ? -INFINITY : -ctl->nm[col];
+          if (!whole) {
+            float *ml = a.part_ml + (size_t)(cta * 2 + piece) * 2 * NT + col;
+            ml[0] = ref;
+            ml[NT] = sum[ch];
+          } else if (a.lse) {
+            const int node = col / a.group, head = s.h * a.group + col - node * a.group;
+            a.lse[(size_t)(s.row0 + s.node0 + node) * a.heads * a.group + head] =
+                sees ? (ref + log2f(sum[ch])) * LN2 : -INFINITY;
+          }
+          ctl->nm[col] = sees ? vs / sum[ch] : 0.0f;  // the rows' factors
+        }
+      }
+      group_sync(bar);
       if (quarter * 32 < D) {
         const int d = token;  // accumulator lane = column of the head
+        int g = c_group % a.group;
+        bf16 *dst = a.out + (s.row0 + s.node0 + c_group / a.group) * a.out_row +
+                    (s.h * a.group + g) * a.out_head + d;
+        const int64_t wrap = a.out_row - a.group * a.out_head;  // to the next node's first head
+        float *po = a.part_o + ((size_t)(cta * 2 + piece) * NT + c_group) * D + d;
 #pragma unroll 1
         for (int j = 0; j < here; j += 16) {
           uint32_t o[16], o_lo[16];
@@ -913,50 +929,21 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
             for (int i = 0; i < 16; ++i)
               if (!finite && (by >> i & 1)) x[i] += v;
           }
-#pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<float4 *>(o_at(d, j + i)) =
-                make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-        }
-      }
-      if (quarter == 0 && lane < CW) {
-#pragma unroll
-        for (int ch = 0; ch < G::CH; ++ch) {
-          const int col = c_group + ch * CW + lane;
-          if (col >= rows) continue;
-          const bool sees = s.ctx > 0 || word[ch] != 0;
-          const float ref = unset[ch] >> lane & 1 ? -INFINITY : -ctl->nm[col];
           if (!whole) {
-            float *ml = a.part_ml + (size_t)(cta * 2 + piece) * 2 * NT + col;
-            ml[0] = ref;
-            ml[NT] = sum[ch];
-          } else if (a.lse) {
-            const int node = col / a.group, head = s.h * a.group + col - node * a.group;
-            a.lse[(size_t)(s.row0 + s.node0 + node) * a.heads * a.group + head] =
-                sees ? (ref + log2f(sum[ch])) * LN2 : -INFINITY;
-          }
-          ctl->nm[col] = sees ? vs / sum[ch] : 0.0f;  // the rows' factors
-        }
-      }
-      group_sync(bar);
-      // a warp takes every fourth column, a lane 32 apart of its elements
-      int g = (c_group + quarter) % a.group, node = (c_group + quarter) / a.group;
-#pragma unroll 1
-      for (int j = quarter; j < here; j += 4) {
-        const float f = ctl->nm[c_group + j];
-        bf16 *dst = a.out + (s.row0 + s.node0 + node) * a.out_row +
-                    (s.h * a.group + g) * a.out_head + lane;
-        float *po = a.part_o + ((size_t)(cta * 2 + piece) * NT + c_group + j) * D + lane;
 #pragma unroll
-        for (int k = 0; k < D; k += 32) {
-          const float x = *o_at(lane + k, j);
-          if (whole) dst[k] = __float2bfloat16_rn(x * f);
-          else po[k] = x;
-        }
-        g += 4;
-        while (g >= a.group) {
-          g -= a.group;
-          ++node;
+            for (int i = 0; i < 16; ++i)
+              if (j + i < here) po[(j + i) * D] = x[i];
+            continue;
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (j + i < here) *dst = __float2bfloat16_rn(x[i] * ctl->nm[c_group + j + i]);
+            dst += a.out_head;
+            if (++g == a.group) {
+              g = 0;
+              dst += wrap;
+            }
+          }
         }
       }
       if (leader && !whole && piece == 1) {
