@@ -137,9 +137,16 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without making a Stream object (3 us of a 3 us launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream: Optional[torch.cuda.Stream]):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and torch.cuda.is_initialized():
+        return _raw_stream(torch._C._cuda_getDevice())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _bf16(t: torch.Tensor) -> torch.Tensor:
@@ -297,34 +304,50 @@ def dspark_verify_residual_rows(dims, workspace, stream=None):
 
 # ------------------------------------------- the target's paged KV cache ----
 
-def _want(what: str, name: str, t, dtype, shape, optional=False):
-    """The tensor's pointer, once its type and shape are what the call reads; a None
-    in `shape` is any size."""
-    if t is None and optional:
-        return None
-    if t is None or t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise DSparkError(f"{what}: {name} must be {dtype}")
-    if len(t.shape) != len(shape) or any(n is not None and n != m
-                                         for n, m in zip(shape, t.shape)):
-        raise DSparkError(f"{what}: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    return _ptr(t)
+# A call's arguments are checked in the 5 to 8 us that the GPU takes for a small one:
+# one expression per tensor, and the message only when it is wanted.
+
+def _want(what: str, name: str, t, dtype, shape) -> int:
+    """The tensor's address, once its type and shape are what the call reads."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise DSparkError(f"{what}: {name} must be a tensor") from None
+    raise DSparkError(f"{what}: {name} must be a contiguous {dtype} tensor {tuple(shape)} on the "
+                      f"GPU, not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _rows_view(what: str, name: str, t, heads, dim):
-    """A bf16 [rows, heads, dim] view whose last dimension is dense: (pointer, strides)."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1:] != (heads, dim):
-        raise DSparkError(f"{what}: {name} must be bfloat16 [rows, {heads}, {dim}]")
-    if not t.is_cuda:
-        raise DSparkError("tensor must live on the GPU")
-    if t.stride(2) != 1:
-        raise DSparkError(f"{what}: {name}'s last dimension must be dense")
+    """A bf16 [rows, heads, dim] view whose last dimension is dense: (address, rows,
+    row stride, head stride)."""
+    try:
+        shape, stride = t.shape, t.stride()
+        if not (t.dtype is torch.bfloat16 and len(shape) == 3 and shape[1] == heads
+                and shape[2] == dim and stride[2] == 1 and t.is_cuda):
+            raise DSparkError(f"{what}: {name} must be bfloat16 [rows, {heads}, {dim}] on the GPU "
+                              "with a dense last dimension")
+    except AttributeError:
+        raise DSparkError(f"{what}: {name} must be a tensor") from None
     # a dimension of one element may carry any stride: what the call would step by is unused
-    head = t.stride(1) if heads > 1 else dim
-    row = t.stride(0) if t.shape[0] > 1 else max(8, heads * head)
-    return ctypes.c_void_p(t.data_ptr()), row, head
+    head = stride[1] if heads > 1 else dim
+    row = stride[0] if shape[0] > 1 else max(8, heads * head)
+    return t.data_ptr(), shape[0], row, head
 
 
-_MASK = (torch.int64, torch.uint64)
+def _size(what: str, name: str, t, dims: int):
+    """A tensor's shape, of so many dimensions."""
+    shape = getattr(t, "shape", ())
+    if len(shape) != dims:
+        raise DSparkError(f"{what}: {name} must have {dims} dimensions")
+    return shape
+
+
+def _masks(what: str, anc, rows: int):
+    if anc is None:
+        return None
+    return _want(what, "anc", anc, torch.int64 if anc.dtype is torch.int64 else torch.uint64,
+                 (rows,))
 
 
 class KVCache:
@@ -347,7 +370,8 @@ class KVCache:
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is not None and not fp8:
                 raise DSparkError("KVCache: a bfloat16 cache has no scales")
-            _want("KVCache", name, t, torch.float32, (self.heads,), optional=True)
+            if t is not None:
+                _want("KVCache", name, t, torch.float32, (self.heads,))
         # strides over a single page or head are never stepped by
         head = k.stride(2) if self.heads > 1 else self.dim
         page = k.stride(0) if self.n_pages > 1 else self.page_size * self.heads * self.dim
@@ -356,41 +380,42 @@ class KVCache:
                                     v_scale.data_ptr() if v_scale is not None else None,
                                     page, k.stride(1), head, self.n_pages, self.page_size,
                                     self.heads, self.dim, KV_E4M3 if fp8 else KV_BF16)
+        self.ref = ctypes.byref(self.struct)
 
 
 def dspark_kv_plan(ctx, length, extra, parent, page_size, held, n_free, free_pages, block_table,
                    held_out, n_free_out, row_start, position, slot, anc=None, stream=None):
     """parent [R, gamma] or None (chains); anc int64 (the 64-bit words) or None."""
     what, i32 = "dspark_kv_plan", torch.int32
-    R, rows = ctx.shape[0], position.shape[0]
-    if block_table.dim() != 2:
-        raise DSparkError(f"{what}: block_table must be [R, max_pages]")
-    gamma = parent.shape[1] if parent is not None and parent.dim() == 2 else 0
+    R, rows = len(ctx), len(position)
+    table = _size(what, "block_table", block_table, 2)
+    gamma = _size(what, "parent", parent, 2)[1] if parent is not None else 0
+    pages = len(free_pages)
     _check(load_library().dspark_kv_plan(
-        R, gamma, int(extra), rows, int(page_size), free_pages.shape[0], block_table.shape[1],
+        R, gamma, extra, rows, page_size, pages, table[1],
         _want(what, "ctx", ctx, i32, (R,)), _want(what, "len", length, i32, (R,)),
-        _want(what, "parent", parent, i32, (R, gamma), optional=True),
+        None if parent is None else _want(what, "parent", parent, i32, (R, gamma)),
         _want(what, "held", held, i32, (R,)), _want(what, "n_free", n_free, i32, (1,)),
-        _want(what, "free_pages", free_pages, i32, (None,)),
-        _want(what, "block_table", block_table, i32, (R, None)),
+        _want(what, "free_pages", free_pages, i32, (pages,)),
+        _want(what, "block_table", block_table, i32, (R, table[1])),
         _want(what, "held_out", held_out, i32, (R,)),
         _want(what, "n_free_out", n_free_out, i32, (1,)),
         _want(what, "row_start", row_start, i32, (R + 1,)),
         _want(what, "position", position, i32, (rows,)),
-        _want(what, "slot", slot, torch.int64, (rows,)),
-        _want(what, "anc", anc, _MASK, (rows,), optional=True), _stream(stream)), what)
+        _want(what, "slot", slot, torch.int64, (rows,)), _masks(what, anc, rows),
+        _stream(stream)), what)
 
 
 def dspark_kv_append(cache: KVCache, k, v, slot, stream=None):
     """k, v bf16 [rows, heads, dim] views of equal strides."""
     what = "dspark_kv_append"
-    kp, row, head = _rows_view(what, "k", k, cache.heads, cache.dim)
-    vp, row_v, head_v = _rows_view(what, "v", v, cache.heads, cache.dim)
-    if k.shape != v.shape or (row, head) != (row_v, head_v):
+    kp, rows, row, head = _rows_view(what, "k", k, cache.heads, cache.dim)
+    vp, *rest = _rows_view(what, "v", v, cache.heads, cache.dim)
+    if rest != [rows, row, head]:
         raise DSparkError(f"{what}: k and v must have equal shapes and strides")
     _check(load_library().dspark_kv_append(
-        ctypes.byref(cache.struct), k.shape[0], kp, vp, row, head,
-        _want(what, "slot", slot, torch.int64, (k.shape[0],)), _stream(stream)), what)
+        cache.ref, rows, kp, vp, row, head, _want(what, "slot", slot, torch.int64, (rows,)),
+        _stream(stream)), what)
 
 
 def dspark_tree_attention_workspace_bytes(cache: KVCache, R, heads_q, max_nodes) -> int:
@@ -403,18 +428,18 @@ def dspark_tree_attention(cache: KVCache, q, ctx, row_start, anc, block_table, m
     """q, out bf16 [rows, heads_q, dim] (views with a dense last dimension); anc or lse may
     be None."""
     what, i32 = "dspark_tree_attention", torch.int32
-    R, rows, heads_q = ctx.shape[0], q.shape[0], q.shape[1] if q.dim() == 3 else 0
-    qp, q_row, q_head = _rows_view(what, "q", q, heads_q, cache.dim)
-    op, o_row, o_head = _rows_view(what, "out", out, heads_q, cache.dim)
-    if out.shape[0] != rows:
+    R, heads_q = len(ctx), _size(what, "q", q, 3)[1]
+    qp, rows, q_row, q_head = _rows_view(what, "q", q, heads_q, cache.dim)
+    op, o_rows, o_row, o_head = _rows_view(what, "out", out, heads_q, cache.dim)
+    if o_rows != rows:
         raise DSparkError(f"{what}: out must have q's rows")
+    pages = _size(what, "block_table", block_table, 2)[1]
     _check(load_library().dspark_tree_attention(
-        ctypes.byref(cache.struct), R, heads_q, int(max_nodes), rows,
-        block_table.shape[1] if block_table.dim() == 2 else 0, qp, q_row, q_head,
+        cache.ref, R, heads_q, max_nodes, rows, pages, qp, q_row, q_head,
         _want(what, "ctx", ctx, i32, (R,)), _want(what, "row_start", row_start, i32, (R + 1,)),
-        _want(what, "anc", anc, _MASK, (rows,), optional=True),
-        _want(what, "block_table", block_table, i32, (R, None)), float(scale), op, o_row, o_head,
-        _want(what, "lse", lse, torch.float32, (rows, heads_q), optional=True),
+        _masks(what, anc, rows), _want(what, "block_table", block_table, i32, (R, pages)), scale,
+        op, o_row, o_head,
+        None if lse is None else _want(what, "lse", lse, torch.float32, (rows, heads_q)),
         _ptr(workspace), workspace.numel(), _stream(stream)), what)
 
 
@@ -422,30 +447,26 @@ def dspark_tree_accept(row_start, parent, tokens, choice, ctx, accepted, bonus, 
                        stream=None):
     """parent [R, gamma] or None (chains)."""
     what, i32 = "dspark_tree_accept", torch.int32
-    if tokens.dim() != 2:
-        raise DSparkError(f"{what}: tokens must be [R, gamma]")
-    R, gamma = tokens.shape
+    R, gamma = shape = _size(what, "tokens", tokens, 2)
+    rows = len(choice)
     _check(load_library().dspark_tree_accept(
-        R, gamma, choice.shape[0], _want(what, "row_start", row_start, i32, (R + 1,)),
-        _want(what, "parent", parent, i32, (R, gamma), optional=True),
-        _want(what, "tokens", tokens, i32, (R, gamma)),
-        _want(what, "choice", choice, i32, (None,)), _want(what, "ctx", ctx, i32, (R,)),
-        _want(what, "accepted", accepted, i32, (R,)), _want(what, "bonus", bonus, i32, (R,)),
-        _want(what, "path", path, i32, (R, gamma)), _want(what, "ctx_out", ctx_out, i32, (R,)),
-        _stream(stream)), what)
+        R, gamma, rows, _want(what, "row_start", row_start, i32, (R + 1,)),
+        None if parent is None else _want(what, "parent", parent, i32, shape),
+        _want(what, "tokens", tokens, i32, shape), _want(what, "choice", choice, i32, (rows,)),
+        _want(what, "ctx", ctx, i32, (R,)), _want(what, "accepted", accepted, i32, (R,)),
+        _want(what, "bonus", bonus, i32, (R,)), _want(what, "path", path, i32, shape),
+        _want(what, "ctx_out", ctx_out, i32, (R,)), _stream(stream)), what)
 
 
 def dspark_kv_compact(cache: KVCache, ctx, accepted, path, block_table, stream=None):
     """ctx as it was before dspark_tree_accept."""
     what, i32 = "dspark_kv_compact", torch.int32
-    if path.dim() != 2 or block_table.dim() != 2:
-        raise DSparkError(f"{what}: path must be [R, gamma], block_table [R, max_pages]")
-    R, gamma = path.shape
+    R, gamma = shape = _size(what, "path", path, 2)
+    pages = _size(what, "block_table", block_table, 2)[1]
     _check(load_library().dspark_kv_compact(
-        ctypes.byref(cache.struct), R, gamma, block_table.shape[1],
-        _want(what, "ctx", ctx, i32, (R,)), _want(what, "accepted", accepted, i32, (R,)),
-        _want(what, "path", path, i32, (R, gamma)),
-        _want(what, "block_table", block_table, i32, (R, None)), _stream(stream)), what)
+        cache.ref, R, gamma, pages, _want(what, "ctx", ctx, i32, (R,)),
+        _want(what, "accepted", accepted, i32, (R,)), _want(what, "path", path, i32, shape),
+        _want(what, "block_table", block_table, i32, (R, pages)), _stream(stream)), what)
 
 
 def dspark_device_status(stream=None, clear: bool = True) -> int:
