@@ -45,7 +45,7 @@ namespace attn {
 
 constexpr int BT = 128;                 // tokens of a tile
 constexpr int SMEM_LIMIT = 232448;      // 227 KB
-constexpr int CTL_BYTES = 2560;
+constexpr int CTL_BYTES = 3072;
 constexpr int MAX_SLOTS = 12;
 constexpr int SEGS = 8;
 // What beginning and ending an item costs a CTA, in tiles (measured: about one
@@ -75,17 +75,22 @@ struct Args {
 template <int TYPE, int D, int NT>
 struct Geo {
   static constexpr bool FP8 = TYPE == DSPARK_KV_E4M3;
-  static constexpr int CW = NT < 32 ? NT : 32;  // columns of a softmax thread
-  static constexpr int CG = NT >= 64 ? 2 : 1;   // groups of softmax warps
-  static constexpr int CH = NT / (CW * CG);     // chunks of columns of a thread
-  static constexpr int SW = 4 * CG;
-  // at most 14 warps with those that widen: a softmax thread keeps its columns'
-  // sums in registers
-  static constexpr int CV = !FP8 ? 0 : CG == 2 ? 4 : 8;
+  // Up to 64 columns two sets of softmax warps take a segment's tiles in turn, each
+  // with its S, P, references, sums and O: what one waits for (S, the tensor
+  // memory, the group's barrier, P's place) the other's work covers.  128 columns
+  // leave no tensor memory for a second O: one set of two groups, each with half
+  // the columns; so do 64 beside the warps that widen, for their registers' sake.
+  static constexpr int SETS = NT <= (FP8 ? 32 : 64) ? 2 : 1;
+  static constexpr int CW = NT < 32 ? NT : 32;       // columns of a softmax thread's chunk
+  static constexpr int CG = SETS == 2 ? 1 : 2;       // groups of four warps in a set
+  static constexpr int CH = NT / (CW * CG);          // chunks of a thread
+  static constexpr int SW = 4 * CG * SETS;
+  static constexpr int CV = FP8 ? 4 : 0;
   static constexpr int THREADS = 32 * (2 + SW + CV);
   static constexpr int SLOT = BT * D * 2;
   static constexpr int Q_BYTES = NT * D * 2;
-  static constexpr int P_BYTES = BT * 128 * (NT > 32 ? NT / 32 : 1);
+  static constexpr int P_SET = BT * 128 * (NT > 32 ? NT / 32 : 1);
+  static constexpr int P_BYTES = SETS * P_SET;
   static constexpr int ROOM = SMEM_LIMIT - CTL_BYTES - Q_BYTES - P_BYTES;
   static constexpr int RAW = FP8 ? BT * D : 0;
   // 8-bit: three widened tiles (one read by each product, one being written);
@@ -94,7 +99,9 @@ struct Geo {
   static constexpr int RAWS_FIT = FP8 ? (ROOM - 3 * SLOT) / (RAW + !FP8) : 0;
   static constexpr int RAWS = RAWS_FIT < MAX_SLOTS ? RAWS_FIT : MAX_SLOTS;
   static constexpr int SMEM_BYTES = SLOTS * SLOT + RAWS * RAW + Q_BYTES + P_BYTES + CTL_BYTES;
-  static constexpr uint32_t TMEM_COLS = 4 * NT;  // two tiles of S, and O's two parts
+  // two tiles of S, and each set's O in its two parts
+  static constexpr uint32_t TMEM_USED = 2 * NT + SETS * 2 * NT;
+  static constexpr uint32_t TMEM_COLS = TMEM_USED <= 128 ? 128 : TMEM_USED <= 256 ? 256 : 512;
   static_assert(SLOTS >= 3 && (!FP8 || RAWS >= 3) && SMEM_BYTES <= SMEM_LIMIT, "shared memory");
 };
 
@@ -205,16 +212,22 @@ __device__ __noinline__ long long divide(long long x, long long y) {
 
 struct Ctl {
   uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], rfull[MAX_SLOTS], rempty[MAX_SLOTS];
-  uint64_t q_full, s_full[2], s_empty[2], p_full, pv_done, drain;
-  alignas(16) float nm[128];  // minus each column's reference exponent (log2)
+  uint64_t q_full, s_full[2], s_empty[2], drain;
+  // by set: P written, its product done, O read by the segment's last set, and the
+  // other's sums ready for it
+  uint64_t p_full[2], pv_done[2], o_free[2], half[2];
+  // by set and column (one set: 128 columns)
+  alignas(16) float nm[128];  // minus the column's reference exponent (log2)
   int top[128];           // how far a tile's scores pass it, as an ordered key
+  alignas(16) float other[2][64];  // a set's references and sums, for the other
   long long sums[32];
   Walker walk;
   // The share's segments as the copying warp comes to them, for the other roles.
   alignas(16) Segment seg[SEGS];
   uint64_t seg_full[SEGS], seg_empty[SEGS];
   int raw_end;            // 8-bit: fills of the raw ring
-  unsigned long long odd[3];  // nodes with non-finite V, by segment mod 3
+  unsigned long long odd[4];  // nodes with non-finite V, by segment mod 4
+  int tail;               // the CTA leaves an item to its successors
   int abort;
   uint32_t tmem;
 };
@@ -337,18 +350,21 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     tc::mbar_init(&ctl->q_full, 1);
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&ctl->s_full[b], 1);
-      tc::mbar_init(&ctl->s_empty[b], G::SW);
+      tc::mbar_init(&ctl->s_empty[b], 4 * CG);
+      tc::mbar_init(&ctl->p_full[b], 4 * CG);
+      tc::mbar_init(&ctl->pv_done[b], 1);
+      tc::mbar_init(&ctl->o_free[b], 4);
+      tc::mbar_init(&ctl->half[b], 1);
     }
-    tc::mbar_init(&ctl->p_full, G::SW);
-    tc::mbar_init(&ctl->pv_done, 1);
     tc::mbar_init(&ctl->drain, 1);
-    for (int i = 0; i < 3; ++i) ctl->odd[i] = 0;
+    for (int i = 0; i < 4; ++i) ctl->odd[i] = 0;
+    ctl->tail = 0;
     ctl->abort = 0;
     ctl->raw_end = -1;
 #pragma unroll 1
     for (int i = 0; i < SEGS; ++i) {
       tc::mbar_init(&ctl->seg_full[i], 1);
-      tc::mbar_init(&ctl->seg_empty[i], 1 + CG);  // the MMA issuer, each softmax group
+      tc::mbar_init(&ctl->seg_empty[i], 1 + G::SETS * CG);  // the MMA issuer, each group
     }
     tc::fence_barrier_init();
     tc::tma_prefetch_desc(&tma_k);
@@ -522,6 +538,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       int k_slot = 0, v_slot = 1;
       uint32_t k_phase = 0, v_phase = 0, t = 0, pv = 0, seg = 0;
       uint32_t acc = 0;  // whether the pending tile adds to O
+      uint32_t uses[2] = {0, 0};  // segments that each set had a part in
       auto advance = [&](int &slot, uint32_t &phase) {
         slot += 2;
         if (slot >= SLOTS) {
@@ -533,7 +550,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       // softmax has the other.  Between two segments the order turns: a segment's
       // last product must not wait for the next one's Q.
       bool ok = true, first = true, more = true;
-      int tile = 0, te = 0;
+      int tile = 0, te = 0, place = 0;  // place: of the tile in its segment
       for (bool pending = false; ok && (more || pending);) {
         if (more && first && !pending) {  // the next segment
           const int i = seg % SEGS;
@@ -544,8 +561,10 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           tc::mbar_arrive(&ctl->seg_empty[i]);
           more = tile < te;
           if (!more) break;
+          place = 0;
         }
-        if (more && (!first || !pending)) {
+        const bool issue = more && (!first || !pending);
+        if (issue) {
           const uint32_t b = t & 1;
           ok = (!first || wait(&ctl->q_full, seg & 1, abort)) &&
                wait(&ctl->full[k_slot], k_phase, abort) &&
@@ -563,30 +582,34 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           advance(k_slot, k_phase);
           ++t;
         }
-        // the product before: of this tile where a segment begins or all is done
-        const bool issued = more && (!first || !pending);
-        if (pending) {
+        if (pending) {  // the product before
+          const int x = G::SETS == 2 ? pv & 1 : 0;
           ok = wait(&ctl->full[v_slot], v_phase, abort) &&
-               wait(&ctl->p_full, pv & 1, abort);
+               wait(&ctl->p_full[x], (pv / G::SETS) & 1, abort);
+          if (ok && G::SETS == 2 && !acc) {  // a segment's first: its last O there is read
+            ok = uses[x] == 0 || wait(&ctl->o_free[x], (uses[x] - 1) & 1, abort);
+            ++uses[x];
+          }
           if (!ok) break;
           tc::fence_after_sync();
           // D = 64: the 128-row operand's second 64 rows are the first again, and
           // accumulator lanes 64..127 are not read
           const uint64_t vd = tc::smem_desc_sw128_mn(slots + v_slot * G::SLOT,
                                                      D == 128 ? HALF_BYTES : 0);
-          const uint64_t pd = tc::smem_desc_sw128_mn(sp, HALF_BYTES);
+          const uint64_t pd = tc::smem_desc_sw128_mn(sp + x * G::P_SET, HALF_BYTES);
 #pragma unroll
           for (int k = 0; k < BT / 16; ++k)
-            tc::umma_bf16(tmem_o, vd + 128 * k, pd + 128 * k, idesc_o, acc | (k != 0));
+            tc::umma_bf16(tmem_o + x * 2 * NT, vd + 128 * k, pd + 128 * k, idesc_o, acc | (k != 0));
           tc::umma_commit(&ctl->empty[v_slot]);
-          tc::umma_commit(&ctl->pv_done);
+          tc::umma_commit(&ctl->pv_done[x]);
           advance(v_slot, v_phase);
           ++pv;
           pending = false;
         }
-        if (issued) {
+        if (issue) {
           pending = true;
-          acc = !first;
+          acc = place >= G::SETS;  // the pending tile adds to what its set has
+          ++place;
           first = false;
           if (++tile == te) {
             ++seg;
@@ -601,22 +624,31 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     __syncwarp();
   } else if (warp < 2 + G::SW) {
     // ----------------------------------------------------------- softmax ----
-    const int quarter = warp & 3, cg = (warp - 2) >> 2, bar = 1 + cg;
+    const int quarter = warp & 3, group = (warp - 2) >> 2, bar = 1 + group;
+    const int set = G::SETS == 2 ? group : 0, cg = G::SETS == 2 ? 0 : group;
     const int token = quarter * 32 + lane, c_group = cg * G::CH * CW;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    const bool leader = warp == 2 && lane == 0;
+    const bool leader = ((warp - 2) & 3) == 0 && lane == 0;  // of the group
+    uint8_t *const sp_set = sp + set * G::P_SET;
+    float *const nm = ctl->nm + set * 64;
+    int *const top = ctl->top + set * 64;
+    const uint32_t tmem_set = tmem_o + set * 2 * NT;
     // P[token][column]: 64-column halves; 16-byte chunk c of a row lies at
     // c ^ (token & 7)
     auto p_at = [&](int col) -> uint4 * {
-      return reinterpret_cast<uint4 *>(sp + (col / 64) * HALF_BYTES + token * 128 +
+      return reinterpret_cast<uint4 *>(sp_set + (col / 64) * HALF_BYTES + token * 128 +
                                        (((col % 64) / 8) ^ (token & 7)) * 16);
     };
     // the column sums' meeting place: the columns' own chunks of P rows 0, 8, ..
     auto sum_slot = [&](int c0, int q, int j) -> float * {
-      return reinterpret_cast<float *>(sp + (c0 / 64) * HALF_BYTES + 8 * (q * 2 + j / 16) * 128 +
-                                       (c0 % 64) * 2) + j % 16;
+      constexpr int PER = CW / 2;  // in a row's bytes
+      return reinterpret_cast<float *>(sp_set + (c0 / 64) * HALF_BYTES +
+                                       8 * (q * 2 + j / PER) * 128 + (c0 % 64) * 2) + j % PER;
     };
-    uint32_t t = 0, seg = 0, v_slot = 1, v_phase = 0, q_loads = 0;
+    uint32_t t0 = 0, seg = 0;   // the segment's first tile, of all of the share's
+    uint32_t mine = 0;          // tiles that this set has taken
+    uint32_t uses[2] = {0, 0}, helped[2] = {0, 0};  // segments that a set had part in; as first
+    int q_last = -1;            // the last segment whose Q this thread has copied
     bool ok = true, gone = false;
     auto segment_here = [&](uint32_t i) {
       return wait(&ctl->seg_full[i % SEGS], (i / SEGS) & 1, abort);
@@ -631,12 +663,9 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       for (int c = 0; c < HALVES; ++c)
         tc::tma_load_3d(sq + c * NT * 128, &tma_q, c * 64, n->h * a.group, n->row0 + n->node0,
                         &ctl->q_full, tc::policy_evict_normal());
-      ++q_loads;
+      q_last = (int)i;
     };
-    if (leader) {
-      a.desc[cta * 8] = 0;
-      load_q(0);
-    }
+    if (leader && group == 0) load_q(0);
     __syncwarp();
     for (;;) {
       ok = ok && __all_sync(0xffffffffu, segment_here(seg));
@@ -646,6 +675,9 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       const float ks = a.k_scale ? a.k_scale[s.h] : 1.0f;
       const float c = a.scale * ks * LOG2E;
       const int rows = s.nodes * a.group;  // columns in use
+      const int n_tiles = s.te - s.tb;
+      const int first = G::SETS == 2 ? (set ^ t0) & 1 : 0;  // this set's tiles: every SETS-th
+      const bool part = first < n_tiles;
       // lane j: the ancestor mask of each chunk's column j
       unsigned long long word[G::CH];
 #pragma unroll
@@ -659,11 +691,10 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         }
         if (quarter == 0 && lane < CW) {
           // a column that no row uses has no weight and calls for nothing
-          ctl->nm[col] = col < rows ? 0.0f : -INFINITY;
-          ctl->top[col] = order_key(-INFINITY);
+          nm[col] = col < rows ? 0.0f : -INFINITY;
+          top[col] = order_key(-INFINITY);
         }
       }
-      if (leader) ctl->odd[(seg + 1) % 3] = 0;
       group_sync(bar);
       float l[G::CH][CW];
 #pragma unroll
@@ -678,13 +709,14 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         unset[ch] = n == 32 ? ~0u : (1u << n) - 1;
       }
 
-      for (int tile = s.tb; tile < s.te; ++tile, ++t) {
-        const uint32_t b = t & 1;
+      for (int k = first; k < n_tiles; k += G::SETS, ++mine) {
+        const int tile = s.tb + k;
+        const uint32_t t = t0 + k, b = t & 1;
         ok = ok && warp_wait(&ctl->s_full[b], (t >> 1) & 1, abort);
-        if (tile == s.te - 1 && leader && ok) load_q(seg + 1);
+        if (k == n_tiles - 1 && leader && cg == 0 && ok) load_q(seg + 1);
         const int pos = tile * BT + token;
         const bool edge = tile * BT + BT > s.ctx;  // some token is a node or past the end
-        bool waited = t == 0;
+        bool waited = mine == 0;
         tc::fence_after_sync();
 #pragma unroll
         for (int ch = 0; ch < G::CH; ++ch) {
@@ -715,11 +747,11 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
                 tc::reg_fence(sr);
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
-                  const float4 nm = *reinterpret_cast<const float4 *>(&ctl->nm[c0 + h + j]);
-                  e[h + j] = fmaf(__uint_as_float(sr[j]), c, nm.x);
-                  e[h + j + 1] = fmaf(__uint_as_float(sr[j + 1]), c, nm.y);
-                  e[h + j + 2] = fmaf(__uint_as_float(sr[j + 2]), c, nm.z);
-                  e[h + j + 3] = fmaf(__uint_as_float(sr[j + 3]), c, nm.w);
+                  const float4 m = *reinterpret_cast<const float4 *>(&nm[c0 + h + j]);
+                  e[h + j] = fmaf(__uint_as_float(sr[j]), c, m.x);
+                  e[h + j + 1] = fmaf(__uint_as_float(sr[j + 1]), c, m.y);
+                  e[h + j + 2] = fmaf(__uint_as_float(sr[j + 2]), c, m.z);
+                  e[h + j + 3] = fmaf(__uint_as_float(sr[j + 3]), c, m.w);
                 }
               }
               if (edge) {
@@ -736,23 +768,23 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
             }
             // by how much the tile passes each reference: lane j for column j
             const float peak = column_max<CW>(e, lane);
-            if (lane < CW) atomicMax(&ctl->top[c0 + lane], order_key(peak));
-            if (!waited) ok = warp_wait(&ctl->pv_done, (t - 1) & 1, abort);
+            if (lane < CW) atomicMax(&top[c0 + lane], order_key(peak));
+            if (!waited) ok = warp_wait(&ctl->pv_done[set], (mine - 1) & 1, abort);
             waited = true;
             group_sync(bar);
-            float raise = order_value(ctl->top[c0 + lane % CW]);
+            float raise = order_value(top[c0 + lane % CW]);
             const bool fresh = unset[ch] >> (lane % CW) & 1;
             if (!(raise > -INFINITY) || (!fresh && raise < 0.0f)) raise = 0.0f;
-            unset[ch] &= __ballot_sync(0xffffffffu, lane < CW && ctl->top[c0 + lane % CW] ==
+            unset[ch] &= __ballot_sync(0xffffffffu, lane < CW && top[c0 + lane % CW] ==
                                                                      order_key(-INFINITY));
-            if (tile != s.tb && ok) {  // what is summed so far, to the new references
+            if (k != first && ok) {  // what is summed so far, to the new references
               tc::fence_after_sync();
               const float keep = fresh ? 1.0f : ex2_fast(-raise);
 #pragma unroll
               for (int j = 0; j < CW; ++j) l[ch][j] *= __shfl_sync(0xffffffffu, keep, j);
 #pragma unroll 1
               for (int h = 0; h < 2 * CW; h += 16) {
-                const uint32_t at = tmem_o + lanes + (h < CW ? 0 : NT - CW) + c0 + h;
+                const uint32_t at = tmem_set + lanes + (h < CW ? 0 : NT - CW) + c0 + h;
                 uint32_t o[16];
                 tc::tmem_ld16(at, o);
                 tc::tmem_wait_ld();
@@ -767,8 +799,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
             }
             group_sync(bar);
             if (quarter == 0 && lane < CW) {
-              ctl->nm[c0 + lane] -= raise;
-              ctl->top[c0 + lane] = order_key(-INFINITY);
+              nm[c0 + lane] -= raise;
+              top[c0 + lane] = order_key(-INFINITY);
             }
             group_sync(bar);
           }
@@ -788,7 +820,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
             e[j] = __uint_as_float(hi);
             e[j + 1] = __uint_as_float(pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi)));
           }
-          if (!waited) ok = warp_wait(&ctl->pv_done, (t - 1) & 1, abort);  // P is free
+          if (!waited) ok = warp_wait(&ctl->pv_done[set], (mine - 1) & 1, abort);  // P is free
           waited = true;
 #pragma unroll
           for (int j = 0; j < CW; j += 8) {
@@ -804,8 +836,9 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           // What a row does not see must not meet its zero weight as infinity or
           // NaN: V past the end is cleared, and so are the nodes' non-finite
           // values, which the epilogue gives to the rows that do see them.
-          ok = ok && warp_wait(&ctl->full[v_slot], v_phase, abort);
-          uint8_t *row = slots + v_slot * G::SLOT + token * 128;
+          const uint32_t fill = 2 * t + 1;
+          ok = ok && warp_wait(&ctl->full[fill % SLOTS], (fill / SLOTS) & 1, abort);
+          uint8_t *row = slots + fill % SLOTS * G::SLOT + token * 128;
           if (ok && pos >= s.ctx) {
 #pragma unroll 1
             for (int i = cg; i < HALVES * 8; i += CG) {
@@ -824,69 +857,95 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
               }
               if (odd) {
                 *x = y;
-                atomicOr(&ctl->odd[seg % 3], 1ull << (pos - s.ctx));
+                atomicOr(&ctl->odd[seg & 3], 1ull << (pos - s.ctx));
               }
             }
           }
         }
         tc::fence_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&ctl->p_full);
-        v_slot += 2;
-        if (v_slot >= SLOTS) {
-          v_slot -= SLOTS;
-          v_phase ^= 1;
-        }
+        if (lane == 0) tc::mbar_arrive(&ctl->p_full[set]);
       }
       if (gone) break;
 
       // ------------------------------------------------- end of a segment ----
-      ok = ok && warp_wait(&ctl->pv_done, (t - 1) & 1, abort);
+      // The set with the segment's last tile takes both sets' sums and O together.
+      const int other = set ^ 1;
+      const bool last = ((t0 + n_tiles - 1 - set) & (G::SETS - 1)) == 0;
+      const bool both = G::SETS == 2 && n_tiles > 1;
+      if (part) {
+        ok = ok && warp_wait(&ctl->pv_done[set], (mine - 1) & 1, abort);
 #pragma unroll
-      for (int ch = 0; ch < G::CH; ++ch) {
-        const float part = column_sums<CW>(l[ch], lane);
-        if (ok && lane < CW) *sum_slot(c_group + ch * CW, quarter, lane) = part;
+        for (int ch = 0; ch < G::CH; ++ch) {
+          const float sums = column_sums<CW>(l[ch], lane);
+          if (ok && lane < CW) *sum_slot(c_group + ch * CW, quarter, lane) = sums;
+        }
+        // `other` is free once its last reader has given this set's O back
+        if (!last && uses[set]) ok = ok && warp_wait(&ctl->o_free[set], (uses[set] - 1) & 1, abort);
+        if (last && both) {
+          const uint32_t theirs = (t0 + n_tiles + (other ^ 1)) / 2;  // tiles of the other set
+          ok = ok && warp_wait(&ctl->half[other], helped[other] & 1, abort) &&
+               warp_wait(&ctl->pv_done[other], (theirs - 1) & 1, abort);
+        }
+        if (group_any(bar, !ok)) {
+          gone = true;
+          break;
+        }
+        tc::fence_after_sync();
       }
-      if (group_any(bar, !ok)) {
-        gone = true;
-        break;
-      }
-      tc::fence_after_sync();
-      const float vs = a.v_scale ? a.v_scale[s.h] : 1.0f;
-      const unsigned long long odd = ctl->odd[seg % 3];
       const bool whole = s.tb == 0 && s.te == s.tiles;
       const int piece = s.tb == 0 ? 1 : 0;
       const int here = min(max(rows - c_group, 0), G::CH * CW);  // the group's columns in use
-      float sum[G::CH];
-#pragma unroll
-      for (int ch = 0; ch < G::CH; ++ch) {
-        const int c0 = c_group + ch * CW;
-        sum[ch] = 0.0f;
-        if (lane < CW)
-          sum[ch] = (*sum_slot(c0, 0, lane) + *sum_slot(c0, 1, lane)) +
-                    (*sum_slot(c0, 2, lane) + *sum_slot(c0, 3, lane));
-      }
-      if (quarter == 0 && lane < CW) {
+      if (part && quarter == 0 && lane < CW) {
+        const float vs = a.v_scale ? a.v_scale[s.h] : 1.0f;
 #pragma unroll
         for (int ch = 0; ch < G::CH; ++ch) {
-          const int col = c_group + ch * CW + lane;
+          const int c0 = c_group + ch * CW, col = c0 + lane;
           if (col >= rows) continue;
+          float sum = (*sum_slot(c0, 0, lane) + *sum_slot(c0, 1, lane)) +
+                      (*sum_slot(c0, 2, lane) + *sum_slot(c0, 3, lane));
+          float ref = unset[ch] >> lane & 1 ? -INFINITY : -nm[col];
+          if (!last) {
+            ctl->other[0][col] = ref;
+            ctl->other[1][col] = sum;
+            continue;
+          }
+          float mine_w = 1.0f, their_w = 0.0f;
+          if (both) {
+            const float their_ref = ctl->other[0][col], to = fmaxf(ref, their_ref);
+            mine_w = ref == -INFINITY ? 0.0f : ex2_fast(ref - to);
+            their_w = their_ref == -INFINITY ? 0.0f : ex2_fast(their_ref - to);
+            sum = mine_w * sum + their_w * ctl->other[1][col];
+            ref = to;
+          }
           const bool sees = s.ctx > 0 || word[ch] != 0;
-          const float ref = unset[ch] >> lane & 1 ? -INFINITY : -ctl->nm[col];
+          float f = 1.0f;
           if (!whole) {
             float *ml = a.part_ml + (size_t)(cta * 2 + piece) * 2 * NT + col;
             ml[0] = ref;
-            ml[NT] = sum[ch];
-          } else if (a.lse) {
-            const int node = col / a.group, head = s.h * a.group + col - node * a.group;
-            a.lse[(size_t)(s.row0 + s.node0 + node) * a.heads * a.group + head] =
-                sees ? (ref + log2f(sum[ch])) * LN2 : -INFINITY;
+            ml[NT] = sum;
+          } else {
+            f = sees ? vs / sum : 0.0f;
+            if (a.lse) {
+              const int node = col / a.group, head = s.h * a.group + col - node * a.group;
+              a.lse[(size_t)(s.row0 + s.node0 + node) * a.heads * a.group + head] =
+                  sees ? (ref + log2f(sum)) * LN2 : -INFINITY;
+            }
           }
-          ctl->nm[col] = sees ? vs / sum[ch] : 0.0f;  // the rows' factors
+          nm[col] = mine_w * f;  // the factors of both O
+          if (G::SETS == 2) ctl->other[1][col] = their_w * f;
         }
       }
-      group_sync(bar);
-      if (quarter * 32 < D) {
+      if (part && !last) {
+        __syncwarp();
+        if (quarter == 0 && lane == 0) tc::mbar_arrive(&ctl->half[set]);
+      }
+      const unsigned long long odd = last ? ctl->odd[seg & 3] : 0;
+      if (last) {
+        group_sync(bar);
+        if (G::SETS == 2 ? leader : leader && group == 0) ctl->odd[(seg + (G::SETS == 2 ? 0 : 2)) & 3] = 0;
+      }
+      if (last && quarter * 32 < D) {
         const int d = token;  // accumulator lane = column of the head
         int g = c_group % a.group;
         bf16 *dst = a.out + (s.row0 + s.node0 + c_group / a.group) * a.out_row +
@@ -895,15 +954,23 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         float *po = a.part_o + ((size_t)(cta * 2 + piece) * NT + c_group) * D + d;
 #pragma unroll 1
         for (int j = 0; j < here; j += 16) {
-          uint32_t o[16], o_lo[16];
-          tc::tmem_ld16(tmem_o + lanes + c_group + j, o);
-          tc::tmem_ld16(tmem_o + lanes + NT + c_group + j, o_lo);
-          tc::tmem_wait_ld();
-          tc::reg_fence(o);
-          tc::reg_fence(o_lo);
           float x[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(o[i]) + __uint_as_float(o_lo[i]);
+          for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+#pragma unroll 1
+          for (int y = 0; y < (both ? 2 : 1); ++y) {  // this set's O, and the other's
+            const int from = y ? other : set;
+            const float *f = y ? ctl->other[1] : nm;
+            uint32_t o[16], o_lo[16];
+            tc::tmem_ld16(tmem_o + from * 2 * NT + lanes + c_group + j, o);
+            tc::tmem_ld16(tmem_o + from * 2 * NT + lanes + NT + c_group + j, o_lo);
+            tc::tmem_wait_ld();
+            tc::reg_fence(o);
+            tc::reg_fence(o_lo);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              x[i] = fmaf(__uint_as_float(o[i]) + __uint_as_float(o_lo[i]), f[c_group + j + i], x[i]);
+          }
 #pragma unroll 1
           for (unsigned long long m = odd; m; m &= m - 1) {
             const int at = __ffsll((long long)m) - 1, pos = s.ctx + at;
@@ -937,7 +1004,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           }
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            if (j + i < here) *dst = __float2bfloat16_rn(x[i] * ctl->nm[c_group + j + i]);
+            if (j + i < here) *dst = __float2bfloat16_rn(x[i]);
             dst += a.out_head;
             if (++g == a.group) {
               g = 0;
@@ -946,7 +1013,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           }
         }
       }
-      if (leader && !whole && piece == 1) {
+      if (last && leader && group == set && !whole && piece == 1) {
         // the item goes on in the CTAs up to the one that holds its last unit
         const long long end = u1 + (s.tiles - s.te);
         int *desc = a.desc + cta * 8;
@@ -957,14 +1024,24 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         const long long u = end - 1, split = longer * (share + 1);
         desc[0] = (int)(u < split ? divide(u, share + 1) : longer + divide(u - split, share)) -
                   cta + 1;
+        *(volatile int *)&ctl->tail = 1;
       }
+      tc::fence_before_sync();
       __syncwarp();
+      if (G::SETS == 2 && last && lane == 0) {  // both O are read
+        tc::mbar_arrive(&ctl->o_free[set]);
+        if (both) tc::mbar_arrive(&ctl->o_free[other]);
+      }
       if (quarter == 0 && lane == 0) tc::mbar_arrive(&ctl->seg_empty[seg % SEGS]);
+      uses[set] += part;
+      uses[other] += both || !part;
+      helped[other] += last && both;
+      t0 += n_tiles;
       ++seg;
     }
-    if (leader && q_loads) {  // a Q copy still in flight lands before the CTA ends
+    if (leader && gone && q_last >= 0) {  // a Q copy still in flight lands before the CTA ends
       volatile int never = 0;
-      tc::mbar_wait(&ctl->q_full, (q_loads - 1) & 1, &never);
+      tc::mbar_wait(&ctl->q_full, q_last & 1, &never);
     }
     __syncwarp();
   } else if constexpr (G::FP8) {
@@ -1020,7 +1097,10 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
 
   tc::fence_before_sync();
   __syncthreads();
-  if (ctl->abort && threadIdx.x == 0) dspark_set_status(DSPARK_ERR_TIMEOUT);
+  if (threadIdx.x == 0) {
+    if (ctl->abort) dspark_set_status(DSPARK_ERR_TIMEOUT);
+    if (!ctl->tail) a.desc[cta * 8] = 0;
+  }
   if (warp == 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, G::TMEM_COLS);
