@@ -50,7 +50,7 @@ constexpr int MAX_SLOTS = 12;
 constexpr int SEGS = 8;
 // What beginning and ending an item costs a CTA, in tiles (measured: about one
 // tile's time at 32 columns); counted so that short contexts balance too.
-constexpr int ITEM_UNITS = 1;
+constexpr int ITEM_UNITS = 2;
 // log2: how far scores may pass the reference.  Weights, their sum and O are
 // floating-point numbers of f32's range, so nothing is lost below 2^32.
 constexpr float RAISE = 32.0f;
@@ -88,7 +88,9 @@ struct Geo {
   static constexpr int CV = FP8 ? 4 : 0;
   static constexpr int THREADS = 32 * (2 + SW + CV);
   static constexpr int SLOT = BT * D * 2;
-  static constexpr int Q_BYTES = NT * D * 2;
+  // Q of the next segment beside the present one's, where two sets leave room
+  static constexpr int QS = SETS;
+  static constexpr int Q_ONE = NT * D * 2, Q_BYTES = QS * Q_ONE;
   static constexpr int P_SET = BT * 128 * (NT > 32 ? NT / 32 : 1);
   static constexpr int P_BYTES = SETS * P_SET;
   static constexpr int ROOM = SMEM_LIMIT - CTL_BYTES - Q_BYTES - P_BYTES;
@@ -117,7 +119,7 @@ __device__ __forceinline__ float order_value(int k) {
 // A request as the kernel takes it: every later index is in bounds by this.
 struct Request {
   int row0, n, ctx, total, tiles, row_tiles;
-  __device__ __noinline__ bool set(const Args &a, int c, int start, int end) {
+  __device__ __forceinline__ bool set(const Args &a, int c, int start, int end) {
     bool ok = true;
     row0 = min(max(start, 0), a.n_rows);
     n = min(max(end, row0), a.n_rows) - row0;
@@ -145,7 +147,8 @@ struct Request {
 
 // One CTA's consecutive tiles of one item; none (tb == te): the end of its share.
 struct Segment {
-  int r, row0, n, ctx, total, tiles, h, node0, nodes, tb, te, unused;
+  int r, row0, n, ctx, total, tiles, h, node0, nodes, tb, te;
+  float c;  // log2(e) * scale (* the head's K scale)
 };
 
 // Where the copying warp stands in its CTA's share of the list of units.
@@ -153,52 +156,57 @@ struct Walker {
   int r, h, rt, tile, over, next_ctx, next_end, end;  // over: own units of the item left
   long long pos, last;  // the next unit, and the end of the share
   Request q;
-  __device__ __forceinline__ void ahead(const Args &a) {  // the next request's lengths
+  float scale;            // of K in head h
+  // What the next request and head need, read before it is needed.
+  __device__ __forceinline__ void ahead(const Args &a) {
     if (r + 1 < a.R) {
       next_ctx = a.ctx[r + 1];
       next_end = a.row_start[r + 2];
     }
   }
+  __device__ __forceinline__ void ahead_head(const Args &a) {
+    scale = a.k_scale ? a.k_scale[h == a.heads ? 0 : h] : 1.0f;
+  }
 };
 
-__device__ __forceinline__ bool next_segment(Walker *w, Segment *s, const Args *a) {
-  w->pos += w->over;
-  w->over = 0;
-  if (w->pos >= w->last) return false;
-  if (w->h == a->heads) {
-    w->h = 0;
+__device__ __forceinline__ bool next_segment(Walker &w, Segment &s, const Args &a) {
+  w.pos += w.over;
+  w.over = 0;
+  if (w.pos >= w.last) return false;
+  if (w.h == a.heads) {
+    w.h = 0;
     do {
-      if (++w->r >= a->R) {
-        w->pos = w->last;
+      if (++w.r >= a.R) {
+        w.pos = w.last;
         return false;
       }
-      const int start = w->end;
-      w->end = w->next_end;
-      w->q.set(*a, w->next_ctx, start, w->end);
-      w->ahead(*a);
-    } while (w->q.n == 0);
+      const int start = w.end;
+      w.end = w.next_end;
+      w.q.set(a, w.next_ctx, start, w.end);
+      w.ahead(a);
+    } while (w.q.n == 0);
   }
-  const Request q = w->q;
-  s->r = w->r;
-  s->row0 = q.row0;
-  s->n = q.n;
-  s->ctx = q.ctx;
-  s->total = q.total;
-  s->tiles = q.tiles;
-  s->h = w->h;
-  s->node0 = w->rt * a->nodes_tile;
-  s->nodes = min(a->nodes_tile, q.n - s->node0);
-  const int tb = w->tile, te = (int)min((long long)q.tiles, tb + (w->last - w->pos));
-  s->tb = tb;
-  s->te = te;
-  w->pos += te - tb;
-  w->tile = te;
-  if (te == q.tiles) {
-    w->tile = 0;
-    w->over = ITEM_UNITS;
-    if (++w->rt == q.row_tiles) {
-      w->rt = 0;
-      ++w->h;
+  s.r = w.r;
+  s.row0 = w.q.row0;
+  s.n = w.q.n;
+  s.ctx = w.q.ctx;
+  s.total = w.q.total;
+  s.tiles = w.q.tiles;
+  s.h = w.h;
+  s.node0 = w.rt * a.nodes_tile;
+  s.nodes = min(a.nodes_tile, w.q.n - s.node0);
+  s.c = a.scale * LOG2E * w.scale;
+  s.tb = w.tile;
+  s.te = (int)min((long long)w.q.tiles, w.tile + (w.last - w.pos));
+  w.pos += s.te - s.tb;
+  w.tile = s.te;
+  if (s.te == w.q.tiles) {
+    w.tile = 0;
+    w.over = ITEM_UNITS;
+    if (++w.rt == w.q.row_tiles) {
+      w.rt = 0;
+      ++w.h;
+      w.ahead_head(a);
     }
   }
   return true;
@@ -212,7 +220,7 @@ __device__ __noinline__ long long divide(long long x, long long y) {
 
 struct Ctl {
   uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], rfull[MAX_SLOTS], rempty[MAX_SLOTS];
-  uint64_t q_full, s_full[2], s_empty[2], drain;
+  uint64_t q_full[2], s_full[2], s_empty[2], drain;
   // by set: P written, its product done, O read by the segment's last set, and the
   // other's sums ready for it
   uint64_t p_full[2], pv_done[2], o_free[2], half[2];
@@ -227,6 +235,7 @@ struct Ctl {
   uint64_t seg_full[SEGS], seg_empty[SEGS];
   int raw_end;            // 8-bit: fills of the raw ring
   unsigned long long odd[4];  // nodes with non-finite V, by segment mod 4
+  int fresh[2];           // of a group: its first references are still to be raised
   int tail;               // the CTA leaves an item to its successors
   int abort;
   uint32_t tmem;
@@ -333,7 +342,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
   uint8_t *sp = sq + G::Q_BYTES;
   Ctl *ctl = reinterpret_cast<Ctl *>(sp + G::P_BYTES);
   volatile int *abort = &ctl->abort;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
 
   if (threadIdx.x == 0) {
@@ -347,8 +356,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       tc::mbar_init(&ctl->rfull[s], 1);
       tc::mbar_init(&ctl->rempty[s], G::CV);
     }
-    tc::mbar_init(&ctl->q_full, 1);
     for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(&ctl->q_full[b], 1);
       tc::mbar_init(&ctl->s_full[b], 1);
       tc::mbar_init(&ctl->s_empty[b], 4 * CG);
       tc::mbar_init(&ctl->p_full[b], 4 * CG);
@@ -438,6 +447,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     walk0->pos = u0;
     walk0->last = u1;
     walk0->ahead(a);
+    walk0->ahead_head(a);
   }
   __syncthreads();
   const uint32_t tmem = ctl->tmem, tmem_o = tmem + 2 * NT;
@@ -456,35 +466,45 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     int slot = 0, fills = 0;
     uint32_t phase = 0, used = 0;
     bool ok = true;
-    // Segments are published one ahead of the copies, so that a role that needs the
-    // next one never waits for room in the ring.
+    // Segments are published ahead of the copies, so that a role that needs a later
+    // one never waits for room in the ring.
+    constexpr int AHEAD = 2;
+    Walker walk = ctl->walk;  // by every lane alike: what it reads ahead stays in flight
     int published = 0;
     auto publish = [&]() {
       const int i = published % SEGS;
       ok = ok && warp_wait(&ctl->seg_empty[i], ((published / SEGS) & 1) ^ 1, abort);
+      Segment n;
+      if (!next_segment(walk, n, a)) n.tb = n.te = n.r = n.total = 0;
       if (ok && lane == 0) {
-        if (!next_segment(&ctl->walk, &ctl->seg[i], &a)) ctl->seg[i].tb = ctl->seg[i].te = 0;
+        ctl->seg[i] = n;
         tc::mbar_arrive(&ctl->seg_full[i]);
       }
       __syncwarp();
       ++published;
     };
+    // the page of box `lane` of a segment's tile; none past the request's end
+    auto page_of = [&](const Segment &s, int tile) {
+      const int p = tile * BT + lane * rows;
+      return lane < boxes && p < s.total
+                 ? a.block_table[(size_t)s.r * a.max_pages + (p >> a.page_shift)]
+                 : 0;
+    };
+    int page = 0, next_page = 0;  // of this tile; of the next segment's first one
     while (ok) {
 #pragma unroll 1
-      for (int k = published ? 1 : 2; k; --k) publish();
-      const Segment s = ctl->seg[(published - 2) % SEGS];
+      for (int k = published ? 1 : AHEAD + 1; k; --k) publish();
+      const Segment s = ctl->seg[(published - 1 - AHEAD) % SEGS];
       if (s.tb == s.te) break;
-      const int *table = a.block_table + (size_t)s.r * a.max_pages;
-      // the page of box `lane` of a tile; none past the request's end
-      auto page_of = [&](int tile) {
-        const int p = tile * BT + lane * rows;
-        return lane < boxes && p < s.total ? table[p >> a.page_shift] : 0;
-      };
-      int page = page_of(s.tb);
+      page = published == AHEAD + 1 ? page_of(s, s.tb) : next_page;
+      {
+        const Segment &n = ctl->seg[(published - AHEAD) % SEGS];
+        next_page = page_of(n, n.tb);
+      }
       for (int tile = s.tb; ok && tile < s.te; ++tile) {
         const int here = page, p = tile * BT + lane * rows;
         const bool mine = lane < boxes && p < s.total;
-        if (tile + 1 < s.te) page = page_of(tile + 1);
+        if (tile + 1 < s.te) page = page_of(s, tile + 1);
         const int n_boxes = __popc(__ballot_sync(0xffffffffu, mine));
         const bool in = here >= 0 && here < a.n_pages;
         if (mine && !in) dspark_set_status(DSPARK_ERR_PAGES);
@@ -532,7 +552,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     }
   } else if (warp == 1) {
     // -------------------------------------------------------- MMA issuer ----
-    if (lane == 0) {
+    {
       constexpr uint32_t idesc_s = tc::idesc_bf16(BT, NT);
       constexpr uint32_t idesc_o = tc::idesc_bf16(128, 2 * NT) | tc::IDESC_A_MN | tc::IDESC_B_MN;
       int k_slot = 0, v_slot = 1;
@@ -551,14 +571,17 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       // last product must not wait for the next one's Q.
       bool ok = true, first = true, more = true;
       int tile = 0, te = 0, place = 0;  // place: of the tile in its segment
+      int total = 0, tokens = 0;        // of the request; from the pending tile on
       for (bool pending = false; ok && (more || pending);) {
         if (more && first && !pending) {  // the next segment
           const int i = seg % SEGS;
-          ok = wait(&ctl->seg_full[i], (seg / SEGS) & 1, abort);
+          ok = warp_wait(&ctl->seg_full[i], (seg / SEGS) & 1, abort);
           if (!ok) break;
           tile = ctl->seg[i].tb;
           te = ctl->seg[i].te;
-          tc::mbar_arrive(&ctl->seg_empty[i]);
+          total = ctl->seg[i].total;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&ctl->seg_empty[i]);
           more = tile < te;
           if (!more) break;
           place = 0;
@@ -566,28 +589,28 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         const bool issue = more && (!first || !pending);
         if (issue) {
           const uint32_t b = t & 1;
-          ok = (!first || wait(&ctl->q_full, seg & 1, abort)) &&
-               wait(&ctl->full[k_slot], k_phase, abort) &&
-               wait(&ctl->s_empty[b], ((t >> 1) & 1) ^ 1, abort);
+          ok = (!first || warp_wait(&ctl->q_full[seg % G::QS], (seg / G::QS) & 1, abort)) &&
+               warp_wait(&ctl->full[k_slot], k_phase, abort) &&
+               warp_wait(&ctl->s_empty[b], ((t >> 1) & 1) ^ 1, abort);
           if (!ok) break;
           tc::fence_after_sync();
           const uint64_t kd = tc::smem_desc_sw128(slots + k_slot * G::SLOT);
-          const uint64_t qd = tc::smem_desc_sw128(sq);
+          const uint64_t qd = tc::smem_desc_sw128(sq + seg % G::QS * G::Q_ONE);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            tc::umma_bf16(tmem + b * NT, kd + (k / 4) * (HALF_BYTES / 16) + 2 * (k & 3),
+            tc::umma_bf16_warp(tmem + b * NT, kd + (k / 4) * (HALF_BYTES / 16) + 2 * (k & 3),
                           qd + (k / 4) * (NT * 128 / 16) + 2 * (k & 3), idesc_s, k != 0);
-          tc::umma_commit(&ctl->empty[k_slot]);
-          tc::umma_commit(&ctl->s_full[b]);
+          tc::umma_commit_warp(&ctl->empty[k_slot]);
+          tc::umma_commit_warp(&ctl->s_full[b]);
           advance(k_slot, k_phase);
           ++t;
         }
         if (pending) {  // the product before
           const int x = G::SETS == 2 ? pv & 1 : 0;
-          ok = wait(&ctl->full[v_slot], v_phase, abort) &&
-               wait(&ctl->p_full[x], (pv / G::SETS) & 1, abort);
+          ok = warp_wait(&ctl->full[v_slot], v_phase, abort) &&
+               warp_wait(&ctl->p_full[x], (pv / G::SETS) & 1, abort);
           if (ok && G::SETS == 2 && !acc) {  // a segment's first: its last O there is read
-            ok = uses[x] == 0 || wait(&ctl->o_free[x], (uses[x] - 1) & 1, abort);
+            ok = uses[x] == 0 || warp_wait(&ctl->o_free[x], (uses[x] - 1) & 1, abort);
             ++uses[x];
           }
           if (!ok) break;
@@ -599,9 +622,11 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           const uint64_t pd = tc::smem_desc_sw128_mn(sp + x * G::P_SET, HALF_BYTES);
 #pragma unroll
           for (int k = 0; k < BT / 16; ++k)
-            tc::umma_bf16(tmem_o + x * 2 * NT, vd + 128 * k, pd + 128 * k, idesc_o, acc | (k != 0));
-          tc::umma_commit(&ctl->empty[v_slot]);
-          tc::umma_commit(&ctl->pv_done[x]);
+            if (k * 16 < tokens)  // of the 16 tokens of a step, some may be past the end
+              tc::umma_bf16_warp(tmem_o + x * 2 * NT, vd + 128 * k, pd + 128 * k, idesc_o,
+                                 acc | (k != 0));
+          tc::umma_commit_warp(&ctl->empty[v_slot]);
+          tc::umma_commit_warp(&ctl->pv_done[x]);
           advance(v_slot, v_phase);
           ++pv;
           pending = false;
@@ -609,6 +634,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         if (issue) {
           pending = true;
           acc = place >= G::SETS;  // the pending tile adds to what its set has
+          tokens = total - tile * BT;
           ++place;
           first = false;
           if (++tile == te) {
@@ -617,9 +643,9 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           }
         }
       }
-      tc::umma_commit(&ctl->drain);  // all MMAs issued have finished
+      tc::umma_commit_warp(&ctl->drain);  // all MMAs issued have finished
       volatile int never = 0;
-      tc::mbar_wait(&ctl->drain, 0, &never);
+      warp_wait(&ctl->drain, 0, &never);
     }
     __syncwarp();
   } else if (warp < 2 + G::SW) {
@@ -653,27 +679,30 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     auto segment_here = [&](uint32_t i) {
       return wait(&ctl->seg_full[i % SEGS], (i / SEGS) & 1, abort);
     };
-    // Q of segment i, by the leader: its place is free once the products with the
-    // last one's are done
+    // Q of segment i, by the leader of the set that sees the last product with what
+    // lies in its place done
     auto load_q = [&](uint32_t i) {
       if (!segment_here(i)) return;
       const Segment *n = &ctl->seg[i % SEGS];
       if (n->tb == n->te) return;
-      tc::mbar_expect_tx(&ctl->q_full, HALVES * a.nodes_tile * a.group * 128);
+      uint64_t *full = &ctl->q_full[i % G::QS];
+      tc::mbar_expect_tx(full, HALVES * a.nodes_tile * a.group * 128);
       for (int c = 0; c < HALVES; ++c)
-        tc::tma_load_3d(sq + c * NT * 128, &tma_q, c * 64, n->h * a.group, n->row0 + n->node0,
-                        &ctl->q_full, tc::policy_evict_normal());
+        tc::tma_load_3d(sq + i % G::QS * G::Q_ONE + c * NT * 128, &tma_q, c * 64, n->h * a.group,
+                        n->row0 + n->node0, full, tc::policy_evict_normal());
       q_last = (int)i;
     };
-    if (leader && group == 0) load_q(0);
+    if (leader && group == 0) {
+      load_q(0);
+      if (G::QS == 2 && ctl->seg[0].tb != ctl->seg[0].te) load_q(1);
+    }
     __syncwarp();
     for (;;) {
       ok = ok && __all_sync(0xffffffffu, segment_here(seg));
       if (group_any(bar, !ok)) break;
       const Segment s = ctl->seg[seg % SEGS];
       if (s.tb == s.te) break;
-      const float ks = a.k_scale ? a.k_scale[s.h] : 1.0f;
-      const float c = a.scale * ks * LOG2E;
+      const float c = s.c;
       const int rows = s.nodes * a.group;  // columns in use
       const int n_tiles = s.te - s.tb;
       const int first = G::SETS == 2 ? (set ^ t0) & 1 : 0;  // this set's tiles: every SETS-th
@@ -687,7 +716,6 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         if (lane < CW && col < rows) {
           const int node = s.node0 + col / a.group;
           word[ch] = a.anc ? a.anc[s.row0 + node] : (2ull << node) - 1;
-          if (s.n < 64) word[ch] &= (1ull << s.n) - 1;
         }
         if (quarter == 0 && lane < CW) {
           // a column that no row uses has no weight and calls for nothing
@@ -713,11 +741,50 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         const int tile = s.tb + k;
         const uint32_t t = t0 + k, b = t & 1;
         ok = ok && warp_wait(&ctl->s_full[b], (t >> 1) & 1, abort);
-        if (k == n_tiles - 1 && leader && cg == 0 && ok) load_q(seg + 1);
+        if (k == n_tiles - 1 && leader && cg == 0 && ok) load_q(seg + G::QS);
         const int pos = tile * BT + token;
         const bool edge = tile * BT + BT > s.ctx;  // some token is a node or past the end
         bool waited = mine == 0;
         tc::fence_after_sync();
+        if (k == first && tile * BT < s.ctx) {
+          // The first references: the scores of the tile's first token, which every
+          // row sees, so that no column's maximum lies below its reference; one
+          // that lies far above it raises it.
+          if (quarter == 0 && ok) {
+            float sum = 0.0f;  // stays 0 unless one is infinite or NaN
+#pragma unroll
+            for (int h = 0; h < G::CH * CW; h += 16) {
+              uint32_t sr[16];
+              tc::tmem_ld16(tmem + lanes + b * NT + c_group + h, sr);
+              tc::tmem_wait_ld();
+              tc::reg_fence(sr);
+#pragma unroll
+              for (int j = 0; j < 16; j += 4) {
+                float m[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const float x = __uint_as_float(sr[j + q]) * c;
+                  const bool used = c_group + h + j + q < rows;
+                  m[q] = used ? -x : -INFINITY;
+                  sum = fmaf(used ? x : 0.0f, 0.0f, sum);
+                }
+                if (lane == 0)
+                  *reinterpret_cast<float4 *>(&nm[c_group + h + j]) =
+                      make_float4(m[0], m[1], m[2], m[3]);
+              }
+            }
+            if (sum != 0.0f && lane == 0) {  // by the longer way then
+#pragma unroll 1
+              for (int j = 0; j < min(rows - c_group, G::CH * CW); ++j) nm[c_group + j] = 0.0f;
+            }
+            if (lane == 0) ctl->fresh[group] = sum != 0.0f;
+          }
+          group_sync(bar);
+          if (!ctl->fresh[group]) {
+#pragma unroll
+            for (int ch = 0; ch < G::CH; ++ch) unset[ch] = 0;
+          }
+        }
 #pragma unroll
         for (int ch = 0; ch < G::CH; ++ch) {
           const int c0 = c_group + ch * CW;
@@ -832,33 +899,42 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           }
         }
         if (gone) break;
-        if (edge) {
+        const int stop16 = (s.total + 15) & ~15;  // the products take 16 tokens a step
+        const int warp_pos = tile * BT + quarter * 32;
+        if (warp_pos + 31 >= s.ctx && warp_pos < stop16) {
           // What a row does not see must not meet its zero weight as infinity or
           // NaN: V past the end is cleared, and so are the nodes' non-finite
           // values, which the epilogue gives to the rows that do see them.
           const uint32_t fill = 2 * t + 1;
           ok = ok && warp_wait(&ctl->full[fill % SLOTS], (fill / SLOTS) & 1, abort);
           uint8_t *row = slots + fill % SLOTS * G::SLOT + token * 128;
-          if (ok && pos >= s.ctx) {
+          if (ok && pos >= s.ctx && pos < stop16) {
+            uint32_t odd = 0;  // sign bit of a half: its exponent is all ones
 #pragma unroll 1
-            for (int i = cg; i < HALVES * 8; i += CG) {
-              uint4 *x = reinterpret_cast<uint4 *>(row + (i / 8) * HALF_BYTES + (i % 8) * 16);
-              if (pos >= s.total) {
-                *x = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              uint4 y = *x;
-              uint32_t *w = reinterpret_cast<uint32_t *>(&y);
-              bool odd = false;
+            for (int i = cg * 4; i < HALVES * 8; i += CG * 4) {
+              // four chunks of the row; which ones, by the token: no bank conflicts
+              uint4 *const x = reinterpret_cast<uint4 *>(row + (i / 8) * HALF_BYTES);
+              const int at = (i & 4) ^ (token & 7);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u, odd = true;
-                if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0xffffu, odd = true;
+              for (int q = 0; q < 4; ++q) {
+                const uint4 y = x[at ^ q];
+                odd |= ((y.x & 0x7f807f80u) + 0x00800080u) | ((y.y & 0x7f807f80u) + 0x00800080u) |
+                       ((y.z & 0x7f807f80u) + 0x00800080u) | ((y.w & 0x7f807f80u) + 0x00800080u);
+                if (pos >= s.total) x[at ^ q] = make_uint4(0, 0, 0, 0);
               }
-              if (odd) {
-                *x = y;
-                atomicOr(&ctl->odd[seg & 3], 1ull << (pos - s.ctx));
-              }
+            }
+            if (pos < s.total && (odd & 0x80008000u)) {
+              atomicOr(&ctl->odd[seg & 3], 1ull << (pos - s.ctx));
+#pragma unroll 1
+              for (int i = cg * 4; i < HALVES * 8; i += CG * 4)
+#pragma unroll 1
+                for (int q = 0; q < 16; ++q) {
+                  uint32_t *const w =
+                      reinterpret_cast<uint32_t *>(row + (i / 8) * HALF_BYTES) +
+                      ((((i & 4) ^ (token & 7)) ^ (q / 4)) * 4 + q % 4);
+                  if ((*w & 0x7f80u) == 0x7f80u) *w &= 0xffff0000u;
+                  if ((*w & 0x7f800000u) == 0x7f800000u) *w &= 0xffffu;
+                }
             }
           }
         }
@@ -895,7 +971,6 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       }
       const bool whole = s.tb == 0 && s.te == s.tiles;
       const int piece = s.tb == 0 ? 1 : 0;
-      const int here = min(max(rows - c_group, 0), G::CH * CW);  // the group's columns in use
       if (part && quarter == 0 && lane < CW) {
         const float vs = a.v_scale ? a.v_scale[s.h] : 1.0f;
 #pragma unroll
@@ -918,7 +993,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
             sum = mine_w * sum + their_w * ctl->other[1][col];
             ref = to;
           }
-          const bool sees = s.ctx > 0 || word[ch] != 0;
+          const bool sees = s.ctx > 0 || (word[ch] & (~0ull >> (64 - s.n))) != 0;
           float f = 1.0f;
           if (!whole) {
             float *ml = a.part_ml + (size_t)(cta * 2 + piece) * 2 * NT + col;
@@ -945,32 +1020,44 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         group_sync(bar);
         if (G::SETS == 2 ? leader : leader && group == 0) ctl->odd[(seg + (G::SETS == 2 ? 0 : 2)) & 3] = 0;
       }
-      if (last && quarter * 32 < D) {
+      if (last) {
         const int d = token;  // accumulator lane = column of the head
-        int g = c_group % a.group;
-        bf16 *dst = a.out + (s.row0 + s.node0 + c_group / a.group) * a.out_row +
-                    (s.h * a.group + g) * a.out_head + d;
-        const int64_t wrap = a.out_row - a.group * a.out_head;  // to the next node's first head
-        float *po = a.part_o + ((size_t)(cta * 2 + piece) * NT + c_group) * D + d;
-#pragma unroll 1
-        for (int j = 0; j < here; j += 16) {
-          float x[16];
+        float x[G::CH * CW];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+        for (int j = 0; j < G::CH * CW; ++j) x[j] = 0.0f;
+        if (quarter * 32 < D) {
 #pragma unroll 1
           for (int y = 0; y < (both ? 2 : 1); ++y) {  // this set's O, and the other's
-            const int from = y ? other : set;
-            const float *f = y ? ctl->other[1] : nm;
-            uint32_t o[16], o_lo[16];
-            tc::tmem_ld16(tmem_o + from * 2 * NT + lanes + c_group + j, o);
-            tc::tmem_ld16(tmem_o + from * 2 * NT + lanes + NT + c_group + j, o_lo);
-            tc::tmem_wait_ld();
-            tc::reg_fence(o);
-            tc::reg_fence(o_lo);
+            const uint32_t from = tmem_o + (y ? other : set) * 2 * NT + lanes + c_group;
+            const float4 *f =
+                reinterpret_cast<const float4 *>((y ? ctl->other[1] : nm) + c_group);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              x[i] = fmaf(__uint_as_float(o[i]) + __uint_as_float(o_lo[i]), f[c_group + j + i], x[i]);
+            for (int j = 0; j < G::CH * CW; j += CW) {
+              uint32_t o[CW], o_lo[CW];
+              tc::tmem_ld(from + j, o);
+              tc::tmem_ld(from + NT + j, o_lo);
+              tc::tmem_wait_ld();
+              tc::reg_fence(o);
+              tc::reg_fence(o_lo);
+#pragma unroll
+              for (int i = 0; i < CW; i += 4) {
+                const float4 g = f[(j + i) / 4];
+                const float h[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  x[j + i + q] = fmaf(__uint_as_float(o[i + q]) + __uint_as_float(o_lo[i + q]),
+                                      h[q], x[j + i + q]);
+              }
+            }
           }
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (G::SETS == 2 && lane == 0) {  // both O are read
+          tc::mbar_arrive(&ctl->o_free[set]);
+          if (both) tc::mbar_arrive(&ctl->o_free[other]);
+        }
+        if (quarter * 32 < D) {
 #pragma unroll 1
           for (unsigned long long m = odd; m; m &= m - 1) {
             const int at = __ffsll((long long)m) - 1, pos = s.ctx + at;
@@ -986,29 +1073,35 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
                 v = __bfloat162float(reinterpret_cast<const bf16 *>(src)[d]);
             }
             const bool finite = fabsf(v) < INFINITY;
-            uint32_t by = 0;
 #pragma unroll
             for (int ch = 0; ch < G::CH; ++ch) {
-              const uint32_t all = __ballot_sync(0xffffffffu, word[ch] >> at & 1);
-              if (j / CW == ch) by = all >> (j % CW);
+              const uint32_t by = __ballot_sync(0xffffffffu, word[ch] >> at & 1);
+#pragma unroll
+              for (int i = 0; i < CW; ++i)
+                if (!finite && (by >> i & 1)) x[ch * CW + i] += v;
             }
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (!finite && (by >> i & 1)) x[i] += v;
-          }
-          if (!whole) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (j + i < here) po[(j + i) * D] = x[i];
-            continue;
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (j + i < here) *dst = __float2bfloat16_rn(x[i]);
-            dst += a.out_head;
-            if (++g == a.group) {
-              g = 0;
-              dst += wrap;
+          for (int ch = 0; ch < G::CH; ++ch) {
+            const int c0 = c_group + ch * CW, count = min(rows - c0, CW);
+            if (count <= 0) break;
+            if (whole) {
+              // lane j: where column j's row of this head begins
+              const int node = (c0 + lane) / a.group, g = c0 + lane - node * a.group;
+              const long long at = (s.row0 + s.node0 + node) * a.out_row +
+                                   (s.h * a.group + g) * a.out_head;
+              const uint32_t lo = (uint32_t)at, hi = (uint32_t)(at >> 32);
+#pragma unroll
+              for (int j = 0; j < CW; ++j) {
+                const long long to = (long long)__shfl_sync(0xffffffffu, hi, j) << 32 |
+                                     __shfl_sync(0xffffffffu, lo, j);
+                if (j < count) a.out[to + d] = __float2bfloat16_rn(x[ch * CW + j]);
+              }
+            } else {
+              float *po = a.part_o + ((size_t)(cta * 2 + piece) * NT + c0) * D + d;
+#pragma unroll
+              for (int j = 0; j < CW; ++j)
+                if (j < count) po[j * D] = x[ch * CW + j];
             }
           }
         }
@@ -1026,12 +1119,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
                   cta + 1;
         *(volatile int *)&ctl->tail = 1;
       }
-      tc::fence_before_sync();
       __syncwarp();
-      if (G::SETS == 2 && last && lane == 0) {  // both O are read
-        tc::mbar_arrive(&ctl->o_free[set]);
-        if (both) tc::mbar_arrive(&ctl->o_free[other]);
-      }
       if (quarter == 0 && lane == 0) tc::mbar_arrive(&ctl->seg_empty[seg % SEGS]);
       uses[set] += part;
       uses[other] += both || !part;
@@ -1041,7 +1129,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     }
     if (leader && gone && q_last >= 0) {  // a Q copy still in flight lands before the CTA ends
       volatile int never = 0;
-      tc::mbar_wait(&ctl->q_full, q_last & 1, &never);
+      for (int i = q_last; i >= 0 && i > q_last - G::QS; --i)
+        tc::mbar_wait(&ctl->q_full[i % G::QS], (i / G::QS) & 1, &never);
     }
     __syncwarp();
   } else if constexpr (G::FP8) {
