@@ -596,10 +596,12 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           tc::fence_after_sync();
           const uint64_t kd = tc::smem_desc_sw128(slots + k_slot * G::SLOT);
           const uint64_t qd = tc::smem_desc_sw128(sq + seg % G::QS * G::Q_ONE);
+#pragma unroll 1
+          for (int h = 0; h < HALVES; ++h)
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc::umma_bf16_warp(tmem + b * NT, kd + (k / 4) * (HALF_BYTES / 16) + 2 * (k & 3),
-                          qd + (k / 4) * (NT * 128 / 16) + 2 * (k & 3), idesc_s, k != 0);
+            for (int k = 0; k < 4; ++k)
+              tc::umma_bf16_warp(tmem + b * NT, kd + h * (HALF_BYTES / 16) + 2 * k,
+                                 qd + h * (NT * 128 / 16) + 2 * k, idesc_s, (h | k) != 0);
           tc::umma_commit_warp(&ctl->empty[k_slot]);
           tc::umma_commit_warp(&ctl->s_full[b]);
           advance(k_slot, k_phase);
@@ -620,11 +622,11 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           const uint64_t vd = tc::smem_desc_sw128_mn(slots + v_slot * G::SLOT,
                                                      D == 128 ? HALF_BYTES : 0);
           const uint64_t pd = tc::smem_desc_sw128_mn(sp + x * G::P_SET, HALF_BYTES);
-#pragma unroll
-          for (int k = 0; k < BT / 16; ++k)
-            if (k * 16 < tokens)  // of the 16 tokens of a step, some may be past the end
-              tc::umma_bf16_warp(tmem_o + x * 2 * NT, vd + 128 * k, pd + 128 * k, idesc_o,
-                                 acc | (k != 0));
+          const int steps = min((tokens + 15) / 16, BT / 16);
+#pragma unroll 1
+          for (int k = 0; k < steps; ++k)
+            tc::umma_bf16_warp(tmem_o + x * 2 * NT, vd + 128 * k, pd + 128 * k, idesc_o,
+                               acc | (k != 0));
           tc::umma_commit_warp(&ctl->empty[v_slot]);
           tc::umma_commit_warp(&ctl->pv_done[x]);
           advance(v_slot, v_phase);
@@ -803,7 +805,9 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           }
           // e = c * S - reference, masked; again where the references are raised
           float e[CW];
-          for (bool again = false;; again = true) {
+          int again;  // a zero that the compiler does not see: one copy of the loop's body
+          asm volatile("mov.u32 %0, 0;" : "=r"(again));
+          for (;; again = 1) {
             float most = -INFINITY;
             if (ok) {
 #pragma unroll
@@ -1020,44 +1024,34 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         group_sync(bar);
         if (G::SETS == 2 ? leader : leader && group == 0) ctl->odd[(seg + (G::SETS == 2 ? 0 : 2)) & 3] = 0;
       }
-      if (last) {
+      if (last && quarter * 32 < D) {
         const int d = token;  // accumulator lane = column of the head
-        float x[G::CH * CW];
+#pragma unroll 1
+        for (int c0 = c_group; c0 < min(rows, c_group + G::CH * CW); c0 += 16) {
+          float x[16];
 #pragma unroll
-        for (int j = 0; j < G::CH * CW; ++j) x[j] = 0.0f;
-        if (quarter * 32 < D) {
+          for (int i = 0; i < 16; ++i) x[i] = 0.0f;
 #pragma unroll 1
           for (int y = 0; y < (both ? 2 : 1); ++y) {  // this set's O, and the other's
-            const uint32_t from = tmem_o + (y ? other : set) * 2 * NT + lanes + c_group;
-            const float4 *f =
-                reinterpret_cast<const float4 *>((y ? ctl->other[1] : nm) + c_group);
+            const uint32_t from = tmem_o + (y ? other : set) * 2 * NT + lanes + c0;
+            const float4 *f = reinterpret_cast<const float4 *>((y ? ctl->other[1] : nm) + c0);
+            uint32_t o[16], o_lo[16];
+            tc::tmem_ld16(from, o);
+            tc::tmem_ld16(from + NT, o_lo);
+            tc::tmem_wait_ld();
+            tc::reg_fence(o);
+            tc::reg_fence(o_lo);
 #pragma unroll
-            for (int j = 0; j < G::CH * CW; j += CW) {
-              uint32_t o[CW], o_lo[CW];
-              tc::tmem_ld(from + j, o);
-              tc::tmem_ld(from + NT + j, o_lo);
-              tc::tmem_wait_ld();
-              tc::reg_fence(o);
-              tc::reg_fence(o_lo);
+            for (int i = 0; i < 16; i += 4) {
+              const float4 g = f[i / 4];
+              const float h[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-              for (int i = 0; i < CW; i += 4) {
-                const float4 g = f[(j + i) / 4];
-                const float h[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  x[j + i + q] = fmaf(__uint_as_float(o[i + q]) + __uint_as_float(o_lo[i + q]),
-                                      h[q], x[j + i + q]);
-              }
+              for (int q = 0; q < 4; ++q)
+                x[i + q] = fmaf(__uint_as_float(o[i + q]) + __uint_as_float(o_lo[i + q]), h[q],
+                                x[i + q]);
             }
           }
-        }
-        tc::fence_before_sync();
-        __syncwarp();
-        if (G::SETS == 2 && lane == 0) {  // both O are read
-          tc::mbar_arrive(&ctl->o_free[set]);
-          if (both) tc::mbar_arrive(&ctl->o_free[other]);
-        }
-        if (quarter * 32 < D) {
+          const int j0 = (c0 - c_group) % CW;  // of the chunk's columns
 #pragma unroll 1
           for (unsigned long long m = odd; m; m &= m - 1) {
             const int at = __ffsll((long long)m) - 1, pos = s.ctx + at;
@@ -1073,38 +1067,42 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
                 v = __bfloat162float(reinterpret_cast<const bf16 *>(src)[d]);
             }
             const bool finite = fabsf(v) < INFINITY;
+            uint32_t by = 0;
 #pragma unroll
             for (int ch = 0; ch < G::CH; ++ch) {
-              const uint32_t by = __ballot_sync(0xffffffffu, word[ch] >> at & 1);
-#pragma unroll
-              for (int i = 0; i < CW; ++i)
-                if (!finite && (by >> i & 1)) x[ch * CW + i] += v;
+              const uint32_t all = __ballot_sync(0xffffffffu, word[ch] >> at & 1);
+              if ((c0 - c_group) / CW == ch) by = all >> j0;
             }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (!finite && (by >> i & 1)) x[i] += v;
           }
+          const int count = min(rows - c0, 16);
+          if (whole) {
+            // lane j: where column j's row of this head begins
+            const int node = (c0 + lane) / a.group, g = c0 + lane - node * a.group;
+            const long long at = (s.row0 + s.node0 + node) * a.out_row +
+                                 (s.h * a.group + g) * a.out_head;
+            const uint32_t lo = (uint32_t)at, hi = (uint32_t)(at >> 32);
 #pragma unroll
-          for (int ch = 0; ch < G::CH; ++ch) {
-            const int c0 = c_group + ch * CW, count = min(rows - c0, CW);
-            if (count <= 0) break;
-            if (whole) {
-              // lane j: where column j's row of this head begins
-              const int node = (c0 + lane) / a.group, g = c0 + lane - node * a.group;
-              const long long at = (s.row0 + s.node0 + node) * a.out_row +
-                                   (s.h * a.group + g) * a.out_head;
-              const uint32_t lo = (uint32_t)at, hi = (uint32_t)(at >> 32);
-#pragma unroll
-              for (int j = 0; j < CW; ++j) {
-                const long long to = (long long)__shfl_sync(0xffffffffu, hi, j) << 32 |
-                                     __shfl_sync(0xffffffffu, lo, j);
-                if (j < count) a.out[to + d] = __float2bfloat16_rn(x[ch * CW + j]);
-              }
-            } else {
-              float *po = a.part_o + ((size_t)(cta * 2 + piece) * NT + c0) * D + d;
-#pragma unroll
-              for (int j = 0; j < CW; ++j)
-                if (j < count) po[j * D] = x[ch * CW + j];
+            for (int j = 0; j < 16; ++j) {
+              const long long to = (long long)__shfl_sync(0xffffffffu, hi, j) << 32 |
+                                   __shfl_sync(0xffffffffu, lo, j);
+              if (j < count) a.out[to + d] = __float2bfloat16_rn(x[j]);
             }
+          } else {
+            float *po = a.part_o + ((size_t)(cta * 2 + piece) * NT + c0) * D + d;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (j < count) po[j * D] = x[j];
           }
         }
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (G::SETS == 2 && last && lane == 0) {  // both O are read
+        tc::mbar_arrive(&ctl->o_free[set]);
+        if (both) tc::mbar_arrive(&ctl->o_free[other]);
       }
       if (last && leader && group == set && !whole && piece == 1) {
         // the item goes on in the CTAs up to the one that holds its last unit
