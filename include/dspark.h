@@ -438,7 +438,8 @@ size_t dspark_tree_attention_workspace_bytes(const dspark_kv_cache *cache, int32
  * masked places included).  Scores, statistics and sums in f32; the weights meet
  * V with 16 bits (the sum of two bf16).
  *   q, out bf16: element i of head h of row m at m * row_stride + h * head_stride
- *          + i; q 16-byte aligned with strides (in elements) that are multiples of 8
+ *          + i; q 16-byte aligned with strides (in elements) that are multiples of 8;
+ *          out's strides at most 2^24
  *   ctx    int32 [R] as dspark_kv_plan took it; row_start int32 [R+1], anc uint64
  *          [n_rows] and block_table int32 [R, max_pages] as it left them; anc
  *          NULL: chains (row i sees nodes 0..i)

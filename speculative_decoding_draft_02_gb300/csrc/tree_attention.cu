@@ -119,10 +119,11 @@ extern "C" int dspark_tree_attention(const dspark_kv_cache *cache, int32_t R, in
   if (need == 0 || n_rows < 0 || max_pages < 1) return DSPARK_ERR_ARG;
   if (n_rows == 0) return DSPARK_OK;
   const int64_t most = (int64_t)1 << 39;  // elements: a tensor map's strides are below 2^40 bytes
+  const int64_t out_most = (int64_t)1 << 24;  // a tile's rows lie within 2^31 elements
   if (!q || !ctx || !row_start || !block_table || !out || ((uintptr_t)q & 15) ||
       ((uintptr_t)out & 1) || q_row_stride <= 0 || q_head_stride <= 0 || q_row_stride >= most ||
       q_head_stride >= most || q_row_stride % 8 || q_head_stride % 8 || out_row_stride <= 0 ||
-      out_head_stride <= 0)
+      out_head_stride <= 0 || out_row_stride > out_most || out_head_stride > out_most)
     return DSPARK_ERR_ARG;
   if (!workspace || ((uintptr_t)workspace & 255) || workspace_bytes < need)
     return DSPARK_ERR_WORKSPACE;

@@ -226,7 +226,9 @@ struct Ctl {
   uint64_t p_full[2], pv_done[2], o_free[2], half[2];
   // by set and column (one set: 128 columns)
   alignas(16) float nm[128];  // minus the column's reference exponent (log2)
-  int top[128];           // how far a tile's scores pass it, as an ordered key
+  // how far a tile's scores pass it, as an ordered key; at a segment's end where the
+  // column's row of the output lies from the tile's first one
+  alignas(16) int top[128];
   alignas(16) float other[2][64];  // a set's references and sums, for the other
   long long sums[32];
   Walker walk;
@@ -235,7 +237,6 @@ struct Ctl {
   uint64_t seg_full[SEGS], seg_empty[SEGS];
   int raw_end;            // 8-bit: fills of the raw ring
   unsigned long long odd[4];  // nodes with non-finite V, by segment mod 4
-  int fresh[2];           // of a group: its first references are still to be raised
   int tail;               // the CTA leaves an item to its successors
   int abort;
   uint32_t tmem;
@@ -286,27 +287,8 @@ __device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t two) {
   return pack_bf16(f.x, f.y);
 }
 
-// Sum of v[j] over the warp's lanes, left in lane j (lanes j and j + 16 of 16
-// columns): 31 exchanges for 32 columns, in a fixed order.
-template <int CW>
-__device__ __forceinline__ float column_sums(float (&v)[CW], int lane) {
-  if constexpr (CW == 16) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], 16);
-  }
-#pragma unroll
-  for (int o = CW / 2; o; o >>= 1) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int j = 0; j < o; ++j) {
-      const float send = up ? v[j] : v[j + o], keep = up ? v[j + o] : v[j];
-      v[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-    }
-  }
-  return v[0];
-}
-
-// The columns' maxima, left the same way (a NaN counts for nothing).
+// The maximum of v[j] over the warp's lanes, left in lane j (lanes j and j + 16 of
+// 16 columns): 31 exchanges for 32 columns.  A NaN counts for nothing.
 template <int CW>
 __device__ __forceinline__ float column_max(float (&v)[CW], int lane) {
   if constexpr (CW == 16) {
@@ -622,11 +604,17 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           const uint64_t vd = tc::smem_desc_sw128_mn(slots + v_slot * G::SLOT,
                                                      D == 128 ? HALF_BYTES : 0);
           const uint64_t pd = tc::smem_desc_sw128_mn(sp + x * G::P_SET, HALF_BYTES);
-          const int steps = min((tokens + 15) / 16, BT / 16);
+          if (tokens >= BT) {
+#pragma unroll
+            for (int k = 0; k < BT / 16; ++k)
+              tc::umma_bf16_warp(tmem_o + x * 2 * NT, vd + 128 * k, pd + 128 * k, idesc_o,
+                                 acc | (k != 0));
+          } else {  // the steps that hold tokens; in the last some may be past the end
 #pragma unroll 1
-          for (int k = 0; k < steps; ++k)
-            tc::umma_bf16_warp(tmem_o + x * 2 * NT, vd + 128 * k, pd + 128 * k, idesc_o,
-                               acc | (k != 0));
+            for (int k = 0; k * 16 < tokens; ++k)
+              tc::umma_bf16_warp(tmem_o + x * 2 * NT, vd + 128 * k, pd + 128 * k, idesc_o,
+                                 acc | (k != 0));
+          }
           tc::umma_commit_warp(&ctl->empty[v_slot]);
           tc::umma_commit_warp(&ctl->pv_done[x]);
           advance(v_slot, v_phase);
@@ -667,11 +655,14 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       return reinterpret_cast<uint4 *>(sp_set + (col / 64) * HALF_BYTES + token * 128 +
                                        (((col % 64) / 8) ^ (token & 7)) * 16);
     };
-    // the column sums' meeting place: the columns' own chunks of P rows 0, 8, ..
-    auto sum_slot = [&](int c0, int q, int j) -> float * {
-      constexpr int PER = CW / 2;  // in a row's bytes
-      return reinterpret_cast<float *>(sp_set + (c0 / 64) * HALF_BYTES +
-                                       8 * (q * 2 + j / PER) * 128 + (c0 % 64) * 2) + j % PER;
+    // At a segment's end the same chunks take f32 numbers, one for each token (or O's
+    // row) and column: four to a chunk, a chunk of columns' first half where the
+    // weights' roundings lay, the second where their rests did.
+    auto f32_at = [&](int row, int j) -> float * {
+      constexpr int HW = CW / 2;
+      const int c = (j % CW < HW ? 0 : NT) + c_group + j / CW * CW + j % HW / 4 * 8;
+      return reinterpret_cast<float *>(sp_set + (c / 64) * HALF_BYTES + row * 128 +
+                                       (((c % 64) / 8) ^ (row & 7)) * 16) + j % 4;
     };
     uint32_t t0 = 0, seg = 0;   // the segment's first tile, of all of the share's
     uint32_t mine = 0;          // tiles that this set has taken
@@ -748,45 +739,6 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         const bool edge = tile * BT + BT > s.ctx;  // some token is a node or past the end
         bool waited = mine == 0;
         tc::fence_after_sync();
-        if (k == first && tile * BT < s.ctx) {
-          // The first references: the scores of the tile's first token, which every
-          // row sees, so that no column's maximum lies below its reference; one
-          // that lies far above it raises it.
-          if (quarter == 0 && ok) {
-            float sum = 0.0f;  // stays 0 unless one is infinite or NaN
-#pragma unroll
-            for (int h = 0; h < G::CH * CW; h += 16) {
-              uint32_t sr[16];
-              tc::tmem_ld16(tmem + lanes + b * NT + c_group + h, sr);
-              tc::tmem_wait_ld();
-              tc::reg_fence(sr);
-#pragma unroll
-              for (int j = 0; j < 16; j += 4) {
-                float m[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const float x = __uint_as_float(sr[j + q]) * c;
-                  const bool used = c_group + h + j + q < rows;
-                  m[q] = used ? -x : -INFINITY;
-                  sum = fmaf(used ? x : 0.0f, 0.0f, sum);
-                }
-                if (lane == 0)
-                  *reinterpret_cast<float4 *>(&nm[c_group + h + j]) =
-                      make_float4(m[0], m[1], m[2], m[3]);
-              }
-            }
-            if (sum != 0.0f && lane == 0) {  // by the longer way then
-#pragma unroll 1
-              for (int j = 0; j < min(rows - c_group, G::CH * CW); ++j) nm[c_group + j] = 0.0f;
-            }
-            if (lane == 0) ctl->fresh[group] = sum != 0.0f;
-          }
-          group_sync(bar);
-          if (!ctl->fresh[group]) {
-#pragma unroll
-            for (int ch = 0; ch < G::CH; ++ch) unset[ch] = 0;
-          }
-        }
 #pragma unroll
         for (int ch = 0; ch < G::CH; ++ch) {
           const int c0 = c_group + ch * CW;
@@ -829,13 +781,68 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
 #pragma unroll
                 for (int j = 0; j < CW; ++j) e[j] = seen >> j & 1 ? e[j] : -INFINITY;
               }
-#pragma unroll
-              for (int j = 0; j < CW; ++j) most = fmaxf(most, e[j]);
             }
+            if (k == first && !again && tile * BT < s.ctx) {
+              // The first references: the scores of the tile's first token, which every
+              // row sees, so that no column's maximum lies below its reference; one
+              // that lies far above raises it.  No number: by the longer way.
+              group_sync(bar);  // the references so far are read
+              if (quarter == 0) {
+                if (lane == 0) {
+#pragma unroll
+                  for (int j = 0; j < CW; j += 4)
+                    *reinterpret_cast<float4 *>(&nm[c0 + j]) =
+                        make_float4(e[j], e[j + 1], e[j + 2], e[j + 3]);
+                }
+                __syncwarp();
+                const float x = nm[c0 + lane % CW];
+                __syncwarp();
+                if (lane < CW)
+                  nm[c0 + lane] =
+                      c0 + lane >= rows ? -INFINITY : (fabsf(x) < INFINITY ? -x : INFINITY);
+              }
+              group_sync(bar);
+#pragma unroll
+              for (int j = 0; j < CW; j += 4) {
+                const float4 m = *reinterpret_cast<const float4 *>(&nm[c0 + j]);
+                e[j] += m.x;
+                e[j + 1] += m.y;
+                e[j + 2] += m.z;
+                e[j + 3] += m.w;
+              }
+              unset[ch] = 0;
+            }
+#pragma unroll
+            for (int j = 0; j < CW; ++j) most = fmaxf(most, e[j]);
             if (again || !group_any(bar, unset[ch] != 0 || most > RAISE || !ok)) break;
             if (group_any(bar, !ok)) {
               gone = true;
               break;
+            }
+            // a first reference that was no number: as if there were none
+            const uint32_t none =
+                __ballot_sync(0xffffffffu, lane < CW && nm[c0 + lane % CW] == INFINITY);
+            if (none) {
+              unset[ch] |= none;
+              group_sync(bar);
+              if (quarter == 0 && lane < CW && (none >> lane & 1)) nm[c0 + lane] = 0.0f;
+              group_sync(bar);
+#pragma unroll
+              for (int j = 0; j < CW; ++j) e[j] = -INFINITY;
+#pragma unroll 1
+              for (int h = 0; h < CW; h += 16) {
+                uint32_t sr[16];
+                tc::tmem_ld16(tmem + lanes + b * NT + c0 + h, sr);
+                tc::tmem_wait_ld();
+                tc::reg_fence(sr);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  const float x = fmaf(__uint_as_float(sr[j]), c, nm[c0 + h + j]);
+                  const float y = seen >> (h + j) & 1 ? x : -INFINITY;
+                  if (h == 0) e[j] = y;
+                  else e[CW - 16 + j] = y;
+                }
+              }
             }
             // by how much the tile passes each reference: lane j for column j
             const float peak = column_max<CW>(e, lane);
@@ -955,10 +962,28 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       const bool both = G::SETS == 2 && n_tiles > 1;
       if (part) {
         ok = ok && warp_wait(&ctl->pv_done[set], (mine - 1) & 1, abort);
+        // A column's sum over the tokens: in the warp by way of shared memory (lane j
+        // adds column j), in a fixed order; then over the four warps.
+        if (ok) {
 #pragma unroll
-        for (int ch = 0; ch < G::CH; ++ch) {
-          const float sums = column_sums<CW>(l[ch], lane);
-          if (ok && lane < CW) *sum_slot(c_group + ch * CW, quarter, lane) = sums;
+          for (int ch = 0; ch < G::CH; ++ch)
+#pragma unroll
+            for (int j = 0; j < CW; j += 4)
+              *reinterpret_cast<float4 *>(f32_at(token, ch * CW + j)) =
+                  make_float4(l[ch][j], l[ch][j + 1], l[ch][j + 2], l[ch][j + 3]);
+          __syncwarp();
+          float sums[G::CH];
+#pragma unroll
+          for (int ch = 0; ch < G::CH; ++ch) {
+            sums[ch] = 0.0f;
+#pragma unroll 4
+            for (int i = 0; i < 32; ++i)
+              sums[ch] += *f32_at(quarter * 32 + i, ch * CW + lane % CW);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int ch = 0; ch < G::CH; ++ch)
+            if (lane < CW) *f32_at(quarter * 32, ch * CW + lane) = sums[ch];
         }
         // `other` is free once its last reader has given this set's O back
         if (!last && uses[set]) ok = ok && warp_wait(&ctl->o_free[set], (uses[set] - 1) & 1, abort);
@@ -981,8 +1006,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         for (int ch = 0; ch < G::CH; ++ch) {
           const int c0 = c_group + ch * CW, col = c0 + lane;
           if (col >= rows) continue;
-          float sum = (*sum_slot(c0, 0, lane) + *sum_slot(c0, 1, lane)) +
-                      (*sum_slot(c0, 2, lane) + *sum_slot(c0, 3, lane));
+          const int j = ch * CW + lane;
+          float sum = (*f32_at(0, j) + *f32_at(32, j)) + (*f32_at(64, j) + *f32_at(96, j));
           float ref = unset[ch] >> lane & 1 ? -INFINITY : -nm[col];
           if (!last) {
             ctl->other[0][col] = ref;
@@ -998,6 +1023,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
             ref = to;
           }
           const bool sees = s.ctx > 0 || (word[ch] & (~0ull >> (64 - s.n))) != 0;
+          const int node = col / a.group, g = col - node * a.group;
           float f = 1.0f;
           if (!whole) {
             float *ml = a.part_ml + (size_t)(cta * 2 + piece) * 2 * NT + col;
@@ -1006,11 +1032,11 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           } else {
             f = sees ? vs / sum : 0.0f;
             if (a.lse) {
-              const int node = col / a.group, head = s.h * a.group + col - node * a.group;
-              a.lse[(size_t)(s.row0 + s.node0 + node) * a.heads * a.group + head] =
+              a.lse[(size_t)(s.row0 + s.node0 + node) * a.heads * a.group + s.h * a.group + g] =
                   sees ? (ref + log2f(sum)) * LN2 : -INFINITY;
             }
           }
+          top[col] = node * (int)a.out_row + g * (int)a.out_head;  // where the column's row lies
           nm[col] = mine_w * f;  // the factors of both O
           if (G::SETS == 2) ctl->other[1][col] = their_w * f;
         }
@@ -1079,16 +1105,15 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           }
           const int count = min(rows - c0, 16);
           if (whole) {
-            // lane j: where column j's row of this head begins
-            const int node = (c0 + lane) / a.group, g = c0 + lane - node * a.group;
-            const long long at = (s.row0 + s.node0 + node) * a.out_row +
-                                 (s.h * a.group + g) * a.out_head;
-            const uint32_t lo = (uint32_t)at, hi = (uint32_t)(at >> 32);
+            bf16 *const dst = a.out + (s.row0 + s.node0) * a.out_row +
+                              (int64_t)s.h * a.group * a.out_head + d;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const long long to = (long long)__shfl_sync(0xffffffffu, hi, j) << 32 |
-                                   __shfl_sync(0xffffffffu, lo, j);
-              if (j < count) a.out[to + d] = __float2bfloat16_rn(x[j]);
+            for (int j = 0; j < 16; j += 4) {
+              const int4 to = *reinterpret_cast<const int4 *>(&top[c0 + j]);
+              if (j < count) dst[to.x] = __float2bfloat16_rn(x[j]);
+              if (j + 1 < count) dst[to.y] = __float2bfloat16_rn(x[j + 1]);
+              if (j + 2 < count) dst[to.z] = __float2bfloat16_rn(x[j + 2]);
+              if (j + 3 < count) dst[to.w] = __float2bfloat16_rn(x[j + 3]);
             }
           } else {
             float *po = a.part_o + ((size_t)(cta * 2 + piece) * NT + c0) * D + d;
