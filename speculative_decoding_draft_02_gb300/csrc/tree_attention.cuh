@@ -86,7 +86,15 @@ struct Geo {
   static constexpr int CH = NT / (CW * CG);          // chunks of a thread
   static constexpr int SW = 4 * CG * SETS;
   static constexpr int CV = FP8 ? 4 : 0;
-  static constexpr int THREADS = 32 * (2 + SW + CV);
+  // Warps 0..3 copy and issue (two of them rest), the softmax's follow, then those
+  // that widen.  The softmax keeps a column's sums and scores in registers, more of
+  // them than a thread's share: the others give theirs up.
+  static constexpr int THREADS = 32 * (4 + SW + CV);
+  static constexpr int REGS_FEW = FP8 ? 72 : 88, REGS_SOFTMAX = FP8 ? 168 : 208, REGS_WIDEN = 104;
+  static_assert(SW == 8 && (CV == 0 || CV == 4), "warps 4..11: the softmax");
+  static_assert(REGS_FEW + 2 * REGS_SOFTMAX + (FP8 ? REGS_WIDEN : 0) <=
+                    65536 / THREADS / 8 * 8 * (THREADS / 128),
+                "a block's registers");
   static constexpr int SLOT = BT * D * 2;
   // Q of the next segment beside the present one's, where two sets leave room
   static constexpr int QS = SETS;
@@ -275,6 +283,16 @@ __device__ __forceinline__ bool group_any(int id, bool p) {
   return r != 0;
 }
 
+// A warpgroup's registers, given up or taken.
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&v);
@@ -434,6 +452,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
   __syncthreads();
   const uint32_t tmem = ctl->tmem, tmem_o = tmem + 2 * NT;
 
+  if (warp < 4) fewer_registers<G::REGS_FEW>();
   if (warp == 0) {
     // -------------------------------------------------- copies of K and V ----
     // Row tiles of one item read the same K and V: keep them in L2 for the next.
@@ -638,13 +657,14 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       warp_wait(&ctl->drain, 0, &never);
     }
     __syncwarp();
-  } else if (warp < 2 + G::SW) {
+  } else if (warp >= 4 && warp < 4 + G::SW) {
+    more_registers<G::REGS_SOFTMAX>();
     // ----------------------------------------------------------- softmax ----
-    const int quarter = warp & 3, group = (warp - 2) >> 2, bar = 1 + group;
+    const int quarter = warp & 3, group = (warp - 4) >> 2, bar = 1 + group;
     const int set = G::SETS == 2 ? group : 0, cg = G::SETS == 2 ? 0 : group;
     const int token = quarter * 32 + lane, c_group = cg * G::CH * CW;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    const bool leader = ((warp - 2) & 3) == 0 && lane == 0;  // of the group
+    const bool leader = quarter == 0 && lane == 0;  // of the group
     uint8_t *const sp_set = sp + set * G::P_SET;
     float *const nm = ctl->nm + set * 64;
     int *const top = ctl->top + set * 64;
@@ -1156,9 +1176,11 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         tc::mbar_wait(&ctl->q_full[i % G::QS], (i / G::QS) & 1, &never);
     }
     __syncwarp();
-  } else if constexpr (G::FP8) {
+  } else if (warp >= 4 + G::SW) {
+    if constexpr (G::FP8) {
+    fewer_registers<G::REGS_WIDEN>();
     // --------------------------------------- 8-bit tiles widened to bf16 ----
-    const int w = warp - 2 - G::SW;
+    const int w = warp - 4 - G::SW;
     int slot = 0, raw = 0;
     uint32_t phase = 0, raw_phase = 0;
     constexpr int PARTS = D / 16;  // 16-byte parts of a raw row
@@ -1204,6 +1226,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         raw = 0;
         raw_phase ^= 1;
       }
+    }
     }
   }
 
