@@ -13,13 +13,13 @@ using attn::Args;
 
 // Query rows of a tile: the narrowest that takes a request's rows, so that no
 // product, exponential or byte of shared memory is spent on empty columns; at
-// most 128 (TMEM holds two tiles of scores and O's two parts, four times as many
-// columns), or 64 beside the warps that widen an 8-bit cache.
+// most 128 (two tiles of scores and O in tensor memory, and Q and P in shared memory,
+// beside the tiles in flight).
 int row_tile(const dspark_kv_cache *c, int heads_q, int max_nodes) {
   const int rows = max_nodes * (heads_q / c->heads);
   if (rows <= 16) return 16;
   if (rows <= 32) return 32;
-  return rows <= 64 || c->type == DSPARK_KV_E4M3 ? 64 : 128;
+  return rows <= 64 ? 64 : 128;
 }
 
 struct Layout {
@@ -92,9 +92,8 @@ template <int TYPE, int D>
 int launch_tile(const Launch &l, int nt) {
   if (nt == 16) return launch<TYPE, D, 16>(l);
   if (nt == 32) return launch<TYPE, D, 32>(l);
-  if constexpr (TYPE == DSPARK_KV_BF16)
-    if (nt == 128) return launch<TYPE, D, 128>(l);
-  return launch<TYPE, D, 64>(l);
+  if (nt == 64) return launch<TYPE, D, 64>(l);
+  return launch<TYPE, D, 128>(l);
 }
 
 }  // namespace

@@ -16,11 +16,16 @@
 // it matters: the exponent's reference is kept from tile to tile and raised (with
 // O rescaled) only when some weight would exceed 2^RAISE.
 //
-// A weight meets V as the sum of two bf16 numbers, its rounding and what that
-// left out (columns j and NT + j of P, and two parts of O added at the end):
-// rounded to one, a row's error would be of the output's own rounding's size,
-// and below 64 rows the wider product costs nothing, as reading V's tile bounds
-// it.
+// A bf16 cache's weight meets V as the sum of two bf16 numbers, its rounding and
+// what that left out (columns j and NT + j of P, and two parts of O added at the
+// end): rounded to one, a row's error would be of the output's own rounding's size,
+// and below 64 rows the wider product costs nothing, as reading V's tile bounds it.
+//
+// An 8-bit cache's tiles are widened to f16, which holds every e4m3 value and takes
+// one conversion for two of them (bf16 takes four), and meet Q and P in f16: Q's
+// tile is scaled by the power of two that brings its largest value to 2^14 (f16
+// then keeps all 8 bits of whatever matters to a score), and a weight has 11 bits.
+// Weights are at most 2^14 there and count down to 2^-24.
 //
 // Work is cut into units of (request, KV head, row tile, 128-token tile), listed
 // in that order, and every CTA takes an equal share of the list: ragged contexts
@@ -51,9 +56,14 @@ constexpr int SEGS = 8;
 // What beginning and ending an item costs a CTA, in tiles (measured: about one
 // tile's time at 32 columns); counted so that short contexts balance too.
 constexpr int ITEM_UNITS = 2;
-// log2: how far scores may pass the reference.  Weights, their sum and O are
-// floating-point numbers of f32's range, so nothing is lost below 2^32.
-constexpr float RAISE = 32.0f;
+// log2: how far scores may pass the reference, and where a raised reference puts the
+// largest.  Beside a bf16 cache weights, their sum and O are floating-point numbers
+// of f32's range, so nothing is lost below 2^32; f16 weights start high, for the
+// sake of the small ones.
+template <bool FP8>
+struct Range {
+  static constexpr float RAISE = FP8 ? 14.0f : 32.0f, PEAK = FP8 ? 6.0f : 0.0f;
+};
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 struct Args {
@@ -75,12 +85,13 @@ struct Args {
 template <int TYPE, int D, int NT>
 struct Geo {
   static constexpr bool FP8 = TYPE == DSPARK_KV_E4M3;
+  static constexpr int PARTS = FP8 ? 1 : 2;          // of a weight, and of O
   // Up to 64 columns two sets of softmax warps take a segment's tiles in turn, each
   // with its S, P, references, sums and O: what one waits for (S, the tensor
   // memory, the group's barrier, P's place) the other's work covers.  128 columns
-  // leave no tensor memory for a second O: one set of two groups, each with half
-  // the columns; so do 64 beside the warps that widen, for their registers' sake.
-  static constexpr int SETS = NT <= (FP8 ? 32 : 64) ? 2 : 1;
+  // leave no room for a second P and O: one set of two groups, each with half the
+  // columns.
+  static constexpr int SETS = NT <= 64 ? 2 : 1;
   static constexpr int CW = NT < 32 ? NT : 32;       // columns of a softmax thread's chunk
   static constexpr int CG = SETS == 2 ? 1 : 2;       // groups of four warps in a set
   static constexpr int CH = NT / (CW * CG);          // chunks of a thread
@@ -90,7 +101,7 @@ struct Geo {
   // that widen.  The softmax keeps a column's sums and scores in registers, more of
   // them than a thread's share: the others give theirs up.
   static constexpr int THREADS = 32 * (4 + SW + CV);
-  static constexpr int REGS_FEW = FP8 ? 72 : 88, REGS_SOFTMAX = FP8 ? 168 : 208, REGS_WIDEN = 104;
+  static constexpr int REGS_FEW = FP8 ? 72 : 88, REGS_SOFTMAX = FP8 ? 176 : 208, REGS_WIDEN = 88;
   static_assert(SW == 8 && (CV == 0 || CV == 4), "warps 4..11: the softmax");
   static_assert(REGS_FEW + 2 * REGS_SOFTMAX + (FP8 ? REGS_WIDEN : 0) <=
                     65536 / THREADS / 8 * 8 * (THREADS / 128),
@@ -99,7 +110,7 @@ struct Geo {
   // Q of the next segment beside the present one's, where two sets leave room
   static constexpr int QS = SETS;
   static constexpr int Q_ONE = NT * D * 2, Q_BYTES = QS * Q_ONE;
-  static constexpr int P_SET = BT * 128 * (NT > 32 ? NT / 32 : 1);
+  static constexpr int P_SET = BT * 128 * (PARTS * NT > 64 ? PARTS * NT / 64 : 1);
   static constexpr int P_BYTES = SETS * P_SET;
   static constexpr int ROOM = SMEM_LIMIT - CTL_BYTES - Q_BYTES - P_BYTES;
   static constexpr int RAW = FP8 ? BT * D : 0;
@@ -109,8 +120,8 @@ struct Geo {
   static constexpr int RAWS_FIT = FP8 ? (ROOM - 3 * SLOT) / (RAW + !FP8) : 0;
   static constexpr int RAWS = RAWS_FIT < MAX_SLOTS ? RAWS_FIT : MAX_SLOTS;
   static constexpr int SMEM_BYTES = SLOTS * SLOT + RAWS * RAW + Q_BYTES + P_BYTES + CTL_BYTES;
-  // two tiles of S, and each set's O in its two parts
-  static constexpr uint32_t TMEM_USED = 2 * NT + SETS * 2 * NT;
+  // two tiles of S, and each set's O in its parts
+  static constexpr uint32_t TMEM_USED = 2 * NT + SETS * PARTS * NT;
   static constexpr uint32_t TMEM_COLS = TMEM_USED <= 128 ? 128 : TMEM_USED <= 256 ? 256 : 512;
   static_assert(SLOTS >= 3 && (!FP8 || RAWS >= 3) && SMEM_BYTES <= SMEM_LIMIT, "shared memory");
 };
@@ -243,7 +254,10 @@ struct Ctl {
   // The share's segments as the copying warp comes to them, for the other roles.
   alignas(16) Segment seg[SEGS];
   uint64_t seg_full[SEGS], seg_empty[SEGS];
-  int raw_end;            // 8-bit: fills of the raw ring
+  // 8-bit: Q of a place is in f16, by which power of two it was multiplied (and
+  // the warps' largest values on the way there)
+  uint64_t q_ready[2];
+  int q_exp[2], q_top[4];
   unsigned long long odd[4];  // nodes with non-finite V, by segment mod 4
   int tail;               // the CTA leaves an item to its successors
   int abort;
@@ -298,11 +312,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// Two 8-bit floats as two bf16 (exact): through f16, which holds every value.
+// Two 8-bit floats as two f16 (exact).
 __device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t two) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-  return pack_bf16(f.x, f.y);
+  return (uint32_t)h.y << 16 | h.x;
 }
 
 // The maximum of v[j] over the warp's lanes, left in lane j (lanes j and j + 16 of
@@ -358,6 +371,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&ctl->q_full[b], 1);
+      tc::mbar_init(&ctl->q_ready[b], 4);
       tc::mbar_init(&ctl->s_full[b], 1);
       tc::mbar_init(&ctl->s_empty[b], 4 * CG);
       tc::mbar_init(&ctl->p_full[b], 4 * CG);
@@ -369,11 +383,11 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     for (int i = 0; i < 4; ++i) ctl->odd[i] = 0;
     ctl->tail = 0;
     ctl->abort = 0;
-    ctl->raw_end = -1;
 #pragma unroll 1
     for (int i = 0; i < SEGS; ++i) {
       tc::mbar_init(&ctl->seg_full[i], 1);
-      tc::mbar_init(&ctl->seg_empty[i], 1 + G::SETS * CG);  // the MMA issuer, each group
+      // the MMA issuer, each group, those that widen
+      tc::mbar_init(&ctl->seg_empty[i], 1 + G::SETS * CG + (G::FP8 ? 1 : 0));
     }
     tc::fence_barrier_init();
     tc::tma_prefetch_desc(&tma_k);
@@ -464,7 +478,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     constexpr int RING_BYTES = G::FP8 ? G::RAW : G::SLOT;
     const int rows = min(1 << a.page_shift, BT), boxes = BT / rows;
     const uint32_t box_bytes = (uint32_t)(rows * D * (G::FP8 ? 1 : 2));
-    int slot = 0, fills = 0;
+    int slot = 0;
     uint32_t phase = 0, used = 0;
     bool ok = true;
     // Segments are published ahead of the copies, so that a role that needs a later
@@ -532,7 +546,6 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
             }
           }
           used |= 1u << slot;
-          ++fills;
           if (++slot == RING) {
             slot = 0;
             phase ^= 1;
@@ -546,16 +559,13 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
 #pragma unroll 1
     for (int i = 0; i < RING; ++i)
       if (used >> i & 1) warp_wait(&full[i], i < slot ? phase : phase ^ 1, &never);
-    if (G::FP8 && ok && warp_wait(&empty[slot], phase ^ 1, abort) && lane == 0) {
-      // one fill more without data: the end
-      *(volatile int *)&ctl->raw_end = fills;
-      tc::mbar_arrive(&full[slot]);
-    }
   } else if (warp == 1) {
     // -------------------------------------------------------- MMA issuer ----
     {
-      constexpr uint32_t idesc_s = tc::idesc_bf16(BT, NT);
-      constexpr uint32_t idesc_o = tc::idesc_bf16(128, 2 * NT) | tc::IDESC_A_MN | tc::IDESC_B_MN;
+      constexpr uint32_t idesc_s = G::FP8 ? tc::idesc_f16(BT, NT) : tc::idesc_bf16(BT, NT);
+      constexpr uint32_t idesc_o =
+          (G::FP8 ? tc::idesc_f16(128, G::PARTS * NT) : tc::idesc_bf16(128, G::PARTS * NT)) |
+          tc::IDESC_A_MN | tc::IDESC_B_MN;
       int k_slot = 0, v_slot = 1;
       uint32_t k_phase = 0, v_phase = 0, t = 0, pv = 0, seg = 0;
       uint32_t acc = 0;  // whether the pending tile adds to O
@@ -590,7 +600,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         const bool issue = more && (!first || !pending);
         if (issue) {
           const uint32_t b = t & 1;
-          ok = (!first || warp_wait(&ctl->q_full[seg % G::QS], (seg / G::QS) & 1, abort)) &&
+          ok = (!first || warp_wait(G::FP8 ? &ctl->q_ready[seg % G::QS] : &ctl->q_full[seg % G::QS],
+                                    (seg / G::QS) & 1, abort)) &&
                warp_wait(&ctl->full[k_slot], k_phase, abort) &&
                warp_wait(&ctl->s_empty[b], ((t >> 1) & 1) ^ 1, abort);
           if (!ok) break;
@@ -601,7 +612,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           for (int h = 0; h < HALVES; ++h)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              tc::umma_bf16_warp(tmem + b * NT, kd + h * (HALF_BYTES / 16) + 2 * k,
+              tc::umma_warp(tmem + b * NT, kd + h * (HALF_BYTES / 16) + 2 * k,
                                  qd + h * (NT * 128 / 16) + 2 * k, idesc_s, (h | k) != 0);
           tc::umma_commit_warp(&ctl->empty[k_slot]);
           tc::umma_commit_warp(&ctl->s_full[b]);
@@ -626,12 +637,12 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           if (tokens >= BT) {
 #pragma unroll
             for (int k = 0; k < BT / 16; ++k)
-              tc::umma_bf16_warp(tmem_o + x * 2 * NT, vd + 128 * k, pd + 128 * k, idesc_o,
+              tc::umma_warp(tmem_o + x * G::PARTS * NT, vd + 128 * k, pd + 128 * k, idesc_o,
                                  acc | (k != 0));
           } else {  // the steps that hold tokens; in the last some may be past the end
 #pragma unroll 1
             for (int k = 0; k * 16 < tokens; ++k)
-              tc::umma_bf16_warp(tmem_o + x * 2 * NT, vd + 128 * k, pd + 128 * k, idesc_o,
+              tc::umma_warp(tmem_o + x * G::PARTS * NT, vd + 128 * k, pd + 128 * k, idesc_o,
                                  acc | (k != 0));
           }
           tc::umma_commit_warp(&ctl->empty[v_slot]);
@@ -665,24 +676,22 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     const int token = quarter * 32 + lane, c_group = cg * G::CH * CW;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const bool leader = quarter == 0 && lane == 0;  // of the group
+    using R = Range<G::FP8>;
     uint8_t *const sp_set = sp + set * G::P_SET;
     float *const nm = ctl->nm + set * 64;
     int *const top = ctl->top + set * 64;
-    const uint32_t tmem_set = tmem_o + set * 2 * NT;
+    const uint32_t tmem_set = tmem_o + set * G::PARTS * NT;
     // P[token][column]: 64-column halves; 16-byte chunk c of a row lies at
     // c ^ (token & 7)
     auto p_at = [&](int col) -> uint4 * {
       return reinterpret_cast<uint4 *>(sp_set + (col / 64) * HALF_BYTES + token * 128 +
                                        (((col % 64) / 8) ^ (token & 7)) * 16);
     };
-    // At a segment's end the same chunks take f32 numbers, one for each token (or O's
-    // row) and column: four to a chunk, a chunk of columns' first half where the
-    // weights' roundings lay, the second where their rests did.
+    // At a segment's end the group's 64 columns of P take a chunk's f32 numbers, one
+    // for each token and column.
     auto f32_at = [&](int row, int j) -> float * {
-      constexpr int HW = CW / 2;
-      const int c = (j % CW < HW ? 0 : NT) + c_group + j / CW * CW + j % HW / 4 * 8;
-      return reinterpret_cast<float *>(sp_set + (c / 64) * HALF_BYTES + row * 128 +
-                                       (((c % 64) / 8) ^ (row & 7)) * 16) + j % 4;
+      return reinterpret_cast<float *>(sp_set + (c_group / 64) * HALF_BYTES + row * 128 +
+                                       ((j / 4) ^ (row & 7)) * 16) + j % 4;
     };
     uint32_t t0 = 0, seg = 0;   // the segment's first tile, of all of the share's
     uint32_t mine = 0;          // tiles that this set has taken
@@ -715,7 +724,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       if (group_any(bar, !ok)) break;
       const Segment s = ctl->seg[seg % SEGS];
       if (s.tb == s.te) break;
-      const float c = s.c;
+      float c = s.c;
       const int rows = s.nodes * a.group;  // columns in use
       const int n_tiles = s.te - s.tb;
       const int first = G::SETS == 2 ? (set ^ t0) & 1 : 0;  // this set's tiles: every SETS-th
@@ -754,6 +763,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         const int tile = s.tb + k;
         const uint32_t t = t0 + k, b = t & 1;
         ok = ok && warp_wait(&ctl->s_full[b], (t >> 1) & 1, abort);
+        // Q's power of two out of its scores: known since the product is done
+        if (G::FP8 && k == first) c = ldexpf(s.c, -ctl->q_exp[seg % G::QS]);
         if (k == n_tiles - 1 && leader && cg == 0 && ok) load_q(seg + G::QS);
         const int pos = tile * BT + token;
         const bool edge = tile * BT + BT > s.ctx;  // some token is a node or past the end
@@ -819,7 +830,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
                 __syncwarp();
                 if (lane < CW)
                   nm[c0 + lane] =
-                      c0 + lane >= rows ? -INFINITY : (fabsf(x) < INFINITY ? -x : INFINITY);
+                      c0 + lane >= rows ? -INFINITY
+                                        : (fabsf(x) < INFINITY ? R::PEAK - x : INFINITY);
               }
               group_sync(bar);
 #pragma unroll
@@ -834,7 +846,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
             }
 #pragma unroll
             for (int j = 0; j < CW; ++j) most = fmaxf(most, e[j]);
-            if (again || !group_any(bar, unset[ch] != 0 || most > RAISE || !ok)) break;
+            if (again || !group_any(bar, unset[ch] != 0 || most > R::RAISE || !ok)) break;
             if (group_any(bar, !ok)) {
               gone = true;
               break;
@@ -872,6 +884,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
             group_sync(bar);
             float raise = order_value(top[c0 + lane % CW]);
             const bool fresh = unset[ch] >> (lane % CW) & 1;
+            raise -= R::PEAK;
             if (!(raise > -INFINITY) || (!fresh && raise < 0.0f)) raise = 0.0f;
             unset[ch] &= __ballot_sync(0xffffffffu, lane < CW && top[c0 + lane % CW] ==
                                                                      order_key(-INFINITY));
@@ -881,7 +894,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
 #pragma unroll
               for (int j = 0; j < CW; ++j) l[ch][j] *= __shfl_sync(0xffffffffu, keep, j);
 #pragma unroll 1
-              for (int h = 0; h < 2 * CW; h += 16) {
+              for (int h = 0; h < G::PARTS * CW; h += 16) {
                 const uint32_t at = tmem_set + lanes + (h < CW ? 0 : NT - CW) + c0 + h;
                 uint32_t o[16];
                 tc::tmem_ld16(at, o);
@@ -908,22 +921,28 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&ctl->s_empty[b]);
           }
-          // e's place is taken by the weights: roundings below, rests above
+          // e's place is taken by the weights, as P has them: two bf16 roundings below
+          // and their rests above, or two f16 ones
 #pragma unroll
           for (int j = 0; j < CW; j += 2) {
             const float x = ex2_fast(e[j]), y = ex2_fast(e[j + 1]);
             l[ch][j] += x;
             l[ch][j + 1] += y;
-            const uint32_t hi = pack_bf16(x, y);
-            e[j] = __uint_as_float(hi);
-            e[j + 1] = __uint_as_float(pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi)));
+            if constexpr (G::FP8) {
+              const __half2 hi = __floats2half2_rn(x, y);
+              e[j] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&hi));
+            } else {
+              const uint32_t hi = pack_bf16(x, y);
+              e[j] = __uint_as_float(hi);
+              e[j + 1] = __uint_as_float(pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi)));
+            }
           }
           if (!waited) ok = warp_wait(&ctl->pv_done[set], (mine - 1) & 1, abort);  // P is free
           waited = true;
 #pragma unroll
           for (int j = 0; j < CW; j += 8) {
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
+            for (int part = 0; part < G::PARTS; ++part)
               *p_at(part * NT + c0 + j) = make_uint4(
                   __float_as_uint(e[j + part]), __float_as_uint(e[j + 2 + part]),
                   __float_as_uint(e[j + 4 + part]), __float_as_uint(e[j + 6 + part]));
@@ -940,7 +959,10 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           ok = ok && warp_wait(&ctl->full[fill % SLOTS], (fill / SLOTS) & 1, abort);
           uint8_t *row = slots + fill % SLOTS * G::SLOT + token * 128;
           if (ok && pos >= s.ctx && pos < stop16) {
-            uint32_t odd = 0;  // sign bit of a half: its exponent is all ones
+            // sign bit of a half of odd: its exponent is all ones
+            constexpr uint32_t EXP = G::FP8 ? 0x7c00u : 0x7f80u, ONE = 0x8000u - EXP;
+            constexpr uint32_t EXPS = EXP << 16 | EXP, ONES = ONE << 16 | ONE;
+            uint32_t odd = 0;
 #pragma unroll 1
             for (int i = cg * 4; i < HALVES * 8; i += CG * 4) {
               // four chunks of the row; which ones, by the token: no bank conflicts
@@ -949,8 +971,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 const uint4 y = x[at ^ q];
-                odd |= ((y.x & 0x7f807f80u) + 0x00800080u) | ((y.y & 0x7f807f80u) + 0x00800080u) |
-                       ((y.z & 0x7f807f80u) + 0x00800080u) | ((y.w & 0x7f807f80u) + 0x00800080u);
+                odd |= ((y.x & EXPS) + ONES) | ((y.y & EXPS) + ONES) | ((y.z & EXPS) + ONES) |
+                       ((y.w & EXPS) + ONES);
                 if (pos >= s.total) x[at ^ q] = make_uint4(0, 0, 0, 0);
               }
             }
@@ -963,8 +985,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
                   uint32_t *const w =
                       reinterpret_cast<uint32_t *>(row + (i / 8) * HALF_BYTES) +
                       ((((i & 4) ^ (token & 7)) ^ (q / 4)) * 4 + q % 4);
-                  if ((*w & 0x7f80u) == 0x7f80u) *w &= 0xffff0000u;
-                  if ((*w & 0x7f800000u) == 0x7f800000u) *w &= 0xffffu;
+                  if ((*w & EXP) == EXP) *w &= 0xffff0000u;
+                  if ((*w & EXP << 16) == EXP << 16) *w &= 0xffffu;
                 }
             }
           }
@@ -985,25 +1007,22 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         // A column's sum over the tokens: in the warp by way of shared memory (lane j
         // adds column j), in a fixed order; then over the four warps.
         if (ok) {
-#pragma unroll
-          for (int ch = 0; ch < G::CH; ++ch)
-#pragma unroll
-            for (int j = 0; j < CW; j += 4)
-              *reinterpret_cast<float4 *>(f32_at(token, ch * CW + j)) =
-                  make_float4(l[ch][j], l[ch][j + 1], l[ch][j + 2], l[ch][j + 3]);
-          __syncwarp();
           float sums[G::CH];
 #pragma unroll
           for (int ch = 0; ch < G::CH; ++ch) {
+#pragma unroll
+            for (int j = 0; j < CW; j += 4)
+              *reinterpret_cast<float4 *>(f32_at(token, j)) =
+                  make_float4(l[ch][j], l[ch][j + 1], l[ch][j + 2], l[ch][j + 3]);
+            __syncwarp();
             sums[ch] = 0.0f;
 #pragma unroll 4
-            for (int i = 0; i < 32; ++i)
-              sums[ch] += *f32_at(quarter * 32 + i, ch * CW + lane % CW);
+            for (int i = 0; i < 32; ++i) sums[ch] += *f32_at(quarter * 32 + i, lane % CW);
+            __syncwarp();
           }
-          __syncwarp();
 #pragma unroll
           for (int ch = 0; ch < G::CH; ++ch)
-            if (lane < CW) *f32_at(quarter * 32, ch * CW + lane) = sums[ch];
+            if (lane < CW) *f32_at(quarter * 32 + ch, lane) = sums[ch];
         }
         // `other` is free once its last reader has given this set's O back
         if (!last && uses[set]) ok = ok && warp_wait(&ctl->o_free[set], (uses[set] - 1) & 1, abort);
@@ -1026,8 +1045,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         for (int ch = 0; ch < G::CH; ++ch) {
           const int c0 = c_group + ch * CW, col = c0 + lane;
           if (col >= rows) continue;
-          const int j = ch * CW + lane;
-          float sum = (*f32_at(0, j) + *f32_at(32, j)) + (*f32_at(64, j) + *f32_at(96, j));
+          float sum = (*f32_at(ch, lane) + *f32_at(32 + ch, lane)) +
+                      (*f32_at(64 + ch, lane) + *f32_at(96 + ch, lane));
           float ref = unset[ch] >> lane & 1 ? -INFINITY : -nm[col];
           if (!last) {
             ctl->other[0][col] = ref;
@@ -1079,14 +1098,14 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           for (int i = 0; i < 16; ++i) x[i] = 0.0f;
 #pragma unroll 1
           for (int y = 0; y < (both ? 2 : 1); ++y) {  // this set's O, and the other's
-            const uint32_t from = tmem_o + (y ? other : set) * 2 * NT + lanes + c0;
+            const uint32_t from = tmem_o + (y ? other : set) * G::PARTS * NT + lanes + c0;
             const float4 *f = reinterpret_cast<const float4 *>((y ? ctl->other[1] : nm) + c0);
-            uint32_t o[16], o_lo[16];
+            uint32_t o[16], o_lo[16] = {};
             tc::tmem_ld16(from, o);
-            tc::tmem_ld16(from + NT, o_lo);
+            if constexpr (G::PARTS == 2) tc::tmem_ld16(from + NT, o_lo);
             tc::tmem_wait_ld();
             tc::reg_fence(o);
-            tc::reg_fence(o_lo);
+            if constexpr (G::PARTS == 2) tc::reg_fence(o_lo);
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
               const float4 g = f[i / 4];
@@ -1108,7 +1127,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
                                    (pos & ((1 << a.page_shift) - 1)) * a.token_bytes +
                                    s.h * a.head_bytes;
               if constexpr (G::FP8)
-                v = __uint_as_float(widen_e4m3x2(src[d]) << 16);
+                v = __half2float(__ushort_as_half((unsigned short)widen_e4m3x2(src[d])));
               else
                 v = __bfloat162float(reinterpret_cast<const bf16 *>(src)[d]);
             }
@@ -1179,54 +1198,106 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
   } else if (warp >= 4 + G::SW) {
     if constexpr (G::FP8) {
     fewer_registers<G::REGS_WIDEN>();
-    // --------------------------------------- 8-bit tiles widened to bf16 ----
-    const int w = warp - 4 - G::SW;
-    int slot = 0, raw = 0;
-    uint32_t phase = 0, raw_phase = 0;
-    constexpr int PARTS = D / 16;  // 16-byte parts of a raw row
-    for (int f = 0;; ++f) {
-      if (!warp_wait(&ctl->rfull[raw], raw_phase, abort) ||
-          f == *(volatile int *)&ctl->raw_end || !warp_wait(&ctl->empty[slot], phase ^ 1, abort))
-        break;
-      const uint8_t *src = raws + raw * G::RAW;
-      uint8_t *dst = slots + slot * G::SLOT;
-      // eight lanes take eight tokens: the swizzles spread both sides over all banks
-      const int token = (w & 3) * 32 + lane;  // eight warps: two for a token's parts
-      // raw rows of 128 bytes are swizzled by token & 7, of 64 bytes by (token >> 1) & 3
-      const int raw_x = D == 128 ? token & 7 : (token >> 1) & 3;
+      // ------------------------- 8-bit tiles, and Q, made f16 -------------
+      const int w = warp - 4 - G::SW, token = w * 32 + lane;
+      int slot = 0, raw = 0;
+      uint32_t phase = 0, raw_phase = 0;
+      bool ok = true;
+      for (uint32_t seg = 0; ok; ++seg) {
+        ok = warp_wait(&ctl->seg_full[seg % SEGS], (seg / SEGS) & 1, abort);
+        if (!ok) break;
+        const int tiles = ctl->seg[seg % SEGS].te - ctl->seg[seg % SEGS].tb;
+        const int rows = ctl->seg[seg % SEGS].nodes * a.group;
+        if (tiles == 0) break;
+        // Q's tile in place, times the power of two that brings its largest finite
+        // value to 2^14; rows that nothing uses stay as they are
+        ok = warp_wait(&ctl->q_full[seg % G::QS], (seg / G::QS) & 1, abort);
+        if (!ok) break;
+        uint8_t *q = sq + seg % G::QS * G::Q_ONE;
+        int most = 0;  // bf16 bits without the sign: ordered as numbers
+#pragma unroll 1
+        for (int i = token; i < rows * HALVES * 8; i += 128) {
+          const int row = i / (HALVES * 8), part = i % (HALVES * 8);
+          const uint4 x = *reinterpret_cast<const uint4 *>(
+              q + (part / 8) * NT * 128 + row * 128 + part % 8 * 16);
+          const uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int i0 = 0; i0 < PARTS * 4 / G::CV; ++i0) {
-        const int p = (G::CV / 4) * i0 + (w >> 2);
-        const uint4 x = *reinterpret_cast<const uint4 *>(src + token * D + ((p ^ raw_x) * 16));
-        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-        uint32_t o[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          o[2 * i] = widen_e4m3x2(v[i] & 0xffffu);
-          o[2 * i + 1] = widen_e4m3x2(v[i] >> 16);
+          for (int k = 0; k < 4; ++k) {
+            const int lo = v[k] & 0x7fff, hi = v[k] >> 16 & 0x7fff;
+            most = max(most, max(lo < 0x7f80 ? lo : 0, hi < 0x7f80 ? hi : 0));
+          }
         }
-        uint8_t *row = dst + (p / 4) * HALF_BYTES + token * 128;
-        const int c = (2 * p) % 8;
-        *reinterpret_cast<uint4 *>(row + ((c ^ (token & 7)) * 16)) =
-            make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4 *>(row + (((c + 1) ^ (token & 7)) * 16)) =
-            make_uint4(o[4], o[5], o[6], o[7]);
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) ctl->q_top[w] = most;
+        group_sync(5);
+        most = max(max(ctl->q_top[0], ctl->q_top[1]), max(ctl->q_top[2], ctl->q_top[3]));
+        // its exponent is (most >> 7) - 127; a subnormal's is taken as the least
+        const int up = most ? 14 + 127 - max(most >> 7, 1) : 0;
+#pragma unroll 1
+        for (int i = token; i < rows * HALVES * 8; i += 128) {
+          const int row = i / (HALVES * 8), part = i % (HALVES * 8);
+          uint4 *at = reinterpret_cast<uint4 *>(q + (part / 8) * NT * 128 + row * 128 +
+                                                part % 8 * 16);
+          const uint4 x = *at;
+          const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+          // in two steps: 2^up alone may pass f32's range
+          const float f = ldexpf(1.0f, up / 2), g = ldexpf(1.0f, up - up / 2);
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const __half2 h = __floats2half2_rn(bf16_lo(v[k]) * f * g, bf16_hi(v[k]) * f * g);
+            o[k] = *reinterpret_cast<const uint32_t *>(&h);
+          }
+          *at = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        if (w == 0 && lane == 0) ctl->q_exp[seg % G::QS] = up;
+        tc::fence_async_smem();
+        group_sync(5);  // q_top is read
+        if (lane == 0) tc::mbar_arrive(&ctl->q_ready[seg % G::QS]);
+        if (w == 0 && lane == 0) tc::mbar_arrive(&ctl->seg_empty[seg % SEGS]);
+#pragma unroll 1
+        for (int fill = 0; fill < 2 * tiles; ++fill) {
+          ok = warp_wait(&ctl->rfull[raw], raw_phase, abort) &&
+               warp_wait(&ctl->empty[slot], phase ^ 1, abort);
+          if (!ok) break;
+          const uint8_t *src = raws + raw * G::RAW;
+          uint8_t *dst = slots + slot * G::SLOT;
+          // eight lanes take eight tokens: the swizzles spread both sides over all
+          // banks (raw rows of 128 bytes by token & 7, of 64 bytes by (token >> 1) & 3)
+          const int raw_x = D == 128 ? token & 7 : (token >> 1) & 3;
+#pragma unroll
+          for (int p = 0; p < D / 16; ++p) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(src + token * D + ((p ^ raw_x) * 16));
+            const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              o[2 * i] = widen_e4m3x2(v[i] & 0xffffu);
+              o[2 * i + 1] = widen_e4m3x2(v[i] >> 16);
+            }
+            uint8_t *row = dst + (p / 4) * HALF_BYTES + token * 128;
+            const int c = (2 * p) % 8;
+            *reinterpret_cast<uint4 *>(row + ((c ^ (token & 7)) * 16)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(row + (((c + 1) ^ (token & 7)) * 16)) =
+                make_uint4(o[4], o[5], o[6], o[7]);
+          }
+          tc::fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tc::mbar_arrive(&ctl->full[slot]);
+            tc::mbar_arrive(&ctl->rempty[raw]);
+          }
+          if (++slot == SLOTS) {
+            slot = 0;
+            phase ^= 1;
+          }
+          if (++raw == RAWS) {
+            raw = 0;
+            raw_phase ^= 1;
+          }
+        }
       }
-      tc::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tc::mbar_arrive(&ctl->full[slot]);
-        tc::mbar_arrive(&ctl->rempty[raw]);
-      }
-      if (++slot == SLOTS) {
-        slot = 0;
-        phase ^= 1;
-      }
-      if (++raw == RAWS) {
-        raw = 0;
-        raw_phase ^= 1;
-      }
-    }
     }
   }
 
