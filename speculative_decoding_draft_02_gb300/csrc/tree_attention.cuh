@@ -1265,10 +1265,13 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           // eight lanes take eight tokens: the swizzles spread both sides over all
           // banks (raw rows of 128 bytes by token & 7, of 64 bytes by (token >> 1) & 3)
           const int raw_x = D == 128 ? token & 7 : (token >> 1) & 3;
+          uint4 x[D / 16];  // all read before the first is written: they might overlap
+#pragma unroll
+          for (int p = 0; p < D / 16; ++p)
+            x[p] = *reinterpret_cast<const uint4 *>(src + token * D + ((p ^ raw_x) * 16));
 #pragma unroll
           for (int p = 0; p < D / 16; ++p) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(src + token * D + ((p ^ raw_x) * 16));
-            const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+            const uint32_t v[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
             uint32_t o[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
