@@ -101,23 +101,24 @@ struct Geo {
   // that widen.  The softmax keeps a column's sums and scores in registers, more of
   // them than a thread's share: the others give theirs up.
   static constexpr int THREADS = 32 * (4 + SW + CV);
-  static constexpr int REGS_FEW = FP8 ? 72 : 88, REGS_SOFTMAX = FP8 ? 176 : 208, REGS_WIDEN = 88;
+  static constexpr int REGS_FEW = FP8 ? 72 : 88, REGS_SOFTMAX = FP8 ? 168 : 208, REGS_WIDEN = 104;
   static_assert(SW == 8 && (CV == 0 || CV == 4), "warps 4..11: the softmax");
   static_assert(REGS_FEW + 2 * REGS_SOFTMAX + (FP8 ? REGS_WIDEN : 0) <=
                     65536 / THREADS / 8 * 8 * (THREADS / 128),
                 "a block's registers");
   static constexpr int SLOT = BT * D * 2;
   // Q of the next segment beside the present one's, where two sets leave room
-  static constexpr int QS = SETS;
+  static constexpr int QS = FP8 && NT == 64 ? 1 : SETS;
   static constexpr int Q_ONE = NT * D * 2, Q_BYTES = QS * Q_ONE;
   static constexpr int P_SET = BT * 128 * (PARTS * NT > 64 ? PARTS * NT / 64 : 1);
   static constexpr int P_BYTES = SETS * P_SET;
   static constexpr int ROOM = SMEM_LIMIT - CTL_BYTES - Q_BYTES - P_BYTES;
   static constexpr int RAW = FP8 ? BT * D : 0;
-  // 8-bit: three widened tiles (one read by each product, one being written);
-  // the copies in flight are the raw ring's
-  static constexpr int SLOTS = FP8 ? 3 : (ROOM / SLOT < MAX_SLOTS ? ROOM / SLOT : MAX_SLOTS);
-  static constexpr int RAWS_FIT = FP8 ? (ROOM - 3 * SLOT) / (RAW + !FP8) : 0;
+  // 8-bit: four widened tiles where they leave room for three of the copies in flight
+  // (two read by the products, two being written), else three
+  static constexpr int SLOTS = FP8 ? (4 * SLOT + 3 * RAW <= ROOM ? 4 : 3)
+                                   : (ROOM / SLOT < MAX_SLOTS ? ROOM / SLOT : MAX_SLOTS);
+  static constexpr int RAWS_FIT = FP8 ? (ROOM - SLOTS * SLOT) / (RAW + !FP8) : 0;
   static constexpr int RAWS = RAWS_FIT < MAX_SLOTS ? RAWS_FIT : MAX_SLOTS;
   static constexpr int SMEM_BYTES = SLOTS * SLOT + RAWS * RAW + Q_BYTES + P_BYTES + CTL_BYTES;
   // two tiles of S, and each set's O in its parts
@@ -569,7 +570,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       int k_slot = 0, v_slot = 1;
       uint32_t k_phase = 0, v_phase = 0, t = 0, pv = 0, seg = 0;
       uint32_t acc = 0;  // whether the pending tile adds to O
-      uint32_t uses[2] = {0, 0};  // segments that each set had a part in
+      uint32_t uses0 = 0, uses1 = 0;  // segments that each set had a part in
       auto advance = [&](int &slot, uint32_t &phase) {
         slot += 2;
         if (slot >= SLOTS) {
@@ -624,8 +625,10 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           ok = warp_wait(&ctl->full[v_slot], v_phase, abort) &&
                warp_wait(&ctl->p_full[x], (pv / G::SETS) & 1, abort);
           if (ok && G::SETS == 2 && !acc) {  // a segment's first: its last O there is read
-            ok = uses[x] == 0 || warp_wait(&ctl->o_free[x], (uses[x] - 1) & 1, abort);
-            ++uses[x];
+            const uint32_t before = x ? uses1 : uses0;
+            ok = before == 0 || warp_wait(&ctl->o_free[x], (before - 1) & 1, abort);
+            uses0 += x == 0;
+            uses1 += x;
           }
           if (!ok) break;
           tc::fence_after_sync();
@@ -695,7 +698,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     };
     uint32_t t0 = 0, seg = 0;   // the segment's first tile, of all of the share's
     uint32_t mine = 0;          // tiles that this set has taken
-    uint32_t uses[2] = {0, 0}, helped[2] = {0, 0};  // segments that a set had part in; as first
+    uint32_t uses = 0, helped = 0;  // segments that this set had a part in; that the other helped
     int q_last = -1;            // the last segment whose Q this thread has copied
     bool ok = true, gone = false;
     auto segment_here = [&](uint32_t i) {
@@ -793,20 +796,17 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           for (;; again = 1) {
             float most = -INFINITY;
             if (ok) {
+              uint32_t sr[CW];
+              tc::tmem_ld(tmem + lanes + b * NT + c0, sr);
+              tc::tmem_wait_ld();
+              tc::reg_fence(sr);
 #pragma unroll
-              for (int h = 0; h < CW; h += 16) {
-                uint32_t sr[16];
-                tc::tmem_ld16(tmem + lanes + b * NT + c0 + h, sr);
-                tc::tmem_wait_ld();
-                tc::reg_fence(sr);
-#pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                  const float4 m = *reinterpret_cast<const float4 *>(&nm[c0 + h + j]);
-                  e[h + j] = fmaf(__uint_as_float(sr[j]), c, m.x);
-                  e[h + j + 1] = fmaf(__uint_as_float(sr[j + 1]), c, m.y);
-                  e[h + j + 2] = fmaf(__uint_as_float(sr[j + 2]), c, m.z);
-                  e[h + j + 3] = fmaf(__uint_as_float(sr[j + 3]), c, m.w);
-                }
+              for (int j = 0; j < CW; j += 4) {
+                const float4 m = *reinterpret_cast<const float4 *>(&nm[c0 + j]);
+                e[j] = fmaf(__uint_as_float(sr[j]), c, m.x);
+                e[j + 1] = fmaf(__uint_as_float(sr[j + 1]), c, m.y);
+                e[j + 2] = fmaf(__uint_as_float(sr[j + 2]), c, m.z);
+                e[j + 3] = fmaf(__uint_as_float(sr[j + 3]), c, m.w);
               }
               if (edge) {
 #pragma unroll
@@ -1025,10 +1025,10 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
             if (lane < CW) *f32_at(quarter * 32 + ch, lane) = sums[ch];
         }
         // `other` is free once its last reader has given this set's O back
-        if (!last && uses[set]) ok = ok && warp_wait(&ctl->o_free[set], (uses[set] - 1) & 1, abort);
+        if (!last && uses) ok = ok && warp_wait(&ctl->o_free[set], (uses - 1) & 1, abort);
         if (last && both) {
           const uint32_t theirs = (t0 + n_tiles + (other ^ 1)) / 2;  // tiles of the other set
-          ok = ok && warp_wait(&ctl->half[other], helped[other] & 1, abort) &&
+          ok = ok && warp_wait(&ctl->half[other], helped & 1, abort) &&
                warp_wait(&ctl->pv_done[other], (theirs - 1) & 1, abort);
         }
         if (group_any(bar, !ok)) {
@@ -1183,9 +1183,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       }
       __syncwarp();
       if (quarter == 0 && lane == 0) tc::mbar_arrive(&ctl->seg_empty[seg % SEGS]);
-      uses[set] += part;
-      uses[other] += both || !part;
-      helped[other] += last && both;
+      uses += part;
+      helped += last && both;
       t0 += n_tiles;
       ++seg;
     }
