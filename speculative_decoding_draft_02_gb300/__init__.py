@@ -496,6 +496,70 @@ def workspace(nbytes: int, device="cuda") -> torch.Tensor:
     return t
 
 
+class PagePool:
+    """The pages of R requests over any number of layers' caches, on the device: who
+    holds which, and one round's rows (no allocation per call).
+
+    `ctx` holds the committed tokens, -1 for a free place; a request enters when its
+    prompt's rows are planned with ctx 0, and leaves when its ctx is set to -1 (its
+    pages go back with the next plan)."""
+
+    def __init__(self, R, n_pages, page_size, max_tokens, n_rows, device="cuda"):
+        new = lambda shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device=device)  # noqa: E731
+        self.page_size, self.n_rows = page_size, n_rows
+        max_pages = -(-max_tokens // page_size)
+        self.ctx = torch.full((R,), -1, dtype=torch.int32, device=device)
+        self.held = torch.zeros((R,), dtype=torch.int32, device=device)
+        self.free_pages = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device)
+        self.n_free = torch.tensor([n_pages], dtype=torch.int32, device=device)
+        self.block_table = torch.full((R, max_pages), -1, dtype=torch.int32, device=device)
+        self.row_start, self.position = new(R + 1), new(n_rows)
+        self.slot, self.anc = new(n_rows, torch.int64), new(n_rows, torch.int64)
+        self.accepted, self.bonus, self.ctx_before = new(R), new(R), new(R)
+        self._ws = {}
+
+    def plan(self, length, extra=1, parent=None, stream=None):
+        """Rows, pages, slots, positions (and masks, in a round) for `length` + extra new
+        rows of each request: extra 1 in a round, 0 for prompts."""
+        dspark_kv_plan(self.ctx, length, extra, parent, self.page_size, self.held, self.n_free,
+                       self.free_pages, self.block_table, self.held, self.n_free,
+                       self.row_start, self.position, self.slot, self.anc if extra else None,
+                       stream)
+
+    def append(self, cache: KVCache, k, v, stream=None):
+        """One layer's new rows into the planned slots."""
+        dspark_kv_append(cache, k, v, self.slot, stream)
+
+    def attend(self, cache: KVCache, q, max_nodes, out, lse=None, scale=None, stream=None):
+        """One layer's attention of a round's rows over contexts and trees."""
+        need = dspark_tree_attention_workspace_bytes(cache, len(self.ctx), q.shape[1], max_nodes)
+        ws = self._ws.get(need)
+        if ws is None:  # once for each size: kept, as a captured graph would need it
+            ws = self._ws[need] = workspace(need, q.device)
+        if stream is not None:
+            ws.record_stream(stream)
+        dspark_tree_attention(cache, q, self.ctx, self.row_start, self.anc, self.block_table,
+                              max_nodes, cache.dim ** -0.5 if scale is None else scale, out, lse,
+                              ws, stream)
+
+    def commit(self, rows):
+        """`rows` of each request's new rows are committed: after dspark_verify the anchor
+        and the accepted drafts (accepted + 1), after a prompt its length."""
+        self.ctx += torch.where(self.ctx >= 0, rows, 0)
+
+    def accept(self, tokens, choice, path, parent=None, stream=None):
+        """The trees' confirmed paths (into `path` [R, gamma], self.accepted, self.bonus);
+        commits them.  Each layer's cache then needs compact()."""
+        s = stream if stream is not None else torch.cuda.current_stream()
+        with torch.cuda.stream(s):
+            self.ctx_before.copy_(self.ctx)
+        dspark_tree_accept(self.row_start, parent, tokens, choice, self.ctx, self.accepted,
+                           self.bonus, path, self.ctx, stream)
+
+    def compact(self, cache: KVCache, path, stream=None):
+        dspark_kv_compact(cache, self.ctx_before, self.accepted, path, self.block_table, stream)
+
+
 @dataclass
 class DraftHead:
     """Device-resident draft-head weights in the library's layouts."""

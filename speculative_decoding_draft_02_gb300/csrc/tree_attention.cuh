@@ -92,7 +92,10 @@ struct Geo {
   // leave no room for a second P and O: one set of two groups, each with half the
   // columns.
   static constexpr int SETS = NT <= 64 ? 2 : 1;
-  static constexpr int CW = NT < 32 ? NT : 32;       // columns of a softmax thread's chunk
+  // Columns of a softmax thread's chunk: 16 beside an 8-bit cache from 64 on, where 32
+  // and their sums did not fit the registers left (36 rows over four contexts of 33 to
+  // 131 thousand tokens: 243 against 260 us; 64 rows beside a bf16 cache: 363 against 340).
+  static constexpr int CW = NT < 32 || (FP8 && NT >= 64) ? 16 : 32;
   static constexpr int CG = SETS == 2 ? 1 : 2;       // groups of four warps in a set
   static constexpr int CH = NT / (CW * CG);          // chunks of a thread
   static constexpr int SW = 4 * CG * SETS;
