@@ -167,54 +167,51 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) kv_plan_kernel(const PlanArgs
   __syncwarp();
   cluster_or_block_sync(ctas > 1);
 
-  // pages: a warp takes a request.  Those covered by the stack are the first
-  // ones, so what is left of it is known from the first request without.
-  for (int r = warp; r < a.R; r += warps) {
-    const int h = held[r], first = need_off[r], need = need_off[r + 1] - first;
-    const bool granted = need_off[r + 1] <= top;
-    int *table = a.block_table + (size_t)r * a.max_pages;
-    for (int j = lane; j < need; j += 32)
-      table[h + j] = granted ? a.free_pages[top - 1 - first - j] : -1;
-    if (lane == 0) {
-      a.held_out[r] = a.ctx[r] < 0 ? 0 : h + (granted ? need : 0);
-      if (!granted && need) dspark_set_status(DSPARK_ERR_PAGES);
-      // the one request whose need crosses the stack's end, or the last of all
-      if (granted ? r == a.R - 1 : first <= top)
-        a.n_free_out[0] = top - (granted ? need_off[r + 1] : first);
-    }
-  }
-  // slot of request r's position: a held page from the table, a new one from the
-  // stack (the table's entry may not be written yet)
-  auto slot_of = [&](int r, int64_t pos) -> int64_t {
-    const int64_t p = pos >> a.page_shift;
-    const int h = held[r], first = need_off[r], need = need_off[r + 1] - first;
-    int page = -1;
-    if (p < h)
-      page = a.block_table[(size_t)r * a.max_pages + p];
-    else if (p - h < need && need_off[r + 1] <= top)
-      page = a.free_pages[top - 1 - first - (int)(p - h)];
-    if (page < 0 || page >= a.n_pages) return -1;
-    return ((int64_t)page << a.page_shift) + (pos & (ps - 1));
-  };
-  if (a.parent) {
-    // trees: a warp takes a request, a lane nodes l and l + 32.  Ancestor masks
-    // by doubling: after k rounds a node knows 2^k levels up.
-    for (int r = warp; r < a.R; r += warps) {
-      const int row0 = row_off[r], n = row_off[r + 1] - row0;
+  // A warp takes a request: its new pages, what it then holds, and in a tree its
+  // rows.  The lanes read 32 of the warp's requests' lengths at once.
+  for (int at = warp; at < a.R; at += 32 * warps) {
+    const int mine_r = at + lane * warps;
+    const int mine_ctx = mine_r < a.R ? a.ctx[mine_r] : -1;
+    for (int k = 0; k < 32 && at + k * warps < a.R; ++k) {
+      const int r = at + k * warps, c = __shfl_sync(0xffffffffu, mine_ctx, k);
+      const int h = held[r], first = need_off[r], need = need_off[r + 1] - first;
+      // the requests that the stack covers come first, so what is left of it is
+      // known from the first one without
+      const bool granted = need_off[r + 1] <= top;
+      int *table = a.block_table + (size_t)r * a.max_pages;
+      const int row0 = row_off[r], n = a.parent ? row_off[r + 1] - row0 : 0;
+      // what the tree needs is asked for before anything is waited for: a node's
+      // parent, and the page of its place
+      int up[2] = {0, 0}, page[2] = {-1, -1};
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int node = lane + 32 * q;
+        if (node < n) {
+          if (node > 0) up[q] = a.parent[(size_t)r * a.gamma + node - 1];
+          const int64_t p = ((int64_t)c + node) >> a.page_shift;
+          if (p < h) page[q] = table[p];
+          else if (p - h < need && granted) page[q] = a.free_pages[top - 1 - first - (int)(p - h)];
+        }
+      }
+      for (int j = lane; j < need; j += 32)
+        table[h + j] = granted ? a.free_pages[top - 1 - first - j] : -1;
+      if (lane == 0) {
+        a.held_out[r] = c < 0 ? 0 : h + (granted ? need : 0);
+        if (!granted && need) dspark_set_status(DSPARK_ERR_PAGES);
+        // the one request whose need crosses the stack's end, or the last of all
+        if (granted ? r == a.R - 1 : first <= top)
+          a.n_free_out[0] = top - (granted ? need_off[r + 1] : first);
+      }
       if (n == 0) continue;
-      const int c = a.ctx[r];
-      const int *par = a.parent + (size_t)r * a.gamma - 1;  // par[node]
-      int up[2];
+      // ancestor masks by doubling: after i rounds a node knows 2^i levels up
       unsigned long long bits[2];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const int node = lane + 32 * q;
-        int p = node > 0 && node < n ? par[node] : 0;
-        if (p < 0 || (node > 0 && p >= node)) {
+        if (up[q] < 0 || (node > 0 && up[q] >= node)) {
           dspark_set_status(DSPARK_ERR_ARG);
-          p = 0;
+          up[q] = 0;
         }
-        up[q] = p;
         bits[q] = 1ull << node;
       }
       for (int levels = 1; levels < n; levels *= 2) {
@@ -231,18 +228,39 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) kv_plan_kernel(const PlanArgs
         }
         bits[0] |= lo0;
         up[0] = u0;
+        if (!__any_sync(0xffffffffu, up[0] | up[1])) {  // every chain has reached the anchor
+          bits[0] |= 1;
+          bits[1] |= 1;
+          break;
+        }
       }
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const int node = lane + 32 * q;
         if (node < n) {
+          const int64_t pos = (int64_t)c + node;
           a.position[row0 + node] = c + __popcll(bits[q]) - 1;
-          a.slot[row0 + node] = slot_of(r, (int64_t)c + node);
+          a.slot[row0 + node] = page[q] < 0 || page[q] >= a.n_pages
+                                    ? -1
+                                    : ((int64_t)page[q] << a.page_shift) + (pos & (ps - 1));
           if (a.anc) a.anc[row0 + node] = bits[q];
         }
       }
     }
   }
+  // slot of request r's position: a held page from the table, a new one from the
+  // stack (the table's entry may not be written yet)
+  auto slot_of = [&](int r, int64_t pos) -> int64_t {
+    const int64_t p = pos >> a.page_shift;
+    const int h = held[r], first = need_off[r], need = need_off[r + 1] - first;
+    int page = -1;
+    if (p < h)
+      page = a.block_table[(size_t)r * a.max_pages + p];
+    else if (p - h < need && need_off[r + 1] <= top)
+      page = a.free_pages[top - 1 - first - (int)(p - h)];
+    if (page < 0 || page >= a.n_pages) return -1;
+    return ((int64_t)page << a.page_shift) + (pos & (ps - 1));
+  };
   // chains: a thread takes a row, its request by search; then the padding
   for (int i = (a.parent ? total : 0) + cta * PLAN_THREADS + tid; i < a.n_rows;
        i += ctas * PLAN_THREADS) {
@@ -297,50 +315,68 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
-// A thread moves 16 values of one head of one row (two 16-byte loads; two
-// 16-byte stores, or one of 8-bit values).  Units of K and V of one row are
-// neighbours, so a warp's accesses are whole lines of one row.
+// A thread moves 16 values of one head (two 16-byte loads; two 16-byte stores, or
+// one of 8-bit values) of every so many rows: its place in a row is found once.
+// Places of one row are neighbours, so a warp's accesses are whole lines.
+constexpr int APPEND_THREADS = 256, APPEND_ROWS = 2;
+
 template <bool FP8>
-__global__ void __launch_bounds__(256) kv_append_kernel(const CacheView c, int n_rows,
-                                                        const bf16 *__restrict__ k,
-                                                        const bf16 *__restrict__ v,
-                                                        int64_t row_stride, int64_t head_stride,
-                                                        const int64_t *__restrict__ slot) {
+__global__ void __launch_bounds__(APPEND_THREADS)
+    kv_append_kernel(const CacheView c, int n_rows, const bf16 *__restrict__ k,
+                     const bf16 *__restrict__ v, int64_t row_stride, int64_t head_stride,
+                     const int64_t *__restrict__ slot) {
   pdl_trigger();
   pdl_wait();
-  const int units_head = c.dim / 16, units = 2 * c.heads * units_head;
-  const int64_t all = (int64_t)n_rows * units;
+  const int per_head = c.dim / 16, units = 2 * c.heads * per_head;
+  const int at_once = max(1, APPEND_THREADS / units);  // rows of a block's pass
   const int64_t n_slots = (int64_t)c.n_pages << c.page_shift;
-  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < all; u += (int64_t)gridDim.x * 256) {
-    const int64_t row = u / units;
-    int e = (int)(u - row * units);
-    const int64_t s = slot[row];
-    if (s < 0) continue;
-    if (s >= n_slots) {
-      dspark_set_status(DSPARK_ERR_PAGES);
-      continue;
-    }
-    const bool is_v = e >= units / 2;
-    if (is_v) e -= units / 2;
-    const int head = e / units_head, part = e - head * units_head;
-    const uint4 *src = reinterpret_cast<const uint4 *>((is_v ? v : k) + row * row_stride +
-                                                       head * head_stride + part * 16);
-    const uint4 x = src[0], y = src[1];
-    uint8_t *dst = (is_v ? c.v : c.k) + (s >> c.page_shift) * c.page_bytes +
-                   (s & ((1 << c.page_shift) - 1)) * c.token_bytes + head * c.head_bytes;
-    if constexpr (FP8) {
-      const float *scales = is_v ? c.v_scale : c.k_scale;
-      const float scale = scales ? scales[head] : 1.0f;
-      const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-      uint32_t o[4];
+  const int64_t rows_pass = (int64_t)gridDim.x * at_once;
+  const int unit0 = threadIdx.x % units, sub = threadIdx.x / units;
+  if (sub >= at_once && units <= APPEND_THREADS) return;
+  for (int unit = units <= APPEND_THREADS ? unit0 : threadIdx.x; unit < units;
+       unit += APPEND_THREADS) {
+    const bool is_v = unit >= units / 2;
+    const int e = is_v ? unit - units / 2 : unit, head = e / per_head, part = e - head * per_head;
+    const bf16 *src = (is_v ? v : k) + head * head_stride + part * 16;
+    uint8_t *dst = (is_v ? c.v : c.k) + head * c.head_bytes + part * (FP8 ? 16 : 32);
+    const float *scales = is_v ? c.v_scale : c.k_scale;
+    const float scale = FP8 && scales ? scales[head] : 1.0f;
+    const int64_t row0 = (int64_t)blockIdx.x * at_once + (units <= APPEND_THREADS ? sub : 0);
+    for (int64_t row = row0; row < n_rows; row += APPEND_ROWS * rows_pass) {
+      uint4 x[APPEND_ROWS], y[APPEND_ROWS];
+      int64_t s[APPEND_ROWS];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        o[i] = pack_e4m3x2(bf16_lo(w[2 * i]) / scale, bf16_hi(w[2 * i]) / scale) |
-               pack_e4m3x2(bf16_lo(w[2 * i + 1]) / scale, bf16_hi(w[2 * i + 1]) / scale) << 16;
-      reinterpret_cast<uint4 *>(dst)[part] = make_uint4(o[0], o[1], o[2], o[3]);
-    } else {
-      reinterpret_cast<uint4 *>(dst)[2 * part] = x;
-      reinterpret_cast<uint4 *>(dst)[2 * part + 1] = y;
+      for (int i = 0; i < APPEND_ROWS; ++i) {  // every row's loads before the first's stores
+        const int64_t m = row + i * rows_pass;
+        s[i] = m < n_rows ? slot[m] : -1;
+        if (m < n_rows) {
+          const uint4 *p = reinterpret_cast<const uint4 *>(src + m * row_stride);
+          x[i] = p[0];
+          y[i] = p[1];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < APPEND_ROWS; ++i) {
+        if (s[i] < 0) continue;
+        if (s[i] >= n_slots) {
+          dspark_set_status(DSPARK_ERR_PAGES);
+          continue;
+        }
+        uint4 *to = reinterpret_cast<uint4 *>(dst + (s[i] >> c.page_shift) * c.page_bytes +
+                                              (s[i] & ((1 << c.page_shift) - 1)) * c.token_bytes);
+        if constexpr (FP8) {
+          const uint32_t w[8] = {x[i].x, x[i].y, x[i].z, x[i].w, y[i].x, y[i].y, y[i].z, y[i].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            o[j] = pack_e4m3x2(bf16_lo(w[2 * j]) / scale, bf16_hi(w[2 * j]) / scale) |
+                   pack_e4m3x2(bf16_lo(w[2 * j + 1]) / scale, bf16_hi(w[2 * j + 1]) / scale) << 16;
+          *to = make_uint4(o[0], o[1], o[2], o[3]);
+        } else {
+          to[0] = x[i];
+          to[1] = y[i];
+        }
+      }
     }
   }
 }
@@ -548,8 +584,10 @@ extern "C" int dspark_kv_append(const dspark_kv_cache *cache, int32_t n_rows, co
   if (((uintptr_t)k | (uintptr_t)v) & 15 || row_stride <= 0 || head_stride <= 0 ||
       row_stride % 8 || head_stride % 8)
     return DSPARK_ERR_ARG;
-  const int64_t units = (int64_t)n_rows * 2 * cache->heads * (cache->dim / 16);
-  const int64_t blocks = (units + 255) / 256, most = (int64_t)dspark_sm_count() * 32;
+  const int units = 2 * cache->heads * (cache->dim / 16);
+  const int64_t at_once = units < APPEND_THREADS ? APPEND_THREADS / units : 1;
+  const int64_t blocks = (n_rows + at_once - 1) / at_once;
+  const int64_t most = (int64_t)dspark_sm_count() * 32;
   const dim3 grid((unsigned)(blocks < most ? blocks : most));
   const CacheView c = view_of(cache);
   const cudaError_t e =

@@ -19,6 +19,7 @@ int row_tile(const dspark_kv_cache *c, int heads_q, int max_nodes) {
   const int rows = max_nodes * (heads_q / c->heads);
   if (rows <= 16) return 16;
   if (rows <= 32) return 32;
+  if (rows <= 48) return 48;
   return rows <= 64 ? 64 : 128;
 }
 
@@ -92,6 +93,7 @@ template <int TYPE, int D>
 int launch_tile(const Launch &l, int nt) {
   if (nt == 16) return launch<TYPE, D, 16>(l);
   if (nt == 32) return launch<TYPE, D, 32>(l);
+  if (nt == 48) return launch<TYPE, D, 48>(l);
   if (nt == 64) return launch<TYPE, D, 64>(l);
   return launch<TYPE, D, 128>(l);
 }

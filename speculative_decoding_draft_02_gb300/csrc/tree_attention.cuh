@@ -95,7 +95,7 @@ struct Geo {
   // Columns of a softmax thread's chunk: 16 beside an 8-bit cache from 64 on, where 32
   // and their sums did not fit the registers left (36 rows over four contexts of 33 to
   // 131 thousand tokens: 243 against 260 us; 64 rows beside a bf16 cache: 363 against 340).
-  static constexpr int CW = NT < 32 || (FP8 && NT >= 64) ? 16 : 32;
+  static constexpr int CW = NT % 32 || (FP8 && NT >= 64) ? 16 : 32;
   static constexpr int CG = SETS == 2 ? 1 : 2;       // groups of four warps in a set
   static constexpr int CH = NT / (CW * CG);          // chunks of a thread
   static constexpr int SW = 4 * CG * SETS;
@@ -104,16 +104,16 @@ struct Geo {
   // that widen.  The softmax keeps a column's sums and scores in registers, more of
   // them than a thread's share: the others give theirs up.
   static constexpr int THREADS = 32 * (4 + SW + CV);
-  static constexpr int REGS_FEW = FP8 ? 72 : 88, REGS_SOFTMAX = FP8 ? 168 : 208, REGS_WIDEN = 104;
+  static constexpr int REGS_FEW = 40, REGS_SOFTMAX = FP8 ? 208 : 232, REGS_WIDEN = 56;
   static_assert(SW == 8 && (CV == 0 || CV == 4), "warps 4..11: the softmax");
   static_assert(REGS_FEW + 2 * REGS_SOFTMAX + (FP8 ? REGS_WIDEN : 0) <=
                     65536 / THREADS / 8 * 8 * (THREADS / 128),
                 "a block's registers");
   static constexpr int SLOT = BT * D * 2;
   // Q of the next segment beside the present one's, where two sets leave room
-  static constexpr int QS = FP8 && NT == 64 ? 1 : SETS;
+  static constexpr int QS = FP8 && NT > 32 ? 1 : SETS;
   static constexpr int Q_ONE = NT * D * 2, Q_BYTES = QS * Q_ONE;
-  static constexpr int P_SET = BT * 128 * (PARTS * NT > 64 ? PARTS * NT / 64 : 1);
+  static constexpr int P_SET = BT * 128 * ((PARTS * NT + 63) / 64);
   static constexpr int P_BYTES = SETS * P_SET;
   static constexpr int ROOM = SMEM_LIMIT - CTL_BYTES - Q_BYTES - P_BYTES;
   static constexpr int RAW = FP8 ? BT * D : 0;
@@ -235,10 +235,31 @@ __device__ __forceinline__ bool next_segment(Walker &w, Segment &s, const Args &
   return true;
 }
 
-// A quotient of two non-negative 64-bit numbers: a call, for its size.
-__device__ __noinline__ long long divide(long long x, long long y) {
-  if (((x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
-  return (long long)((unsigned long long)x / (unsigned long long)y);
+// 2^k in two factors, as 2^k alone may pass f32's range (|k| <= 252).
+__device__ __forceinline__ float times_power(float x, int k) {
+  const int half = k / 2;
+  return x * __int_as_float((127 + half) << 23) * __int_as_float((127 + k - half) << 23);
+}
+
+// Quotients of non-negative 64-bit numbers without the long division's code, which is
+// a call: by a divisor below 2^16, digit by digit; and a quotient below 2^20, by an
+// estimate that is at most one off.
+__device__ __forceinline__ long long divide_small(long long x, uint32_t d) {
+  uint32_t rest = 0;
+  long long q = 0;
+#pragma unroll 1
+  for (int i = 48; i >= 0; i -= 16) {
+    const uint32_t now = rest << 16 | ((uint32_t)(x >> i) & 0xffffu);
+    q = q << 16 | now / d;
+    rest = now % d;
+  }
+  return q;
+}
+__device__ __forceinline__ int quotient(long long x, long long y) {
+  int q = (int)__fdividef((float)x, (float)y);
+  if (q * y > x) --q;
+  if ((q + 1) * y <= x) ++q;
+  return q;
 }
 
 struct Ctl {
@@ -406,12 +427,12 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
   const int per = (a.R + G::THREADS - 1) / G::THREADS;
   const int r_lo = min((int)threadIdx.x * per, a.R), r_hi = min(r_lo + per, a.R);
   long long mine = 0;
+  Request own;  // the thread's only request, where it has one
 #pragma unroll 1
   for (int r = r_lo; r < r_hi; ++r) {
-    Request q;
-    if (!q.set(a, a.ctx[r], a.row_start[r], a.row_start[r + 1]) && cta == 0)
+    if (!own.set(a, a.ctx[r], a.row_start[r], a.row_start[r + 1]) && cta == 0)
       dspark_set_status(DSPARK_ERR_LENGTH);
-    mine += q.units(a);
+    mine += own.units(a);
   }
   long long upto = mine;
 #pragma unroll
@@ -423,17 +444,19 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  long long units = 0, first = upto - mine;  // of all requests, and before this thread's
-#pragma unroll 1
-  for (int w = 0; w < G::THREADS / 32; ++w) {
-    const long long t = ctl->sums[w];
-    units += t;
-    if (w < warp) first += t;
+  long long units = lane < G::THREADS / 32 ? ctl->sums[lane] : 0;  // of warps up to the lane's
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, units, o);
+    if (lane >= o) units += t;
   }
+  const long long before = __shfl_sync(0xffffffffu, units, max(warp - 1, 0));
+  const long long first = (warp ? before : 0) + upto - mine;  // of requests before the thread's
+  units = __shfl_sync(0xffffffffu, units, 31);                // of all requests
   // equal shares, the first ones a unit longer; with fewer units than CTAs the
   // first take one each, so that an item's pieces lie in consecutive CTAs
   const int shares = (int)min((long long)gridDim.x, max(units, 1ll));
-  const long long share = divide(units, shares), longer = units - share * shares;
+  const long long share = divide_small(units, (uint32_t)shares), longer = units - share * shares;
   const long long u0 = cta < shares ? cta * share + min((long long)cta, longer) : units;
   const long long u1 = cta < shares ? u0 + share + (cta < longer) : units;
   Walker *walk0 = &ctl->walk;
@@ -445,16 +468,18 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
   } else if (mine > 0 && first <= u0 && u0 < first + mine) {
     long long off = u0 - first;
     int r = r_lo;
-    Request q;
+    Request q = own;
+    if (per > 1) {
 #pragma unroll 1
-    for (;; ++r) {
-      q.set(a, a.ctx[r], a.row_start[r], a.row_start[r + 1]);
-      const long long m = q.units(a);
-      if (off < m) break;
-      off -= m;
+      for (;; ++r) {
+        q.set(a, a.ctx[r], a.row_start[r], a.row_start[r + 1]);
+        const long long m = q.units(a);
+        if (off < m) break;
+        off -= m;
+      }
     }
     const int each = q.tiles + ITEM_UNITS;
-    const int item = (int)divide(off, each), rest = (int)(off - (long long)item * each);
+    const int item = quotient(off, each), rest = (int)(off - (long long)item * each);
     walk0->over = max(ITEM_UNITS - rest, 0);
     walk0->tile = max(rest - ITEM_UNITS, 0);
     walk0->h = item / q.row_tiles;
@@ -510,24 +535,21 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
                  : 0;
     };
     int page = 0, next_page = 0;  // of this tile; of the next segment's first one
+    int here = 0;                 // the segment
     while (ok) {
-#pragma unroll 1
-      for (int k = published ? 1 : AHEAD + 1; k; --k) publish();
-      const Segment s = ctl->seg[(published - 1 - AHEAD) % SEGS];
+      if (published == 0) publish();
+      const Segment s = ctl->seg[here % SEGS];
       if (s.tb == s.te) break;
-      page = published == AHEAD + 1 ? page_of(s, s.tb) : next_page;
-      {
-        const Segment &n = ctl->seg[(published - AHEAD) % SEGS];
-        next_page = page_of(n, n.tb);
-      }
+      page = here == 0 ? page_of(s, s.tb) : next_page;
+      bool asked = false;  // for the next segment's first page
       for (int tile = s.tb; ok && tile < s.te; ++tile) {
-        const int here = page, p = tile * BT + lane * rows;
+        const int id = page, p = tile * BT + lane * rows;
         const bool mine = lane < boxes && p < s.total;
         if (tile + 1 < s.te) page = page_of(s, tile + 1);
         const int n_boxes = __popc(__ballot_sync(0xffffffffu, mine));
-        const bool in = here >= 0 && here < a.n_pages;
+        const bool in = id >= 0 && id < a.n_pages;
         if (mine && !in) dspark_set_status(DSPARK_ERR_PAGES);
-        const int z = in ? here : -1;  // outside the map: zeros
+        const int z = in ? id : -1;  // outside the map: zeros
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           if (!warp_wait(&empty[slot], phase ^ 1, abort)) {
@@ -555,7 +577,16 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
             phase ^= 1;
           }
         }
+        // under the first tile's copies, what the next segments need
+#pragma unroll 1
+        while (ok && published <= here + AHEAD) publish();
+        if (ok && !asked) {
+          const Segment &n = ctl->seg[(here + 1) % SEGS];
+          next_page = page_of(n, n.tb);
+          asked = true;
+        }
       }
+      ++here;
     }
     // drain: every copy issued has landed (a slot's last fill is of this pass of
     // the ring before `slot`, of the last pass from it on)
@@ -770,90 +801,118 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         const uint32_t t = t0 + k, b = t & 1;
         ok = ok && warp_wait(&ctl->s_full[b], (t >> 1) & 1, abort);
         // Q's power of two out of its scores: known since the product is done
-        if (G::FP8 && k == first) c = ldexpf(s.c, -ctl->q_exp[seg % G::QS]);
+        if (G::FP8 && k == first) c = times_power(s.c, -ctl->q_exp[seg % G::QS]);
         if (k == n_tiles - 1 && leader && cg == 0 && ok) load_q(seg + G::QS);
         const int pos = tile * BT + token;
         const bool edge = tile * BT + BT > s.ctx;  // some token is a node or past the end
         bool waited = mine == 0;
         tc::fence_after_sync();
+        // which of each chunk's columns see this thread's token
+        uint32_t seen[G::CH];
 #pragma unroll
-        for (int ch = 0; ch < G::CH; ++ch) {
-          const int c0 = c_group + ch * CW;
-          if (ch > 0 && c0 >= rows) break;
-          // which of the chunk's columns see this thread's token
-          uint32_t seen = 0xffffffffu;
-          if (edge) {
-            const int node0 = tile * BT + quarter * 32 - s.ctx;  // lane 0's node
-            if (node0 + lane >= 0) seen = 0;
-            const int stop = min(s.total - s.ctx, node0 + 32);
+        for (int ch = 0; ch < G::CH; ++ch) seen[ch] = 0xffffffffu;
+        if (edge) {
+          const int node0 = tile * BT + quarter * 32 - s.ctx;  // lane 0's node
+          const int stop = min(s.total - s.ctx, node0 + 32);
+#pragma unroll
+          for (int ch = 0; ch < G::CH; ++ch) {
+            if (node0 + lane >= 0) seen[ch] = 0;
 #pragma unroll 1
             for (int j = max(node0, 0); j < stop; ++j) {
               const uint32_t by = __ballot_sync(0xffffffffu, word[ch] >> j & 1);
-              if (lane == j - node0) seen = by;
+              if (lane == j - node0) seen[ch] = by;
             }
           }
-          // e = c * S - reference, masked; again where the references are raised
-          float e[CW];
-          int again;  // a zero that the compiler does not see: one copy of the loop's body
-          asm volatile("mov.u32 %0, 0;" : "=r"(again));
-          for (;; again = 1) {
-            float most = -INFINITY;
-            if (ok) {
-              uint32_t sr[CW];
-              tc::tmem_ld(tmem + lanes + b * NT + c0, sr);
-              tc::tmem_wait_ld();
-              tc::reg_fence(sr);
+        }
+        // e = c * S - reference, masked; again where the references are raised
+        float e[G::CH][CW];
+        auto used = [&](int ch) { return ch == 0 || c_group + ch * CW < rows; };
+        int again;  // a zero that the compiler does not see: one copy of the loop's body
+        asm volatile("mov.u32 %0, 0;" : "=r"(again));
+        for (;; again = 1) {
+          float most = -INFINITY;
+          if (ok) {
+            uint32_t sr[G::CH][CW];
+#pragma unroll
+            for (int ch = 0; ch < G::CH; ++ch)
+              if (used(ch)) tc::tmem_ld(tmem + lanes + b * NT + c_group + ch * CW, sr[ch]);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int ch = 0; ch < G::CH; ++ch) {
+              if (!used(ch)) break;
+              tc::reg_fence(sr[ch]);
 #pragma unroll
               for (int j = 0; j < CW; j += 4) {
-                const float4 m = *reinterpret_cast<const float4 *>(&nm[c0 + j]);
-                e[j] = fmaf(__uint_as_float(sr[j]), c, m.x);
-                e[j + 1] = fmaf(__uint_as_float(sr[j + 1]), c, m.y);
-                e[j + 2] = fmaf(__uint_as_float(sr[j + 2]), c, m.z);
-                e[j + 3] = fmaf(__uint_as_float(sr[j + 3]), c, m.w);
+                const float4 m = *reinterpret_cast<const float4 *>(&nm[c_group + ch * CW + j]);
+                e[ch][j] = fmaf(__uint_as_float(sr[ch][j]), c, m.x);
+                e[ch][j + 1] = fmaf(__uint_as_float(sr[ch][j + 1]), c, m.y);
+                e[ch][j + 2] = fmaf(__uint_as_float(sr[ch][j + 2]), c, m.z);
+                e[ch][j + 3] = fmaf(__uint_as_float(sr[ch][j + 3]), c, m.w);
               }
               if (edge) {
 #pragma unroll
-                for (int j = 0; j < CW; ++j) e[j] = seen >> j & 1 ? e[j] : -INFINITY;
+                for (int j = 0; j < CW; ++j) e[ch][j] = seen[ch] >> j & 1 ? e[ch][j] : -INFINITY;
               }
             }
-            if (k == first && !again && tile * BT < s.ctx) {
-              // The first references: the scores of the tile's first token, which every
-              // row sees, so that no column's maximum lies below its reference; one
-              // that lies far above raises it.  No number: by the longer way.
-              group_sync(bar);  // the references so far are read
-              if (quarter == 0) {
+          }
+          if (k == first && !again && tile * BT < s.ctx) {
+            // The first references: the scores of the tile's first token, which every
+            // row sees, so that no column's maximum lies below its reference; one
+            // that lies far above raises it.  No number: by the longer way.
+            group_sync(bar);  // the references so far are read
+#pragma unroll
+            for (int ch = 0; ch < G::CH; ++ch) {
+              const int c0 = c_group + ch * CW;
+              if (quarter == 0 && used(ch)) {
                 if (lane == 0) {
 #pragma unroll
                   for (int j = 0; j < CW; j += 4)
                     *reinterpret_cast<float4 *>(&nm[c0 + j]) =
-                        make_float4(e[j], e[j + 1], e[j + 2], e[j + 3]);
+                        make_float4(e[ch][j], e[ch][j + 1], e[ch][j + 2], e[ch][j + 3]);
                 }
                 __syncwarp();
                 const float x = nm[c0 + lane % CW];
                 __syncwarp();
                 if (lane < CW)
-                  nm[c0 + lane] =
-                      c0 + lane >= rows ? -INFINITY
-                                        : (fabsf(x) < INFINITY ? R::PEAK - x : INFINITY);
+                  nm[c0 + lane] = c0 + lane >= rows
+                                      ? -INFINITY
+                                      : (fabsf(x) < INFINITY ? R::PEAK - x : INFINITY);
               }
-              group_sync(bar);
+            }
+            group_sync(bar);
+#pragma unroll
+            for (int ch = 0; ch < G::CH; ++ch) {
+              if (!used(ch)) break;
 #pragma unroll
               for (int j = 0; j < CW; j += 4) {
-                const float4 m = *reinterpret_cast<const float4 *>(&nm[c0 + j]);
-                e[j] += m.x;
-                e[j + 1] += m.y;
-                e[j + 2] += m.z;
-                e[j + 3] += m.w;
+                const float4 m = *reinterpret_cast<const float4 *>(&nm[c_group + ch * CW + j]);
+                e[ch][j] += m.x;
+                e[ch][j + 1] += m.y;
+                e[ch][j + 2] += m.z;
+                e[ch][j + 3] += m.w;
               }
               unset[ch] = 0;
             }
+          }
+          uint32_t fresh_any = 0;
 #pragma unroll
-            for (int j = 0; j < CW; ++j) most = fmaxf(most, e[j]);
-            if (again || !group_any(bar, unset[ch] != 0 || most > R::RAISE || !ok)) break;
-            if (group_any(bar, !ok)) {
-              gone = true;
-              break;
-            }
+          for (int ch = 0; ch < G::CH; ++ch) {
+            if (!used(ch)) break;
+            fresh_any |= unset[ch];
+#pragma unroll
+            for (int j = 0; j < CW; ++j) most = fmaxf(most, e[ch][j]);
+          }
+          if (again || !group_any(bar, fresh_any != 0 || most > R::RAISE || !ok)) break;
+          if (group_any(bar, !ok)) {
+            gone = true;
+            break;
+          }
+          if (!waited) ok = warp_wait(&ctl->pv_done[set], (mine - 1) & 1, abort);
+          waited = true;
+#pragma unroll
+          for (int ch = 0; ch < G::CH; ++ch) {
+            const int c0 = c_group + ch * CW;
+            if (!used(ch)) break;
             // a first reference that was no number: as if there were none
             const uint32_t none =
                 __ballot_sync(0xffffffffu, lane < CW && nm[c0 + lane % CW] == INFINITY);
@@ -862,28 +921,18 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
               group_sync(bar);
               if (quarter == 0 && lane < CW && (none >> lane & 1)) nm[c0 + lane] = 0.0f;
               group_sync(bar);
+              uint32_t sr[CW];
+              tc::tmem_ld(tmem + lanes + b * NT + c0, sr);
+              tc::tmem_wait_ld();
+              tc::reg_fence(sr);
 #pragma unroll
-              for (int j = 0; j < CW; ++j) e[j] = -INFINITY;
-#pragma unroll 1
-              for (int h = 0; h < CW; h += 16) {
-                uint32_t sr[16];
-                tc::tmem_ld16(tmem + lanes + b * NT + c0 + h, sr);
-                tc::tmem_wait_ld();
-                tc::reg_fence(sr);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  const float x = fmaf(__uint_as_float(sr[j]), c, nm[c0 + h + j]);
-                  const float y = seen >> (h + j) & 1 ? x : -INFINITY;
-                  if (h == 0) e[j] = y;
-                  else e[CW - 16 + j] = y;
-                }
-              }
+              for (int j = 0; j < CW; ++j)
+                e[ch][j] = seen[ch] >> j & 1 ? fmaf(__uint_as_float(sr[j]), c, nm[c0 + j])
+                                             : -INFINITY;
             }
             // by how much the tile passes each reference: lane j for column j
-            const float peak = column_max<CW>(e, lane);
+            const float peak = column_max<CW>(e[ch], lane);
             if (lane < CW) atomicMax(&top[c0 + lane], order_key(peak));
-            if (!waited) ok = warp_wait(&ctl->pv_done[set], (mine - 1) & 1, abort);
-            waited = true;
             group_sync(bar);
             float raise = order_value(top[c0 + lane % CW]);
             const bool fresh = unset[ch] >> (lane % CW) & 1;
@@ -918,40 +967,45 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
             }
             group_sync(bar);
           }
-          if (gone) break;
-          if (ch == G::CH - 1 || rows <= c0 + CW) {  // the tile's scores are read
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&ctl->s_empty[b]);
-          }
-          // e's place is taken by the weights, as P has them: two bf16 roundings below
-          // and their rests above, or two f16 ones
+        }
+        if (gone) break;
+        tc::fence_before_sync();  // the tile's scores are read
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ctl->s_empty[b]);
+        // e's place is taken by the weights, as P has them: two bf16 roundings below
+        // and their rests above, or two f16 ones
+#pragma unroll
+        for (int ch = 0; ch < G::CH; ++ch) {
+          if (!used(ch)) break;
 #pragma unroll
           for (int j = 0; j < CW; j += 2) {
-            const float x = ex2_fast(e[j]), y = ex2_fast(e[j + 1]);
+            const float x = ex2_fast(e[ch][j]), y = ex2_fast(e[ch][j + 1]);
             l[ch][j] += x;
             l[ch][j + 1] += y;
             if constexpr (G::FP8) {
               const __half2 hi = __floats2half2_rn(x, y);
-              e[j] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&hi));
+              e[ch][j] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&hi));
             } else {
               const uint32_t hi = pack_bf16(x, y);
-              e[j] = __uint_as_float(hi);
-              e[j + 1] = __uint_as_float(pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi)));
+              e[ch][j] = __uint_as_float(hi);
+              e[ch][j + 1] = __uint_as_float(pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi)));
             }
           }
-          if (!waited) ok = warp_wait(&ctl->pv_done[set], (mine - 1) & 1, abort);  // P is free
-          waited = true;
+        }
+        if (!waited) ok = warp_wait(&ctl->pv_done[set], (mine - 1) & 1, abort);  // P is free
+#pragma unroll
+        for (int ch = 0; ch < G::CH; ++ch) {
+          if (!used(ch)) break;
 #pragma unroll
           for (int j = 0; j < CW; j += 8) {
 #pragma unroll
             for (int part = 0; part < G::PARTS; ++part)
-              *p_at(part * NT + c0 + j) = make_uint4(
-                  __float_as_uint(e[j + part]), __float_as_uint(e[j + 2 + part]),
-                  __float_as_uint(e[j + 4 + part]), __float_as_uint(e[j + 6 + part]));
+              *p_at(part * NT + c_group + ch * CW + j) =
+                  make_uint4(__float_as_uint(e[ch][j + part]), __float_as_uint(e[ch][j + 2 + part]),
+                             __float_as_uint(e[ch][j + 4 + part]),
+                             __float_as_uint(e[ch][j + 6 + part]));
           }
         }
-        if (gone) break;
         const int stop16 = (s.total + 15) & ~15;  // the products take 16 tokens a step
         const int warp_pos = tile * BT + quarter * 32;
         if (warp_pos + 31 >= s.ctx && warp_pos < stop16) {
@@ -1072,7 +1126,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
             ml[0] = ref;
             ml[NT] = sum;
           } else {
-            f = sees ? vs / sum : 0.0f;
+            f = sees ? __fdividef(vs, sum) : 0.0f;
             if (a.lse) {
               a.lse[(size_t)(s.row0 + s.node0 + node) * a.heads * a.group + s.h * a.group + g] =
                   sees ? (ref + log2f(sum)) * LN2 : -INFINITY;
@@ -1180,7 +1234,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         desc[3] = s.nodes;
         desc[4] = s.h;
         const long long u = end - 1, split = longer * (share + 1);
-        desc[0] = (int)(u < split ? divide(u, share + 1) : longer + divide(u - split, share)) -
+        desc[0] = (u < split ? quotient(u, share + 1) : (int)longer + quotient(u - split, share)) -
                   cta + 1;
         *(volatile int *)&ctl->tail = 1;
       }
@@ -1242,12 +1296,11 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
                                                 part % 8 * 16);
           const uint4 x = *at;
           const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-          // in two steps: 2^up alone may pass f32's range
-          const float f = ldexpf(1.0f, up / 2), g = ldexpf(1.0f, up - up / 2);
           uint32_t o[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const __half2 h = __floats2half2_rn(bf16_lo(v[k]) * f * g, bf16_hi(v[k]) * f * g);
+            const __half2 h = __floats2half2_rn(times_power(bf16_lo(v[k]), up),
+                                                times_power(bf16_hi(v[k]), up));
             o[k] = *reinterpret_cast<const uint32_t *>(&h);
           }
           *at = make_uint4(o[0], o[1], o[2], o[3]);
