@@ -602,9 +602,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           (G::FP8 ? tc::idesc_f16(128, G::PARTS * NT) : tc::idesc_bf16(128, G::PARTS * NT)) |
           tc::IDESC_A_MN | tc::IDESC_B_MN;
       int k_slot = 0, v_slot = 1;
-      uint32_t k_phase = 0, v_phase = 0, t = 0, pv = 0, seg = 0;
-      uint32_t acc = 0;  // whether the pending tile adds to O
-      uint32_t uses0 = 0, uses1 = 0;  // segments that each set had a part in
+      uint32_t k_phase = 0, v_phase = 0;
       auto advance = [&](int &slot, uint32_t &phase) {
         slot += 2;
         if (slot >= SLOTS) {
@@ -612,91 +610,115 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           phase ^= 1;
         }
       };
-      // Tile t's S, then tile t - 1's O: the tensor cores work on the one while the
-      // softmax has the other.  Between two segments the order turns: a segment's
-      // last product must not wait for the next one's Q.
-      bool ok = true, first = true, more = true;
-      int tile = 0, te = 0, place = 0;  // place: of the tile in its segment
-      int total = 0, tokens = 0;        // of the request; from the pending tile on
-      for (bool pending = false; ok && (more || pending);) {
-        if (more && first && !pending) {  // the next segment
+      auto ready = [&](uint64_t *bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, tc::mbar_test(bar, parity)) != 0;
+      };
+      // The products in the order in which their operands come: a tile's S as soon as
+      // there are K, Q and a place for it, at most two tiles ahead of the O's, which
+      // follow in turn.  Neither then waits behind the other: O's product frees V's
+      // and P's places, S keeps the softmax fed.
+      uint32_t t = 0, pv = 0, seg = 0;  // S and O products issued, segments begun
+      bool more = true, have = false, first = true;
+      int tile = 0, te = 0, total = 0, place = 0;  // place: of the tile in its segment
+      // of the tiles between S and O, by turns: whether the tile adds to what its set
+      // has, and the tokens from it on
+      bool acc0 = false, acc1 = false;
+      int tokens0 = 0, tokens1 = 0;
+      uint32_t uses0 = 0, uses1 = 0;  // segments that each set had a part in
+      uint32_t idle = 0;
+      uint64_t since = 0;
+      for (;;) {
+        bool did = false;
+        if (more && !have) {
           const int i = seg % SEGS;
-          ok = warp_wait(&ctl->seg_full[i], (seg / SEGS) & 1, abort);
-          if (!ok) break;
-          tile = ctl->seg[i].tb;
-          te = ctl->seg[i].te;
-          total = ctl->seg[i].total;
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&ctl->seg_empty[i]);
-          more = tile < te;
-          if (!more) break;
-          place = 0;
-        }
-        const bool issue = more && (!first || !pending);
-        if (issue) {
-          const uint32_t b = t & 1;
-          ok = (!first || warp_wait(G::FP8 ? &ctl->q_ready[seg % G::QS] : &ctl->q_full[seg % G::QS],
-                                    (seg / G::QS) & 1, abort)) &&
-               warp_wait(&ctl->full[k_slot], k_phase, abort) &&
-               warp_wait(&ctl->s_empty[b], ((t >> 1) & 1) ^ 1, abort);
-          if (!ok) break;
-          tc::fence_after_sync();
-          const uint64_t kd = tc::smem_desc_sw128(slots + k_slot * G::SLOT);
-          const uint64_t qd = tc::smem_desc_sw128(sq + seg % G::QS * G::Q_ONE);
-#pragma unroll 1
-          for (int h = 0; h < HALVES; ++h)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc::umma_warp(tmem + b * NT, kd + h * (HALF_BYTES / 16) + 2 * k,
-                                 qd + h * (NT * 128 / 16) + 2 * k, idesc_s, (h | k) != 0);
-          tc::umma_commit_warp(&ctl->empty[k_slot]);
-          tc::umma_commit_warp(&ctl->s_full[b]);
-          advance(k_slot, k_phase);
-          ++t;
-        }
-        if (pending) {  // the product before
-          const int x = G::SETS == 2 ? pv & 1 : 0;
-          ok = warp_wait(&ctl->full[v_slot], v_phase, abort) &&
-               warp_wait(&ctl->p_full[x], (pv / G::SETS) & 1, abort);
-          if (ok && G::SETS == 2 && !acc) {  // a segment's first: its last O there is read
-            const uint32_t before = x ? uses1 : uses0;
-            ok = before == 0 || warp_wait(&ctl->o_free[x], (before - 1) & 1, abort);
-            uses0 += x == 0;
-            uses1 += x;
-          }
-          if (!ok) break;
-          tc::fence_after_sync();
-          // D = 64: the 128-row operand's second 64 rows are the first again, and
-          // accumulator lanes 64..127 are not read
-          const uint64_t vd = tc::smem_desc_sw128_mn(slots + v_slot * G::SLOT,
-                                                     D == 128 ? HALF_BYTES : 0);
-          const uint64_t pd = tc::smem_desc_sw128_mn(sp + x * G::P_SET, HALF_BYTES);
-          if (tokens >= BT) {
-#pragma unroll
-            for (int k = 0; k < BT / 16; ++k)
-              tc::umma_warp(tmem_o + x * G::PARTS * NT, vd + 128 * k, pd + 128 * k, idesc_o,
-                                 acc | (k != 0));
-          } else {  // the steps that hold tokens; in the last some may be past the end
-#pragma unroll 1
-            for (int k = 0; k * 16 < tokens; ++k)
-              tc::umma_warp(tmem_o + x * G::PARTS * NT, vd + 128 * k, pd + 128 * k, idesc_o,
-                                 acc | (k != 0));
-          }
-          tc::umma_commit_warp(&ctl->empty[v_slot]);
-          tc::umma_commit_warp(&ctl->pv_done[x]);
-          advance(v_slot, v_phase);
-          ++pv;
-          pending = false;
-        }
-        if (issue) {
-          pending = true;
-          acc = place >= G::SETS;  // the pending tile adds to what its set has
-          tokens = total - tile * BT;
-          ++place;
-          first = false;
-          if (++tile == te) {
-            ++seg;
+          if (ready(&ctl->seg_full[i], (seg / SEGS) & 1)) {
+            tile = ctl->seg[i].tb;
+            te = ctl->seg[i].te;
+            total = ctl->seg[i].total;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&ctl->seg_empty[i]);
+            more = have = tile < te;
             first = true;
+            place = 0;
+          }
+        }
+        if (have && t - pv < 2) {
+          const uint32_t b = t & 1;
+          uint64_t *const q = G::FP8 ? &ctl->q_ready[seg % G::QS] : &ctl->q_full[seg % G::QS];
+          if (ready(&ctl->full[k_slot], k_phase) && ready(&ctl->s_empty[b], ((t >> 1) & 1) ^ 1) &&
+              (!first || ready(q, (seg / G::QS) & 1))) {
+            did = true;
+            tc::fence_after_sync();
+            const uint64_t kd = tc::smem_desc_sw128(slots + k_slot * G::SLOT);
+            const uint64_t qd = tc::smem_desc_sw128(sq + seg % G::QS * G::Q_ONE);
+#pragma unroll 1
+            for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc::umma_warp(tmem + b * NT, kd + h * (HALF_BYTES / 16) + 2 * k,
+                              qd + h * (NT * 128 / 16) + 2 * k, idesc_s, (h | k) != 0);
+            tc::umma_commit_warp(&ctl->empty[k_slot]);
+            tc::umma_commit_warp(&ctl->s_full[b]);
+            advance(k_slot, k_phase);
+            if (b) {
+              acc1 = place >= G::SETS;
+              tokens1 = total - tile * BT;
+            } else {
+              acc0 = place >= G::SETS;
+              tokens0 = total - tile * BT;
+            }
+            ++place;
+            ++t;
+            first = false;
+            if (++tile == te) {
+              ++seg;
+              have = false;
+            }
+          }
+        }
+        if (!did && pv < t) {
+          const int x = G::SETS == 2 ? pv & 1 : 0;
+          const bool acc = pv & 1 ? acc1 : acc0;
+          const int tokens = pv & 1 ? tokens1 : tokens0;
+          const uint32_t uses = x ? uses1 : uses0;
+          // a segment's first: the set's last O is read
+          if (ready(&ctl->p_full[x], (pv / G::SETS) & 1) && ready(&ctl->full[v_slot], v_phase) &&
+              (G::SETS == 1 || acc || uses == 0 || ready(&ctl->o_free[x], (uses - 1) & 1))) {
+            did = true;
+            uses0 += !acc && x == 0;
+            uses1 += !acc && x == 1;
+            tc::fence_after_sync();
+            // D = 64: the 128-row operand's second 64 rows are the first again, and
+            // accumulator lanes 64..127 are not read
+            const uint64_t vd = tc::smem_desc_sw128_mn(slots + v_slot * G::SLOT,
+                                                       D == 128 ? HALF_BYTES : 0);
+            const uint64_t pd = tc::smem_desc_sw128_mn(sp + x * G::P_SET, HALF_BYTES);
+            const uint32_t to = tmem_o + x * G::PARTS * NT;
+            if (tokens >= BT) {
+#pragma unroll
+              for (int k = 0; k < BT / 16; ++k)
+                tc::umma_warp(to, vd + 128 * k, pd + 128 * k, idesc_o, acc | (k != 0));
+            } else {  // the steps that hold tokens; in the last some may be past the end
+#pragma unroll 1
+              for (int k = 0; k * 16 < tokens; ++k)
+                tc::umma_warp(to, vd + 128 * k, pd + 128 * k, idesc_o, acc | (k != 0));
+            }
+            tc::umma_commit_warp(&ctl->empty[v_slot]);
+            tc::umma_commit_warp(&ctl->pv_done[x]);
+            advance(v_slot, v_phase);
+            ++pv;
+          }
+        }
+        if (did) {
+          idle = 0;
+          since = 0;
+        } else {
+          if (!more && !have && pv == t) break;
+          if ((++idle & 63) == 0) {
+            const uint64_t now = tc::globaltimer();
+            if (since == 0) since = now;
+            if (__any_sync(0xffffffffu, *abort != 0)) break;
+            if (now - since > tc::WAIT_LIMIT_NS) *abort = 1;
           }
         }
       }
