@@ -913,7 +913,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
                 e[ch][j + 2] += m.z;
                 e[ch][j + 3] += m.w;
               }
-              unset[ch] = 0;
+              const int c0 = c_group + ch * CW;
+              unset[ch] = __ballot_sync(0xffffffffu, lane < CW && nm[c0 + lane % CW] == INFINITY);
             }
           }
           uint32_t fresh_any = 0;
