@@ -66,7 +66,7 @@ __device__ __forceinline__ void block_scan3(int64_t (&v)[3], int64_t (&sum)[3],
 // them.  One barrier separates the pages pushed by requests that left from the
 // pages popped.  Sums in 64 bits: no input overflows them.
 // 0.4 MB for 1024 trees of 31 drafts: bound by the chain of dependent reads, sums and
-// barriers.  12.3 us there with the cluster, 3.8 us for one request (one CTA), in a graph.
+// barriers.  12.1 us there with the cluster, 3.9 us for four requests (one CTA), in a graph.
 __global__ void __launch_bounds__(PLAN_THREADS, 1) kv_plan_kernel(const PlanArgs a) {
   extern __shared__ int smem[];
   __shared__ int64_t warp_sums[32][3];
@@ -344,7 +344,7 @@ __device__ __forceinline__ uint32_t scale_four(uint32_t a, uint32_t b, float sca
 // Places of one row are neighbours, so a warp's accesses are whole lines.  Blocks
 // stay (a grid of many more, of a pass or two each, took 33 us for the prompts
 // above, this one 25, both behind a write of all of L2; one row at a time 27, four
-// 31).  Bound by its 101 MB: 20.4 us, 4.9 TB/s; 1536 rows of a round 3.2 us in a graph.
+// 31).  Bound by its 101 MB: 20.4 us, 4.9 TB/s; a round of 256 chains 2.9 us in a graph.
 constexpr int APPEND_THREADS = 256, APPEND_ROWS = 2, APPEND_BLOCKS_SM = 8;
 
 template <bool FP8>
@@ -415,8 +415,8 @@ __global__ void __launch_bounds__(APPEND_THREADS)
 // A warp takes a request, a lane drafts l + 1 and l + 33.  Whether a node's
 // token is its parent's choice is known for all nodes at once; the walk from the
 // anchor then only asks, once per level, which matching node has the present one
-// as its parent.  Under 1 MB: bound by its launch and the walk's ballots, 3.0 us in a
-// graph for one chain as for 1024 trees.
+// as its parent.  Under 1 MB: bound by its launch and the walk's ballots, 1.5 us in a
+// graph for one chain, 2.9 for 1024 trees of 64 nodes.
 __global__ void __launch_bounds__(128)
     tree_accept_kernel(int R, int gamma, int n_rows, const int *__restrict__ row_start,
                        const int *__restrict__ parent, const int *__restrict__ tokens,
@@ -474,7 +474,8 @@ __global__ void __launch_bounds__(128)
 // moved down the path by one thread.  Every source lies at or past its
 // destination and both ascend, so a batch of sources read before its
 // destinations are written is never overwritten too early, and columns are
-// independent: no barrier.  78 MB of a batch's cache in 13 us in a graph, 6.0 TB/s.
+// independent: no barrier.  78 MB of a batch's cache in 14.4 us in a
+// graph, 5.4 TB/s.
 __global__ void __launch_bounds__(128)
     kv_compact_kernel(const CacheView c, int size, int gamma, int max_pages,
                       const int *__restrict__ ctx, const int *__restrict__ accepted,

@@ -41,7 +41,8 @@
 //
 // What it measured, and what bounds it (D = 128, 32 query heads over 8 KV heads):
 //   256 chains of 1..6 rows over contexts of 64 to 8192 tokens, bf16: 1.77 GB in
-//     278 us, 6.4 TB/s; eight chains over 65536 tokens 6.6 TB/s: reading K and V.
+//     265 us in a graph (281 by calls), 6.7 TB/s; eight chains over 65536 tokens 6.6:
+//     reading K and V.
 //     The copies then are late often enough that the softmax's own time is hidden.
 //   1024 chains over 400 tokens 4.6 TB/s: items begin and end every four tiles.
 //   64 trees of 64 rows over 512 to 4096 tokens, bf16 (two tiles of 128 rows):
@@ -53,7 +54,7 @@
 //     2.9 TB/s.  1690 ns a tile: the tile is copied in, read, written as f16 and read
 //     by the products, 224 KB of shared-memory traffic or 1750 cycles, beside the
 //     conversions and the exponentials.
-//   One row over 1000 tokens: 12.5 us in a graph, launches and latencies.
+//   One row over 1000 tokens: 13.5 us in a graph, launches and latencies.
 // Every wait is bounded; on expiry the CTA raises DSPARK_ERR_TIMEOUT, drains its
 // own copies and MMAs, frees TMEM and exits.
 #pragma once
@@ -1414,7 +1415,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
 // could not finish, a warp taking one row, its own pieces in order:
 //   out = sum_k e^{m_k - m} O_k / sum_k e^{m_k - m} l_k,  m the largest m_k.
 // At most two pieces a CTA, a few MB from L2: bound by its launch, which the
-// attention's end overlaps (some 3 us of the 12.5 of a single row).
+// attention's end overlaps (some 3 us of the 13.5 of a single row).
 template <int D>
 __global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant__ Args a, int nt) {
   constexpr int E = D / 32;
