@@ -113,6 +113,11 @@ struct Geo {
   // and their sums did not fit the registers left (36 rows over four contexts of 33 to
   // 131 thousand tokens: 243 against 260 us; 64 rows beside a bf16 cache: 363 against 340).
   static constexpr int CW = NT % 32 || (FP8 && NT >= 64) ? 16 : 32;
+  // Whether a segment's description is read again at its end, and what a tile needs of
+  // it alone kept in registers: for wide tiles and beside an 8-bit cache, where they are
+  // short (four contexts in 8 bits: 192 against 198 us); 1024 chains of 400 tokens in
+  // tiles of 32 columns took 408 with it, 391 without.
+  static constexpr bool REREAD = FP8 || NT > 32;
   static constexpr int CG = SETS == 2 ? 1 : 2;       // groups of four warps in a set
   static constexpr int CH = NT / (CW * CG);          // chunks of a thread
   static constexpr int SW = 4 * CG * SETS;
@@ -798,11 +803,13 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     for (;;) {
       ok = ok && __all_sync(0xffffffffu, segment_here(seg));
       if (group_any(bar, !ok)) break;
-      const Segment s = ctl->seg[seg % SEGS];
-      if (s.tb == s.te) break;
-      float c = s.c;
-      const int rows = s.nodes * a.group;  // columns in use
-      const int n_tiles = s.te - s.tb;
+      const Segment *const now = &ctl->seg[seg % SEGS];
+      Segment s;
+      if constexpr (!G::REREAD) s = *now;
+      const int tb = now->tb, n_tiles = now->te - tb, seg_ctx = now->ctx, total = now->total;
+      if (n_tiles == 0) break;
+      float c = now->c;
+      const int rows = now->nodes * a.group;  // columns in use
       const int first = G::SETS == 2 ? (set ^ t0) & 1 : 0;  // this set's tiles: every SETS-th
       const bool part = first < n_tiles;
       // lane j: the ancestor mask of each chunk's column j
@@ -812,8 +819,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         const int col = c_group + ch * CW + lane;
         word[ch] = 0;
         if (lane < CW && col < rows) {
-          const int node = s.node0 + col / a.group;
-          word[ch] = a.anc ? a.anc[s.row0 + node] : (2ull << node) - 1;
+          const int node = now->node0 + col / a.group;
+          word[ch] = a.anc ? a.anc[now->row0 + node] : (2ull << node) - 1;
         }
         if (quarter == 0 && lane < CW) {
           // a column that no row uses has no weight and calls for nothing
@@ -836,14 +843,14 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       }
 
       for (int k = first; k < n_tiles; k += G::SETS, ++mine) {
-        const int tile = s.tb + k;
+        const int tile = tb + k;
         const uint32_t t = t0 + k, b = t & 1;
         ok = ok && warp_wait(&ctl->s_full[b], (t >> 1) & 1, abort);
         // Q's power of two out of its scores: known since the product is done
-        if (G::FP8 && k == first) c = times_power(s.c, -ctl->q_exp[seg % G::QS]);
+        if (G::FP8 && k == first) c = times_power(now->c, -ctl->q_exp[seg % G::QS]);
         if (k == n_tiles - 1 && leader && cg == 0 && ok) load_q(seg + G::QS);
         const int pos = tile * BT + token;
-        const bool edge = tile * BT + BT > s.ctx;  // some token is a node or past the end
+        const bool edge = tile * BT + BT > seg_ctx;  // some token is a node or past the end
         bool waited = mine == 0;
         tc::fence_after_sync();
         // which of each chunk's columns see this thread's token
@@ -851,8 +858,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
 #pragma unroll
         for (int ch = 0; ch < G::CH; ++ch) seen[ch] = 0xffffffffu;
         if (edge) {
-          const int node0 = tile * BT + quarter * 32 - s.ctx;  // lane 0's node
-          const int stop = min(s.total - s.ctx, node0 + 32);
+          const int node0 = tile * BT + quarter * 32 - seg_ctx;  // lane 0's node
+          const int stop = min(total - seg_ctx, node0 + 32);
 #pragma unroll
           for (int ch = 0; ch < G::CH; ++ch) {
             if (node0 + lane >= 0) seen[ch] = 0;
@@ -894,7 +901,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
               }
             }
           }
-          if (k == first && !again && tile * BT < s.ctx) {
+          if (k == first && !again && tile * BT < seg_ctx) {
             // The first references: the scores of the tile's first token, which every
             // row sees, so that no column's maximum lies below its reference; one
             // that lies far above raises it.  No number: by the longer way.
@@ -1046,16 +1053,16 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
                              __float_as_uint(e[ch][j + 6 + part]));
           }
         }
-        const int stop16 = (s.total + 15) & ~15;  // the products take 16 tokens a step
+        const int stop16 = (total + 15) & ~15;  // the products take 16 tokens a step
         const int warp_pos = tile * BT + quarter * 32;
-        if (warp_pos + 31 >= s.ctx && warp_pos < stop16) {
+        if (warp_pos + 31 >= seg_ctx && warp_pos < stop16) {
           // What a row does not see must not meet its zero weight as infinity or
           // NaN: V past the end is cleared, and so are the nodes' non-finite
           // values, which the epilogue gives to the rows that do see them.
           const uint32_t fill = 2 * t + 1;
           ok = ok && warp_wait(&ctl->full[fill % SLOTS], (fill / SLOTS) & 1, abort);
           uint8_t *row = slots + fill % SLOTS * G::SLOT + token * 128;
-          if (ok && pos >= s.ctx && pos < stop16) {
+          if (ok && pos >= seg_ctx && pos < stop16) {
             // sign bit of a half of odd: its exponent is all ones
             constexpr uint32_t EXP = G::FP8 ? 0x7c00u : 0x7f80u, ONE = 0x8000u - EXP;
             constexpr uint32_t EXPS = EXP << 16 | EXP, ONES = ONE << 16 | ONE;
@@ -1070,11 +1077,11 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
                 const uint4 y = x[at ^ q];
                 odd |= ((y.x & EXPS) + ONES) | ((y.y & EXPS) + ONES) | ((y.z & EXPS) + ONES) |
                        ((y.w & EXPS) + ONES);
-                if (pos >= s.total) x[at ^ q] = make_uint4(0, 0, 0, 0);
+                if (pos >= total) x[at ^ q] = make_uint4(0, 0, 0, 0);
               }
             }
-            if (pos < s.total && (odd & 0x80008000u)) {
-              atomicOr(&ctl->odd[seg & 3], 1ull << (pos - s.ctx));
+            if (pos < total && (odd & 0x80008000u)) {
+              atomicOr(&ctl->odd[seg & 3], 1ull << (pos - seg_ctx));
 #pragma unroll 1
               for (int i = cg * 4; i < HALVES * 8; i += CG * 4)
 #pragma unroll 1
@@ -1096,6 +1103,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
 
       // ------------------------------------------------- end of a segment ----
       // The set with the segment's last tile takes both sets' sums and O together.
+      if constexpr (G::REREAD) s = *now;
       const int other = set ^ 1;
       const bool last = ((t0 + n_tiles - 1 - set) & (G::SETS - 1)) == 0;
       const bool both = G::SETS == 2 && n_tiles > 1;
@@ -1278,6 +1286,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
                   cta + 1;
         *(volatile int *)&ctl->tail = 1;
       }
+      // the group's warps have read the segment's place (with a part in it they have met)
+      if (G::REREAD && !part) group_sync(bar);
       __syncwarp();
       if (quarter == 0 && lane == 0) tc::mbar_arrive(&ctl->seg_empty[seg % SEGS]);
       uses += part;
