@@ -34,8 +34,8 @@
 // and tree_attention_join adds the pieces in order (no atomics: the same bits
 // from call to call).
 //
-// One CTA per SM: warp 0 loads (TMA, one copy per page and 64 columns), warp 1
-// issues the MMAs, one or two groups of four warps do the softmax (a warp for each
+// One CTA per SM: warp 0 loads K and V (TMA, one copy per page and 64 columns), warp
+// 1 issues the MMAs, warp 2 loads Q, one or two groups of four warps do the softmax (a warp for each
 // 32 tokens, CH chunks of 16 or 32 columns one after the other), and for an 8-bit
 // cache four more widen the tiles to f16 between two rings.
 //
@@ -122,7 +122,7 @@ struct Geo {
   static constexpr int CH = NT / (CW * CG);          // chunks of a thread
   static constexpr int SW = 4 * CG * SETS;
   static constexpr int CV = FP8 ? 4 : 0;
-  // Warps 0..3 copy and issue (two of them rest), the softmax's follow, then those
+  // Warps 0..3 copy and issue (one of them rests), the softmax's follow, then those
   // that widen.  The softmax keeps a column's sums and scores in registers, more of
   // them than a thread's share: the others give theirs up.
   static constexpr int THREADS = 32 * (4 + SW + CV);
@@ -286,7 +286,7 @@ __device__ __forceinline__ int quotient(long long x, long long y) {
 
 struct Ctl {
   uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], rfull[MAX_SLOTS], rempty[MAX_SLOTS];
-  uint64_t q_full[2], s_full[2], s_empty[2], drain;
+  uint64_t q_full[2], q_empty[2], s_full[2], s_empty[2], drain;
   // by set: P written, its product done, O read by the segment's last set, and the
   // other's sums ready for it
   uint64_t p_full[2], pv_done[2], o_free[2], half[2];
@@ -301,10 +301,10 @@ struct Ctl {
   // The share's segments as the copying warp comes to them, for the other roles.
   alignas(16) Segment seg[SEGS];
   uint64_t seg_full[SEGS], seg_empty[SEGS];
-  // 8-bit: Q of a place is in f16, by which power of two it was multiplied (and
-  // the warps' largest values on the way there)
+  // 8-bit: Q of a place is in f16, by which power of two it was multiplied (by segment
+  // mod 4: S of three segments before is read), the warps' largest values on the way
   uint64_t q_ready[2];
-  int q_exp[2], q_top[4];
+  int q_exp[4], q_top[4];
   unsigned long long odd[4];  // nodes with non-finite V, by segment mod 4
   int tail;               // the CTA leaves an item to its successors
   int abort;
@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&ctl->q_full[b], 1);
+      tc::mbar_init(&ctl->q_empty[b], 1);
       tc::mbar_init(&ctl->q_ready[b], 4);
       tc::mbar_init(&ctl->s_full[b], 1);
       tc::mbar_init(&ctl->s_empty[b], 4 * CG);
@@ -433,8 +434,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
 #pragma unroll 1
     for (int i = 0; i < SEGS; ++i) {
       tc::mbar_init(&ctl->seg_full[i], 1);
-      // the MMA issuer, each group, those that widen
-      tc::mbar_init(&ctl->seg_empty[i], 1 + G::SETS * CG + (G::FP8 ? 1 : 0));
+      // the MMA issuer, the warp that copies Q, each group, those that widen
+      tc::mbar_init(&ctl->seg_empty[i], 2 + G::SETS * CG + (G::FP8 ? 1 : 0));
     }
     tc::fence_barrier_init();
     tc::tma_prefetch_desc(&tma_k);
@@ -693,6 +694,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
             ++t;
             first = false;
             if (++tile == te) {
+              tc::umma_commit_warp(&ctl->q_empty[seg % G::QS]);
               ++seg;
               have = false;
             }
@@ -749,6 +751,34 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       warp_wait(&ctl->drain, 0, &never);
     }
     __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------ copies of Q ----
+    // A segment's tile of Q, as soon as the last product with what lay in its place
+    // is done: rows node0.. of the request, the heads of one KV head.
+    uint32_t i = 0;
+    bool ok = true;
+    for (;; ++i) {
+      ok = warp_wait(&ctl->seg_full[i % SEGS], (i / SEGS) & 1, abort);
+      if (!ok) break;
+      const Segment *n = &ctl->seg[i % SEGS];
+      if (n->tb == n->te) break;
+      const int head = n->h * a.group, row = n->row0 + n->node0;
+      if (i >= G::QS) ok = warp_wait(&ctl->q_empty[i % G::QS], (i / G::QS - 1) & 1, abort);
+      if (!ok) break;
+      if (lane == 0) {
+        tc::mbar_arrive(&ctl->seg_empty[i % SEGS]);
+        uint64_t *full = &ctl->q_full[i % G::QS];
+        tc::mbar_expect_tx(full, HALVES * a.nodes_tile * a.group * 128);
+        for (int c = 0; c < HALVES; ++c)
+          tc::tma_load_3d(sq + i % G::QS * G::Q_ONE + c * NT * 128, &tma_q, c * 64, head, row, full,
+                          tc::policy_evict_normal());
+      }
+      __syncwarp();
+    }
+    // drain: the last copies have landed (no later one took their place)
+    volatile int never = 0;
+    for (uint32_t k = i > G::QS ? i - G::QS : 0; k < i; ++k)
+      warp_wait(&ctl->q_full[k % G::QS], (k / G::QS) & 1, &never);
   } else if (warp >= 4 && warp < 4 + G::SW) {
     more_registers<G::REGS_SOFTMAX>();
     // ----------------------------------------------------------- softmax ----
@@ -777,29 +807,10 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
     uint32_t t0 = 0, seg = 0;   // the segment's first tile, of all of the share's
     uint32_t mine = 0;          // tiles that this set has taken
     uint32_t uses = 0, helped = 0;  // segments that this set had a part in; that the other helped
-    int q_last = -1;            // the last segment whose Q this thread has copied
     bool ok = true, gone = false;
     auto segment_here = [&](uint32_t i) {
       return wait(&ctl->seg_full[i % SEGS], (i / SEGS) & 1, abort);
     };
-    // Q of segment i, by the leader of the set that sees the last product with what
-    // lies in its place done
-    auto load_q = [&](uint32_t i) {
-      if (!segment_here(i)) return;
-      const Segment *n = &ctl->seg[i % SEGS];
-      if (n->tb == n->te) return;
-      uint64_t *full = &ctl->q_full[i % G::QS];
-      tc::mbar_expect_tx(full, HALVES * a.nodes_tile * a.group * 128);
-      for (int c = 0; c < HALVES; ++c)
-        tc::tma_load_3d(sq + i % G::QS * G::Q_ONE + c * NT * 128, &tma_q, c * 64, n->h * a.group,
-                        n->row0 + n->node0, full, tc::policy_evict_normal());
-      q_last = (int)i;
-    };
-    if (leader && group == 0) {
-      load_q(0);
-      if (G::QS == 2 && ctl->seg[0].tb != ctl->seg[0].te) load_q(1);
-    }
-    __syncwarp();
     for (;;) {
       ok = ok && __all_sync(0xffffffffu, segment_here(seg));
       if (group_any(bar, !ok)) break;
@@ -847,8 +858,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
         const uint32_t t = t0 + k, b = t & 1;
         ok = ok && warp_wait(&ctl->s_full[b], (t >> 1) & 1, abort);
         // Q's power of two out of its scores: known since the product is done
-        if (G::FP8 && k == first) c = times_power(now->c, -ctl->q_exp[seg % G::QS]);
-        if (k == n_tiles - 1 && leader && cg == 0 && ok) load_q(seg + G::QS);
+        if (G::FP8 && k == first) c = times_power(now->c, -ctl->q_exp[seg & 3]);
         const int pos = tile * BT + token;
         const bool edge = tile * BT + BT > seg_ctx;  // some token is a node or past the end
         bool waited = mine == 0;
@@ -1295,11 +1305,6 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       t0 += n_tiles;
       ++seg;
     }
-    if (leader && gone && q_last >= 0) {  // a Q copy still in flight lands before the CTA ends
-      volatile int never = 0;
-      for (int i = q_last; i >= 0 && i > q_last - G::QS; --i)
-        tc::mbar_wait(&ctl->q_full[i % G::QS], (i / G::QS) & 1, &never);
-    }
     __syncwarp();
   } else if (warp >= 4 + G::SW) {
     if constexpr (G::FP8) {
@@ -1355,7 +1360,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
           }
           *at = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        if (w == 0 && lane == 0) ctl->q_exp[seg % G::QS] = up;
+        if (w == 0 && lane == 0) ctl->q_exp[seg & 3] = up;
         tc::fence_async_smem();
         group_sync(5);  // q_top is read
         if (lane == 0) tc::mbar_arrive(&ctl->q_ready[seg % G::QS]);
