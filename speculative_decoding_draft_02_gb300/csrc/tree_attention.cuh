@@ -296,7 +296,9 @@ struct Ctl {
   // column's row of the output lies from the tile's first one
   alignas(16) int top[128];
   alignas(16) float other[2][64];  // a set's references and sums, for the other
-  long long sums[32];
+  // of the warps before the shares are known; the shares' size, how many are a unit
+  // longer, and where this CTA's ends, for an item that goes on in others
+  long long sums[16], share, longer, end;
   Walker walk;
   // The share's segments as the copying warp comes to them, for the other roles.
   alignas(16) Segment seg[SEGS];
@@ -467,6 +469,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  static_assert(G::THREADS / 32 <= 16, "a sum for each warp");
   long long units = lane < G::THREADS / 32 ? ctl->sums[lane] : 0;  // of warps up to the lane's
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -482,6 +485,11 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
   const long long share = divide_small(units, (uint32_t)shares), longer = units - share * shares;
   const long long u0 = cta < shares ? cta * share + min((long long)cta, longer) : units;
   const long long u1 = cta < shares ? u0 + share + (cta < longer) : units;
+  if (threadIdx.x == 0) {
+    ctl->share = share;
+    ctl->longer = longer;
+    ctl->end = u1;
+  }
   Walker *walk0 = &ctl->walk;
   if (u0 == u1) {
     if (threadIdx.x == 0) {
@@ -1285,7 +1293,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
       }
       if (last && leader && group == set && !whole && piece == 1) {
         // the item goes on in the CTAs up to the one that holds its last unit
-        const long long end = u1 + (s.tiles - s.te);
+        const long long end = ctl->end + (s.tiles - s.te), share = ctl->share, longer = ctl->longer;
         int *desc = a.desc + cta * 8;
         desc[1] = s.row0;
         desc[2] = s.node0;
