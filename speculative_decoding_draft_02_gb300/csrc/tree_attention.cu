@@ -14,17 +14,16 @@ using attn::Args;
 // Query rows of a tile: the narrowest that takes a request's rows, so that no
 // product, exponential or byte of shared memory is spent on empty columns; at
 // most 128 (two tiles of scores and O in tensor memory, and Q and P in shared memory,
-// beside the tiles in flight).  Beside an 8-bit cache at most 48, and 32 from 49 on:
-// the warps that widen leave the softmax fewer registers, and its columns and their
-// sums would not fit (eight contexts of 32768, 64 rows: 276 us in tiles of 32, 365 in
-// tiles of 48, 446 in one of 64; 128 rows: 531, 527, 659).
+// beside the tiles in flight).  Beside an 8-bit cache the widening warps leave room for
+// 64 (eight contexts of 32768, 64 rows: 172 us, 272 in tiles of 32; 128 rows: 324 and
+// 519; 64 trees of 64 nodes over 512 to 4096 tokens, where the masked tiles weigh more:
+// 742 and 692), and take 33 to 48 rows so too (36 rows: 307 us, 311 in tiles of 48).
 int row_tile(const dspark_kv_cache *c, int heads_q, int max_nodes) {
   const int group = heads_q / c->heads, rows = max_nodes * group;
   if (rows <= 16) return 16;
   if (rows <= 32) return 32;
+  if (c->type == DSPARK_KV_E4M3) return 64;
   if (rows <= 48) return 48;
-  if (c->type == DSPARK_KV_E4M3)  // a tile holds one node's rows at least
-    return group <= 32 ? 32 : group <= 48 ? 48 : 64;
   return rows <= 64 ? 64 : 128;
 }
 
@@ -98,9 +97,10 @@ template <int TYPE, int D>
 int launch_tile(const Launch &l, int nt) {
   if (nt == 16) return launch<TYPE, D, 16>(l);
   if (nt == 32) return launch<TYPE, D, 32>(l);
-  if (nt == 48) return launch<TYPE, D, 48>(l);
-  if constexpr (TYPE == DSPARK_KV_BF16)
+  if constexpr (TYPE == DSPARK_KV_BF16) {
+    if (nt == 48) return launch<TYPE, D, 48>(l);
     if (nt == 128) return launch<TYPE, D, 128>(l);
+  }
   return launch<TYPE, D, 64>(l);
 }
 

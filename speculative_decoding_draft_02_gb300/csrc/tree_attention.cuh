@@ -41,20 +41,20 @@
 //
 // What it measured, and what bounds it (D = 128, 32 query heads over 8 KV heads):
 //   256 chains of 1..6 rows over contexts of 64 to 8192 tokens, bf16: 1.77 GB in
-//     265 us in a graph (281 by calls), 6.7 TB/s; eight chains over 65536 tokens 6.6:
-//     reading K and V.
+//     264 to 273 us in a graph (boxes differ; 271 to 279 by calls), 6.5 to 6.7 TB/s;
+//     eight chains over 65536 tokens 6.6 to 6.8: reading K and V.
 //     The copies then are late often enough that the softmax's own time is hidden.
-//   1024 chains over 400 tokens 4.6 TB/s: items begin and end every four tiles.
+//   1024 chains over 400 tokens 4.8 TB/s: items begin and end every four tiles.
 //   64 trees of 64 rows over 512 to 4096 tokens, bf16 (two tiles of 128 rows):
-//     120 GFLOP in 303 us.  A tile takes 4200 cycles, of which the softmax's chain is
+//     120 GFLOP in 299 us.  A tile takes 4200 cycles, of which the softmax's chain is
 //     3650 (scores read and masked 1350, exponentials 1050, which is their unit's
 //     rate, waiting for P's place 400, P written 850); shared memory alone would
 //     take 2300.
-//   Four chains of 9 rows over 33 to 131 thousand tokens, 8 bits: 0.58 GB in 197 us,
-//     2.9 TB/s.  1690 ns a tile: the tile is copied in, read, written as f16 and read
+//   Four chains of 9 rows over 33 to 131 thousand tokens, 8 bits: 0.58 GB in 179 us,
+//     3.2 TB/s.  1530 ns a tile: the tile is copied in, read, written as f16 and read
 //     by the products, 224 KB of shared-memory traffic or 1750 cycles, beside the
 //     conversions and the exponentials.
-//   One row over 1000 tokens: 13.5 us in a graph, launches and latencies.
+//   One row over 1000 tokens: 12.1 us in a graph, launches and latencies.
 // Every wait is bounded; on expiry the CTA raises DSPARK_ERR_TIMEOUT, drains its
 // own copies and MMAs, frees TMEM and exits.
 #pragma once
@@ -71,7 +71,7 @@ constexpr int CTL_BYTES = 3072;
 constexpr int MAX_SLOTS = 12;           // tiles in a ring
 constexpr int SEGS = 8;                 // segments published ahead
 // What beginning and ending an item costs a CTA, in tiles; counted so that short
-// contexts balance too (256 ragged chains: 290 us with one, 281 with two).
+// contexts balance too (256 ragged chains: 282 us with one, 279 with two, 282 with three).
 constexpr int ITEM_UNITS = 2;
 // log2: how far scores may pass the reference, and where a raised reference puts the
 // largest.  Beside a bf16 cache weights, their sum and O are floating-point numbers
@@ -109,14 +109,14 @@ struct Geo {
   // leave no room for a second P and O: one set of two groups, each with half the
   // columns.
   static constexpr int SETS = NT <= 64 ? 2 : 1;
-  // Columns of a softmax thread's chunk: 16 beside an 8-bit cache from 64 on, where 32
-  // and their sums did not fit the registers left (36 rows over four contexts of 33 to
-  // 131 thousand tokens: 243 against 260 us; 64 rows beside a bf16 cache: 363 against 340).
-  static constexpr int CW = NT % 32 || (FP8 && NT >= 64) ? 16 : 32;
+  // Columns of a softmax thread's chunk: 32 where they divide the tile (128 rows in
+  // chunks of 16: 558 against 299 us for 64 trees; 64 rows beside an 8-bit cache: 443
+  // against 172 us for eight contexts of 32768).
+  static constexpr int CW = NT % 32 ? 16 : 32;
   // Whether a segment's description is read again at its end, and what a tile needs of
   // it alone kept in registers: for wide tiles and beside an 8-bit cache, where they are
-  // short (four contexts in 8 bits: 192 against 198 us); 1024 chains of 400 tokens in
-  // tiles of 32 columns took 408 with it, 391 without.
+  // short (four contexts in 8 bits: 183 against 186 us; 64 trees: 299 against 303); 1024
+  // chains of 400 tokens in tiles of 32 columns took 380 with it, 376 without.
   static constexpr bool REREAD = FP8 || NT > 32;
   static constexpr int CG = SETS == 2 ? 1 : 2;       // groups of four warps in a set
   static constexpr int CH = NT / (CW * CG);          // chunks of a thread
@@ -1438,7 +1438,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
 // could not finish, a warp taking one row, its own pieces in order:
 //   out = sum_k e^{m_k - m} O_k / sum_k e^{m_k - m} l_k,  m the largest m_k.
 // At most two pieces a CTA, a few MB from L2: bound by its launch, which the
-// attention's end overlaps (some 3 us of the 13.5 of a single row).
+// attention's end overlaps (some 3 us of the 12.1 of a single row).
 template <int D>
 __global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant__ Args a, int nt) {
   constexpr int E = D / 32;
