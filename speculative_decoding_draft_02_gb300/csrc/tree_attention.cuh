@@ -1199,8 +1199,10 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
             }
           }
           top[col] = node * (int)a.out_row + g * (int)a.out_head;  // where the column's row lies
-          nm[col] = mine_w * f;  // the factors of both O
-          if (G::SETS == 2) ctl->other[1][col] = their_w * f;
+          // The factors of both O.  Without the other set's part `other` is not this set's
+          // to write: the other may be at a later segment's end already, and its sums there.
+          nm[col] = mine_w * f;
+          if (both) ctl->other[1][col] = their_w * f;
         }
       }
       if (part && !last) {
