@@ -516,6 +516,7 @@ class PagePool:
         self.row_start, self.position = new(R + 1), new(n_rows)
         self.slot, self.anc = new(n_rows, torch.int64), new(n_rows, torch.int64)
         self.accepted, self.bonus, self.ctx_before = new(R), new(R), new(R)
+        self._prompts = False  # the rows planned last are prompts': anc is not theirs
         self._ws = {}
 
     def plan(self, length, extra=1, parent=None, stream=None):
@@ -525,22 +526,25 @@ class PagePool:
                        self.free_pages, self.block_table, self.held, self.n_free,
                        self.row_start, self.position, self.slot, self.anc if extra else None,
                        stream)
+        self._prompts = not extra
 
     def append(self, cache: KVCache, k, v, stream=None):
         """One layer's new rows into the planned slots."""
         dspark_kv_append(cache, k, v, self.slot, stream)
 
     def attend(self, cache: KVCache, q, max_nodes, out, lse=None, scale=None, stream=None):
-        """One layer's attention of a round's rows over contexts and trees."""
+        """One layer's attention of the rows that plan was last called for, over contexts and
+        trees; a prompt's (up to MAX_NODES rows a request) are chains.  Which of the two is
+        settled at the call: a graph that holds an attend holds its plan too."""
         need = dspark_tree_attention_workspace_bytes(cache, len(self.ctx), q.shape[1], max_nodes)
         ws = self._ws.get(need)
         if ws is None:  # once for each size: kept, as a captured graph would need it
             ws = self._ws[need] = workspace(need, q.device)
         if stream is not None:
             ws.record_stream(stream)
-        dspark_tree_attention(cache, q, self.ctx, self.row_start, self.anc, self.block_table,
-                              max_nodes, cache.dim ** -0.5 if scale is None else scale, out, lse,
-                              ws, stream)
+        dspark_tree_attention(cache, q, self.ctx, self.row_start,
+                              None if self._prompts else self.anc, self.block_table, max_nodes,
+                              cache.dim ** -0.5 if scale is None else scale, out, lse, ws, stream)
 
     def commit(self, rows):
         """`rows` of each request's new rows are committed: after dspark_verify the anchor

@@ -1,0 +1,59 @@
+"""PagePool's own dealings (which masks, which scratch, which stream go into a call),
+without a GPU: the entry points are replaced by recorders."""
+import contextlib
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+import speculative_decoding_draft_02_gb300 as dsp
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The arguments of every entry point that the pool calls, by name."""
+    got = []
+
+    def record(name, result=None):
+        def call(*args, **kw):
+            got.append(SimpleNamespace(name=name, args=args, kw=kw))
+            return result
+        monkeypatch.setattr(dsp, name, call)
+
+    record("dspark_kv_plan")
+    record("dspark_kv_append")
+    record("dspark_tree_attention")
+    record("dspark_tree_attention_workspace_bytes", 512)
+    # the streams here are stand-ins, and no current one exists
+    monkeypatch.setattr(dsp, "_stream", lambda s: 0 if s is None else s.cuda_stream)
+    monkeypatch.setattr(dsp, "workspace", lambda n, device: torch.empty(n, dtype=torch.uint8))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    return got
+
+
+def make_pool():
+    return dsp.PagePool(2, 8, 16, 64, 32, device="cpu")
+
+
+CACHE = SimpleNamespace(dim=64)
+Q = torch.zeros((32, 4, 64), dtype=torch.bfloat16)
+
+
+def masks_of(pool, calls):
+    pool.attend(CACHE, Q, 8, Q.clone())
+    call = calls[-1]
+    assert call.name == "dspark_tree_attention"
+    return call.args[4]
+
+
+def test_a_prompts_rows_are_attended_as_chains(calls):
+    pool = make_pool()
+    two = torch.full((2,), 2, dtype=torch.int32)
+    pool.plan(two, extra=0)
+    assert calls[-1].args[14] is None     # no masks are written for prompts
+    assert masks_of(pool, calls) is None  # so none may be read: chains
+    pool.plan(two)
+    assert calls[-1].args[14] is pool.anc and masks_of(pool, calls) is pool.anc
+    pool.plan(two, extra=0)
+    assert masks_of(pool, calls) is None
