@@ -435,7 +435,9 @@ size_t dspark_tree_attention_workspace_bytes(const dspark_kv_cache *cache, int32
  *   lse = log sum_p e^{s_p}
  * A row that sees nothing gives out = 0 and lse = -inf.  What a row does not see
  * does not reach it, whatever its bits (infinities and NaN in unwritten or
- * masked places included).  Scores, statistics and sums in f32.  Beside a bf16 cache
+ * masked places included).  Infinities and NaN in values that a row sees come out as the
+ * sum has them, for weights above f32's least; finite values below 2^64 never overflow.
+ * Scores, statistics and sums in f32.  Beside a bf16 cache
  * the weights meet V with 16 bits (the sum of two bf16); beside an 8-bit one as f16,
  * with 11 bits, and those below 2^-31 of a row's largest may be lost; q is f16 there too,
  * scaled by a power of two: its 8 bits are whole down to 2^-28 of a tile's largest.

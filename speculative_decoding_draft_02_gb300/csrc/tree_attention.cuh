@@ -75,8 +75,8 @@ constexpr int SEGS = 8;                 // segments published ahead
 constexpr int ITEM_UNITS = 2;
 // log2: how far scores may pass the reference, and where a raised reference puts the
 // largest.  Beside a bf16 cache weights, their sum and O are floating-point numbers
-// of f32's range, so nothing is lost below 2^32; f16 weights start high, for the
-// sake of the small ones.
+// of f32's range, so nothing is lost by weights up to 2^32 (O of fewer than 2^31 tokens
+// stays finite for |V| < 2^64); f16 weights start high, for the sake of the small ones.
 template <bool FP8>
 struct Range {
   static constexpr float RAISE = FP8 ? 14.0f : 32.0f, PEAK = FP8 ? 6.0f : 0.0f;
@@ -1236,9 +1236,14 @@ __global__ void __launch_bounds__(Geo<TYPE, D, NT>::THREADS, 1)
               const float4 g = f[i / 4];
               const float h[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
-                x[i + q] = fmaf(__uint_as_float(o[i + q]) + __uint_as_float(o_lo[i + q]), h[q],
-                                x[i + q]);
+              for (int q = 0; q < 4; ++q) {
+                // an infinite V met both parts of a weight, of which the second may be
+                // zero or below: the first part's product alone has its sign
+                float both_parts = __uint_as_float(o[i + q]);
+                if (G::PARTS == 2 && fabsf(both_parts) < INFINITY)
+                  both_parts += __uint_as_float(o_lo[i + q]);
+                x[i + q] = fmaf(both_parts, h[q], x[i + q]);
+              }
             }
           }
           const int j0 = (c0 - c_group) % CW;  // of the chunk's columns
