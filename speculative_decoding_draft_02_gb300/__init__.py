@@ -537,14 +537,23 @@ class PagePool:
         trees; a prompt's (up to MAX_NODES rows a request) are chains.  Which of the two is
         settled at the call: a graph that holds an attend holds its plan too."""
         need = dspark_tree_attention_workspace_bytes(cache, len(self.ctx), q.shape[1], max_nodes)
-        ws = self._ws.get(need)
-        if ws is None:  # once for each size: kept, as a captured graph would need it
-            ws = self._ws[need] = workspace(need, q.device)
-        if stream is not None:
-            ws.record_stream(stream)
+        ws = self._scratch(need, q.device, stream)
         dspark_tree_attention(cache, q, self.ctx, self.row_start,
                               None if self._prompts else self.anc, self.block_table, max_nodes,
                               cache.dim ** -0.5 if scale is None else scale, out, lse, ws, stream)
+
+    def _scratch(self, need, device, stream):
+        """An attention's workspace, which no call on another stream may use meanwhile: kept
+        for each size and stream.  Under capture it is the graph's own memory, as the graph
+        may be replayed beside calls on the stream that it was captured on."""
+        key = need, device, _stream(stream)
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return workspace(need, device)
+            ws = self._ws.get(key)
+            if ws is None:
+                ws = self._ws[key] = workspace(need, device)
+        return ws
 
     def commit(self, rows):
         """`rows` of each request's new rows are committed: after dspark_verify the anchor

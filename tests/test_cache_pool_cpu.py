@@ -9,6 +9,11 @@ import torch
 import speculative_decoding_draft_02_gb300 as dsp
 
 
+class Scratch:
+    def record_stream(self, stream):
+        pass
+
+
 @pytest.fixture
 def calls(monkeypatch):
     """The arguments of every entry point that the pool calls, by name."""
@@ -26,7 +31,7 @@ def calls(monkeypatch):
     record("dspark_tree_attention_workspace_bytes", 512)
     # the streams here are stand-ins, and no current one exists
     monkeypatch.setattr(dsp, "_stream", lambda s: 0 if s is None else s.cuda_stream)
-    monkeypatch.setattr(dsp, "workspace", lambda n, device: torch.empty(n, dtype=torch.uint8))
+    monkeypatch.setattr(dsp, "workspace", lambda n, device: Scratch())
     monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     return got
@@ -57,3 +62,27 @@ def test_a_prompts_rows_are_attended_as_chains(calls):
     assert calls[-1].args[14] is pool.anc and masks_of(pool, calls) is pool.anc
     pool.plan(two, extra=0)
     assert masks_of(pool, calls) is None
+
+
+def scratch_of(pool, calls, **kw):
+    pool.attend(CACHE, Q, 8, Q.clone(), **kw)
+    return calls[-1].args[10]
+
+
+def test_streams_do_not_share_scratch(calls, monkeypatch):
+    # an attention's pieces lie in its scratch until its join has read them
+    pool = make_pool()
+    one, two = SimpleNamespace(cuda_stream=11), SimpleNamespace(cuda_stream=12)
+    at = [scratch_of(pool, calls, stream=s) for s in (None, one, two)]
+    assert len(set(at)) == 3
+    # kept for the next call there
+    assert all(scratch_of(pool, calls, stream=s) is t for s, t in zip((None, one, two), at))
+    # the current stream's, where none is named
+    monkeypatch.setattr(dsp, "_stream", lambda s: 12 if s is None else s.cuda_stream)
+    assert scratch_of(pool, calls) is at[2]
+    # a graph may be replayed on any stream: its scratch is its own
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    held = [scratch_of(pool, calls, stream=s) for s in (one, one, None)]
+    assert not set(held) & set(at)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    assert scratch_of(pool, calls, stream=one) is at[1]
