@@ -498,7 +498,9 @@ def workspace(nbytes: int, device="cuda") -> torch.Tensor:
 
 class PagePool:
     """The pages of R requests over any number of layers' caches, on the device: who
-    holds which, and one round's rows (no allocation per call).
+    holds which, and one round's rows.  A call makes no tensors but attend's scratch, once
+    for each size and stream.  A round's calls go on one stream (or are ordered by events):
+    they read and write the pool's tensors.
 
     `ctx` holds the committed tokens, -1 for a free place; a request enters when its
     prompt's rows are planned with ctx 0, and leaves when its ctx is set to -1 (its
@@ -516,6 +518,8 @@ class PagePool:
         self.row_start, self.position = new(R + 1), new(n_rows)
         self.slot, self.anc = new(n_rows, torch.int64), new(n_rows, torch.int64)
         self.accepted, self.bonus, self.ctx_before = new(R), new(R), new(R)
+        # commit's: who is there, and by how much each goes on
+        self._live, self._step = new(R, torch.bool), new(R)
         self._prompts = False  # the rows planned last are prompts': anc is not theirs
         self._ws = {}
 
@@ -555,10 +559,13 @@ class PagePool:
                 ws = self._ws[key] = workspace(need, device)
         return ws
 
-    def commit(self, rows):
+    def commit(self, rows, stream=None):
         """`rows` of each request's new rows are committed: after dspark_verify the anchor
         and the accepted drafts (accepted + 1), after a prompt its length."""
-        self.ctx += torch.where(self.ctx >= 0, rows, 0)
+        with torch.cuda.stream(stream):
+            torch.ge(self.ctx, 0, out=self._live)
+            torch.mul(self._live, rows, out=self._step)
+            self.ctx.add_(self._step)
 
     def accept(self, tokens, choice, path, parent=None, stream=None):
         """The trees' confirmed paths (into `path` [R, gamma], self.accepted, self.bonus);

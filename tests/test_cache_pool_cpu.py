@@ -86,3 +86,31 @@ def test_streams_do_not_share_scratch(calls, monkeypatch):
     assert not set(held) & set(at)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     assert scratch_of(pool, calls, stream=one) is at[1]
+
+
+@pytest.mark.parametrize("rows", [torch.tensor([3, 9], dtype=torch.int32), torch.tensor([3, 9]), 3],
+                         ids=["int32", "int64", "number"])
+def test_commit_goes_on_the_stream_that_is_named(calls, monkeypatch, rows):
+    # what it changes is read by the kernels of that stream
+    pool = make_pool()
+    pool.ctx.copy_(torch.tensor([7, -1]))
+    inside = []
+
+    class On(contextlib.AbstractContextManager):
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            inside.append(self.stream)
+            self.before = pool.ctx.clone()
+
+        def __exit__(self, *_):
+            inside.append(not torch.equal(self.before, pool.ctx))
+
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    s = SimpleNamespace(cuda_stream=5)
+    pool.commit(rows, stream=s)
+    assert inside == [s, True]              # the change was made within
+    assert pool.ctx.tolist() == [10, -1] and pool.ctx.dtype is torch.int32
+    pool.commit(rows)
+    assert inside == [s, True, None, True] and pool.ctx.tolist() == [13, -1]

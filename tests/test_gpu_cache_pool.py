@@ -179,3 +179,30 @@ def test_a_replay_beside_attends_of_the_stream_it_was_captured_on(fp8):
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(out, want[i]) for out in got[i])
+
+
+@TYPES
+def test_rounds_on_a_side_stream(fp8):
+    # every call of several rounds on a stream that is named, none waited for
+    def rounds(stream):
+        pool, (cache,) = long_contexts(1, fp8)
+        length, step = i32([7, 0, 3]), i32([5, 1, 2])
+        kv = [normal((pool.n_rows, 2 * HEADS, DIM), 100 + i) for i in range(8)]
+        q = [normal((pool.n_rows, HEADS * GROUP, DIM), 110 + i) for i in range(8)]
+        outs = [torch.zeros_like(x) for x in q]
+        seen = torch.zeros((8, 3), dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(8):
+            pool.plan(length, stream=stream)
+            pool.append(cache, kv[i][:, :HEADS], kv[i][:, HEADS:], stream=stream)
+            pool.attend(cache, q[i], 8, outs[i], stream=stream)
+            pool.commit(step, stream=stream)
+            with torch.cuda.stream(stream):
+                seen[i].copy_(pool.ctx)
+        torch.cuda.synchronize()
+        return outs, seen
+
+    want, ctx = rounds(None)
+    assert ctx[:, 0].tolist() == list(range(2505, 2545, 5))
+    got, ctx2 = rounds(torch.cuda.Stream())
+    assert torch.equal(ctx, ctx2) and all(torch.equal(a, b) for a, b in zip(got, want))
