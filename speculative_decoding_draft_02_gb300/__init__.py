@@ -331,7 +331,7 @@ def _rows_view(what: str, name: str, t, heads, dim):
         raise DSparkError(f"{what}: {name} must be a tensor") from None
     # a dimension of one element may carry any stride: what the call would step by is unused
     head = stride[1] if heads > 1 else dim
-    row = stride[0] if shape[0] > 1 else max(8, heads * head)
+    row = stride[0] if shape[0] > 1 else dim
     return t.data_ptr(), shape[0], row, head
 
 
