@@ -78,39 +78,27 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
 
 }  // namespace
 
-int dspark_make_tmap(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base,
-                     const uint64_t *dims, const uint64_t *strides, const uint32_t *box,
-                     CUtensorMapSwizzle swizzle) {
-  static const EncodeTiledFn encode = [] {
+int dspark_make_tmap_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
+                          uint32_t box_rows) {
+  static EncodeTiledFn encode = nullptr;
+  if (!encode) {
     void *fn = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
                                          &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      fn = nullptr;
-    return (EncodeTiledFn)fn;
-  }();
-  if (!encode || rank < 1 || rank > 5) return -1;
-  cuuint64_t d[5], s[5] = {};
-  cuuint32_t b[5], estr[5];
-  for (int i = 0; i < rank; ++i) {
-    d[i] = dims[i];
-    b[i] = box[i];
-    estr[i] = 1;
-    if (i + 1 < rank) s[i] = strides[i];
+        q != cudaDriverEntryPointSuccess || !fn)
+      return -1;
+    encode = (EncodeTiledFn)fn;
   }
-  const CUresult r = encode(map, type, (cuuint32_t)rank, const_cast<void *>(base), d, s, b, estr,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {cols * 2};
+  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base),
+                            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? 0 : -1;
-}
-
-int dspark_make_tmap_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
-                          uint32_t box_rows) {
-  const uint64_t dims[2] = {cols, rows}, strides[1] = {cols * 2};
-  const uint32_t box[2] = {64, box_rows};
-  return dspark_make_tmap(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box,
-                          CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 int dspark_sm_count() {

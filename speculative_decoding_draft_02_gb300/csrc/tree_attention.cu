@@ -1,7 +1,9 @@
 // tree_attention.cu — dspark_tree_attention: checks, the choice of the row tile,
 // and the launches of tree_attention.cuh.
+#include <atomic>
+
 #include "kv_cache.cuh"
-#include "tcgen05.cuh"
+#include "tcgen05_attn.cuh"
 
 DSPARK_DECLARE_STATUS(s_status_attention)
 
@@ -25,6 +27,49 @@ int row_tile(const dspark_kv_cache *c, int heads_q, int max_nodes) {
   if (c->type == DSPARK_KV_E4M3) return 64;
   if (rows <= 48) return 48;
   return rows <= 64 ? 64 : 128;
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                             const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                             const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's encoder of tensor maps; null while there is none (asked for again then).
+EncodeFn tensor_map_encoder() {
+  static std::atomic<EncodeFn> kept{nullptr};
+  EncodeFn f = kept.load();
+  if (!f) {
+    void *fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    f = (EncodeFn)fn;
+    kept.store(f);
+  }
+  return f;
+}
+
+// A tensor map of RANK dimensions: dims and box in elements (dimension 0 contiguous),
+// strides in bytes for dimensions 1.. (multiples of 16); zeros outside.
+template <int RANK>
+bool make_map(CUtensorMap *map, CUtensorMapDataType type, const void *base,
+              const uint64_t (&dims)[RANK], const uint64_t (&strides)[RANK - 1],
+              const uint32_t (&box)[RANK], CUtensorMapSwizzle swizzle) {
+  const EncodeFn encode = tensor_map_encoder();
+  if (!encode) return false;
+  cuuint64_t d[RANK], s[RANK - 1];
+  cuuint32_t b[RANK], step[RANK];
+  for (int i = 0; i < RANK; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    step[i] = 1;
+    if (i + 1 < RANK) s[i] = strides[i];
+  }
+  return encode(map, type, RANK, const_cast<void *>(base), d, s, b, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 struct Layout {
@@ -68,10 +113,10 @@ int launch(const Launch &l) {
   const uint64_t q_strides[2] = {(uint64_t)l.q_head * 2, (uint64_t)l.q_row * 2};
   const uint32_t q_box[3] = {64, (uint32_t)a.group, (uint32_t)a.nodes_tile};
   CUtensorMap tk, tv, tq;
-  if (dspark_make_tmap(&tk, type, 4, c->k, dims, strides, box, swizzle) != 0 ||
-      dspark_make_tmap(&tv, type, 4, c->v, dims, strides, box, swizzle) != 0 ||
-      dspark_make_tmap(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, l.q, q_dims, q_strides, q_box,
-                       CU_TENSOR_MAP_SWIZZLE_128B) != 0)
+  if (!make_map(&tk, type, c->k, dims, strides, box, swizzle) ||
+      !make_map(&tv, type, c->v, dims, strides, box, swizzle) ||
+      !make_map(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, l.q, q_dims, q_strides, q_box,
+                CU_TENSOR_MAP_SWIZZLE_128B))
     return DSPARK_ERR_CUDA;
   auto kernel = attn::tree_attention_kernel<TYPE, D, NT>;
   static DsparkPerDevice attr;

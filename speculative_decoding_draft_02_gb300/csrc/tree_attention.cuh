@@ -61,7 +61,7 @@
 #include <cuda_fp8.h>
 
 #include "kv_cache.cuh"
-#include "tcgen05.cuh"
+#include "tcgen05_attn.cuh"
 
 namespace attn {
 
