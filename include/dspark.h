@@ -437,10 +437,11 @@ size_t dspark_tree_attention_workspace_bytes(const dspark_kv_cache *cache, int32
  * does not reach it, whatever its bits (infinities and NaN in unwritten or
  * masked places included).  Infinities and NaN in values that a row sees come out as the
  * sum has them, for weights above f32's least; finite values below 2^64 never overflow.
- * Scores, statistics and sums in f32.  Beside a bf16 cache
- * the weights meet V with 16 bits (the sum of two bf16); beside an 8-bit one as f16,
- * with 11 bits, and those below 2^-31 of a row's largest may be lost; q is f16 there too,
- * scaled by a power of two: its 8 bits are whole down to 2^-28 of a tile's largest.
+ * Scores, statistics and sums in f32.  Beside a bf16 cache the weights meet V with 16 bits
+ * (the sum of two bf16); beside an 8-bit one as f16: with 11 bits down to 2^-20 of a row's
+ * largest, below that in steps of 2^-30 of it, and those below 2^-31 of it may be lost (their
+ * sum takes them unrounded); q is f16 there too, scaled by a power of two: its 8 bits are
+ * whole down to 2^-28 of the largest value of a tile, which other rows and heads share.
  *   q, out bf16: element i of head h of row m at m * row_stride + h * head_stride
  *          + i; q 16-byte aligned with strides (in elements) that are multiples of 8;
  *          out's strides at most 2^24

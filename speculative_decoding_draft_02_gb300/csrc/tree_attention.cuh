@@ -24,8 +24,9 @@
 // An 8-bit cache's tiles are widened to f16, which holds every e4m3 value and takes
 // one conversion for two of them (bf16 takes four), and meet Q and P in f16: Q's
 // tile is scaled by the power of two that brings its largest value to 2^14 (f16
-// then keeps all 8 bits of whatever matters to a score), and a weight has 11 bits.
-// Weights are at most 2^14 there and count down to 2^-24.
+// then keeps all 8 bits of what lies within 2^28 of it; a row beside one that is larger
+// by more keeps fewer), and a weight has 11 bits.  Weights are at most 2^14 there and
+// count down to 2^-24, with fewer bits below 2^-14.
 //
 // Work is cut into units of (request, KV head, row tile, 128-token tile), listed
 // in that order, and every CTA takes an equal share of the list: ragged contexts
@@ -35,18 +36,18 @@
 // from call to call).
 //
 // One CTA per SM: warp 0 loads K and V (TMA, one copy per page and 64 columns), warp
-// 1 issues the MMAs, warp 2 loads Q, one or two groups of four warps do the softmax (a warp for each
-// 32 tokens, CH chunks of 16 or 32 columns one after the other), and for an 8-bit
+// 1 issues the MMAs, warp 2 loads Q, two groups of four warps do the softmax (a warp for
+// each 32 tokens, CH chunks of 16 or 32 columns one after the other), and for an 8-bit
 // cache four more widen the tiles to f16 between two rings.
 //
 // What it measured, and what bounds it (D = 128, 32 query heads over 8 KV heads):
 //   256 chains of 1..6 rows over contexts of 64 to 8192 tokens, bf16: 1.77 GB in
-//     264 to 273 us in a graph (boxes differ; 271 to 279 by calls), 6.5 to 6.7 TB/s;
+//     264 to 273 us in a graph (boxes differ; 271 to 281 by calls), 6.5 to 6.7 TB/s;
 //     eight chains over 65536 tokens 6.6 to 6.8: reading K and V.
 //     The copies then are late often enough that the softmax's own time is hidden.
 //   1024 chains over 400 tokens 4.8 TB/s: items begin and end every four tiles.
 //   64 trees of 64 rows over 512 to 4096 tokens, bf16 (two tiles of 128 rows):
-//     120 GFLOP in 299 us.  A tile takes 4200 cycles, of which the softmax's chain is
+//     120 GFLOP in 296 to 303 us.  A tile takes 4200 cycles, of which the softmax's chain is
 //     3650 (scores read and masked 1350, exponentials 1050, which is their unit's
 //     rate, waiting for P's place 400, P written 850); shared memory alone would
 //     take 2300.
@@ -71,7 +72,8 @@ constexpr int CTL_BYTES = 3072;
 constexpr int MAX_SLOTS = 12;           // tiles in a ring
 constexpr int SEGS = 8;                 // segments published ahead
 // What beginning and ending an item costs a CTA, in tiles; counted so that short
-// contexts balance too (256 ragged chains: 282 us with one, 279 with two, 282 with three).
+// contexts balance too.  The number is not critical (256 ragged chains: 282 us with one,
+// 279 with two, 282 with three, where boxes differ by as much).
 constexpr int ITEM_UNITS = 2;
 // log2: how far scores may pass the reference, and where a raised reference puts the
 // largest.  Beside a bf16 cache weights, their sum and O are floating-point numbers
