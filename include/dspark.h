@@ -21,6 +21,13 @@
  *   attention of a drafted tree (or chain) over the cache (dspark_tree_attention)
  *   the path of the tree that the target's choices confirm (dspark_tree_accept)
  *   that path's K and V moved together                    (dspark_kv_compact)
+ * And a prompt's way into that cache, all at once or in chunks beside other
+ * requests' rows, with continuations that share its pages:
+ *   norm and rotation of queries and keys, and the append  (dspark_rope_append)
+ *   attention of any number of new rows over the cache     (dspark_chunk_attention)
+ *   continuations of a request, and pages given back       (dspark_kv_fork, dspark_kv_release)
+ *   the pages in use moved to the lowest numbers           (dspark_kv_squeeze)
+ *   what these two move                                    (dspark_kv_copy)
  *
  * Sources (page title, section):
  *   "DSpark 深度解读" (zhichai.net) §二 设计一 (Markov head, W1: V x r, W2: r x V),
@@ -489,6 +496,139 @@ int dspark_tree_accept(int32_t R, int32_t gamma, int32_t n_rows, const int32_t *
 int dspark_kv_compact(const dspark_kv_cache *cache, int32_t R, int32_t gamma, int32_t max_pages,
                       const int32_t *ctx, const int32_t *accepted, const int32_t *path,
                       const int32_t *block_table, dspark_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A prompt's way into the cache.
+ *
+ * Rows here are those of dspark_kv_plan: a prompt's (extra 0), a chunk of one, or
+ * a round's, any number a request.
+ */
+enum {
+  DSPARK_ROPE_HALVES = 0, /* value i turns with value i + dims / 2                   */
+  DSPARK_ROPE_PAIRS = 1   /* value 2 i turns with value 2 i + 1                      */
+};
+
+/* The rotation of a head's first `dims` values by position p: pair i, (a, b), becomes
+ *   (a cos t - b sin t, b cos t + a sin t),  t = 2 pi p turns[i] / 2^64.
+ * turns[i] is the pair's frequency (radians a position) over 2 pi, as a fraction of
+ * 2^64: p turns[i] modulo 2^64 is then the angle itself, with no error that grows
+ * before p nears 2^31. */
+typedef struct dspark_rope {
+  const uint64_t *turns; /* device [dims / 2]                                        */
+  int32_t dims;          /* a multiple of 16, at most the head's dimension; 0: none  */
+  int32_t style;         /* DSPARK_ROPE_*                                            */
+} dspark_rope;
+
+/* Every head of the queries and keys normalised and turned, the queries into q_out,
+ * keys and values into their slots:
+ *   y = x / sqrt(mean_i x_i^2 + eps) * weight   (weight NULL: y = x)
+ *   q_out[row] = rotation of y, rounded once to bf16
+ *   cache K[slot[row]] = rotation of y, rounded once to bf16, or in a DSPARK_KV_E4M3
+ *   cache clamp(. / scale[head], -448, 448) rounded once (nearest even); V as by
+ *   dspark_kv_append.  Sums, angles and products in f32 or better.
+ *   q        bf16: element i of head h of row m at m * q_row_stride + h * q_head_stride
+ *            + i; k and v alike with the kv strides, q_out with its own.  16-byte
+ *            aligned, strides in elements, multiples of 8.  q_out may be q itself
+ *            (then with the same strides).
+ *   q_weight, k_weight  bf16 [dim], 16-byte aligned, or NULL: no norm of that side
+ *   position int32 [n_rows]: a row whose position is negative is padding, and
+ *            neither read nor written
+ *   slot     int64 [n_rows]: a negative one writes nothing to the cache; one past the
+ *            cache writes nothing there and sets DSPARK_ERR_PAGES
+ * heads_q and the cache's heads at most 65535 each. */
+int dspark_rope_append(const dspark_kv_cache *cache, int32_t n_rows, int32_t heads_q,
+                       const void *q, int64_t q_row_stride, int64_t q_head_stride, const void *k,
+                       const void *v, int64_t kv_row_stride, int64_t kv_head_stride,
+                       const void *q_weight, const void *k_weight, float eps,
+                       const dspark_rope *rope, const int32_t *position, const int64_t *slot,
+                       void *q_out, int64_t out_row_stride, int64_t out_head_stride,
+                       dspark_stream_t stream);
+
+/* Workspace bytes dspark_chunk_attention needs (0 when the sizes are invalid). */
+size_t dspark_chunk_attention_workspace_bytes(const dspark_kv_cache *cache, int32_t R,
+                                              int32_t heads_q, int32_t max_rows);
+
+/* dspark_tree_attention for chains of any length: row i of request r sees the tokens at
+ * positions up to ctx[r] + i, which lie in the cache, its own and the chunk's earlier
+ * ones included (append first).  The formulas, arguments and limits are those of
+ * dspark_tree_attention, but for:
+ *   max_rows  the most rows of a request, >= 1: rows past it are not computed (status
+ *             DSPARK_ERR_LENGTH)
+ *   out       16-byte aligned, its strides multiples of 8 below 2^39
+ * Scores, statistics and sums in f32.  A weight meets V as one bf16 (8 bits; the sum of
+ * the weights takes it unrounded), beside an 8-bit cache too, and K, V and q enter their
+ * products unrounded.  Where no request has more than DSPARK_MAX_NODES rows the call
+ * may be dspark_tree_attention's, with that call's precision. */
+int dspark_chunk_attention(const dspark_kv_cache *cache, int32_t R, int32_t heads_q,
+                           int32_t max_rows, int32_t n_rows, int32_t max_pages, const void *q,
+                           int64_t q_row_stride, int64_t q_head_stride, const int32_t *ctx,
+                           const int32_t *row_start, const int32_t *block_table, float scale,
+                           void *out, int64_t out_row_stride, int64_t out_head_stride, float *lse,
+                           void *workspace, size_t workspace_bytes, dspark_stream_t stream);
+
+/* Pages with several holders.  refs[page] counts a page's holders beyond the first: 0
+ * for a free page and for one that a single request holds, so that it starts at zeros
+ * and dspark_kv_plan's new pages need no entry.  With any page shared, requests that
+ * left (ctx < 0) are released here before dspark_kv_plan, which then finds them without
+ * pages; and a request's ctx does not go back below what it was when it was forked. */
+
+/* Continuations: place target[i] becomes a request like source[i], with its committed
+ * tokens.  The full pages are shared; the tokens of a last page that is not full go to
+ * one from the stack of free pages, whose copy is left to dspark_kv_copy (layer by layer).
+ *   source, target  int32 [n]: places; source[i] < 0: no fork.  A source is there
+ *            (ctx >= 0) and holds pages for its tokens, a target is free (ctx < 0, held
+ *            0); otherwise, or where an earlier fork has the same target, nothing is
+ *            done for this one (status DSPARK_ERR_ARG)
+ *   pages    taken fork by fork, as by dspark_kv_plan.  Once the stack does not cover a
+ *            fork, neither it nor any later one in need gets a page: nothing is done for
+ *            it (status DSPARK_ERR_PAGES)
+ *   ctx, held int32 [R], n_free int32 [1], block_table int32 [R, max_pages], refs int32
+ *            [n_pages]: read and written
+ *   copy_from, copy_to, copy_tokens  int32 [n] out: the page to copy, the page that
+ *            takes it and how many tokens (-1, -1 and 0 without a copy)
+ * R <= 16384, n <= R. */
+int dspark_kv_fork(int32_t n, const int32_t *source, const int32_t *target, int32_t R,
+                   int32_t page_size, int32_t n_pages, int32_t max_pages, int32_t *ctx,
+                   int32_t *held, int32_t *n_free, const int32_t *free_pages,
+                   int32_t *block_table, int32_t *refs, int32_t *copy_from, int32_t *copy_to,
+                   int32_t *copy_tokens, dspark_stream_t stream);
+
+/* The pages of every request that has left (ctx < 0): each gives up its hold, and a page
+ * that nobody holds any more goes back to the stack, request by request and in block
+ * order, a page with several holders that leave together in the place of the last of
+ * them.  held becomes 0.  Tables are left as they are.  A table entry outside the cache, or a page with
+ * more holders than refs says, sets DSPARK_ERR_PAGES.  R <= 16384. */
+int dspark_kv_release(int32_t R, int32_t n_pages, int32_t max_pages, const int32_t *ctx,
+                      int32_t *held, int32_t *n_free, int32_t *free_pages,
+                      const int32_t *block_table, int32_t *refs, dspark_stream_t stream);
+
+/* The pages in use (all but the free ones), U of them, moved to numbers 0..U - 1: those
+ * from U on, ascending, into the free ones below U, ascending.  The rest of the cache is
+ * then free, and its memory may go back.
+ *   free_pages, block_table, refs in, and *_out after the call, which may be the same
+ *            memory: held entries of the table renamed, free_pages_out[i] = n_pages - 1 - i
+ *            for i < n_free (n_free itself stays); what lies past held and past n_free is
+ *            copied
+ *   new_page int32 [n_pages] out: where each page now lies, -1 for a free one
+ *   move_from, move_to  int32 [n_pages / 2] out: the moves, for dspark_kv_copy, then -1
+ *   n_moves  int32 [1] out
+ * A page outside the cache, or twice on the stack, sets DSPARK_ERR_PAGES.  R <= 16384,
+ * n_pages >= 2. */
+int dspark_kv_squeeze(int32_t R, int32_t n_pages, int32_t max_pages, const int32_t *held,
+                      const int32_t *n_free, const int32_t *free_pages,
+                      const int32_t *block_table, const int32_t *refs, int32_t *free_pages_out,
+                      int32_t *block_table_out, int32_t *refs_out, int32_t *new_page,
+                      int32_t *move_from, int32_t *move_to, int32_t *n_moves,
+                      dspark_stream_t stream);
+
+/* One layer's K and V of whole pages, or of a page's first tokens: page to[i] receives
+ * what page from[i] holds, for i < n.  from[i] < 0: nothing.
+ *   tokens  int32 [n], 0..page_size, or NULL: all of them
+ * No page is written twice in a call, or both read and written.  A page outside the
+ * cache sets DSPARK_ERR_PAGES, a count outside its range DSPARK_ERR_LENGTH; neither is
+ * copied. */
+int dspark_kv_copy(const dspark_kv_cache *cache, int32_t n, const int32_t *from,
+                   const int32_t *to, const int32_t *tokens, dspark_stream_t stream);
 
 /* Failure detection self-test (no fault is involved).  Every device-side wait
  * of the library is bounded in time; on expiry the kernel records

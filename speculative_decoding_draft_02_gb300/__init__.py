@@ -10,6 +10,7 @@ tensors; `draft`, `schedule`, `verify` and `run_round` compose them.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 from typing import Dict, Optional
@@ -34,12 +35,16 @@ EXPORTS = [
     "dspark_rnn_draft", "dspark_selftest_wait_timeout", "dspark_fused_workspace_bytes",
     "dspark_pack_fused", "dspark_fused_draft", "dspark_verify_residual_rows",
     "dspark_kv_plan", "dspark_kv_append", "dspark_tree_attention_workspace_bytes",
-    "dspark_tree_attention", "dspark_tree_accept", "dspark_kv_compact",
+    "dspark_tree_attention", "dspark_tree_accept", "dspark_kv_compact", "dspark_rope_append",
+    "dspark_chunk_attention_workspace_bytes", "dspark_chunk_attention", "dspark_kv_fork",
+    "dspark_kv_release", "dspark_kv_squeeze", "dspark_kv_copy",
 ]
 STATIC_SCRATCH_BYTES = 16 << 20
 KV_BF16 = 0
 KV_E4M3 = 1
 MAX_NODES = 64
+ROPE_HALVES = 0
+ROPE_PAIRS = 1
 
 
 class DSparkError(RuntimeError):
@@ -59,6 +64,10 @@ class KVCacheStruct(ctypes.Structure):
                 ("heads", ctypes.c_int32), ("dim", ctypes.c_int32), ("type", ctypes.c_int32)]
 
 
+class RopeStruct(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("dims", ctypes.c_int32), ("style", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -75,6 +84,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                             ctypes.c_float)
     DP = ctypes.POINTER(Dims)
     CP, I64 = ctypes.POINTER(KVCacheStruct), ctypes.c_int64
+    RP = ctypes.POINTER(RopeStruct)
     sig = {
         "dspark_lm_head": (ctypes.c_int, [DP, P, P, P, P]),
         "dspark_pack_w2": (ctypes.c_int, [DP, P, P, P]),
@@ -109,6 +119,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                                  P, F32, P, I64, I64, P, P, SZ, P]),
         "dspark_tree_accept": (ctypes.c_int, [I32, I32, I32, P, P, P, P, P, P, P, P, P, P]),
         "dspark_kv_compact": (ctypes.c_int, [CP, I32, I32, I32, P, P, P, P, P]),
+        "dspark_rope_append": (ctypes.c_int, [CP, I32, I32, P, I64, I64, P, P, I64, I64, P, P, F32,
+                                              RP, P, P, P, I64, I64, P]),
+        "dspark_chunk_attention_workspace_bytes": (SZ, [CP, I32, I32, I32]),
+        "dspark_chunk_attention": (ctypes.c_int, [CP, I32, I32, I32, I32, I32, P, I64, I64, P, P, P,
+                                                  F32, P, I64, I64, P, P, SZ, P]),
+        "dspark_kv_fork": (ctypes.c_int, [I32, P, P, I32, I32, I32, I32] + [P] * 9 + [P]),
+        "dspark_kv_release": (ctypes.c_int, [I32, I32, I32] + [P] * 6 + [P]),
+        "dspark_kv_squeeze": (ctypes.c_int, [I32, I32, I32] + [P] * 12 + [P]),
+        "dspark_kv_copy": (ctypes.c_int, [CP, I32, P, P, P, P]),
         "dspark_device_status": (ctypes.c_int, [P, ctypes.c_int]),
         "dspark_error_string": (ctypes.c_char_p, [ctypes.c_int]),
         "dspark_launch_count": (U64, []),
@@ -469,6 +488,133 @@ def dspark_kv_compact(cache: KVCache, ctx, accepted, path, block_table, stream=N
         _want(what, "block_table", block_table, i32, (R, pages)), _stream(stream)), what)
 
 
+class Rotary:
+    """The rotation of a head's first 2 * len(inv_freq) values (a multiple of 16): pair i by
+    position * inv_freq[i] radians, f64.  A pair is values i and i + len(inv_freq), or with
+    `pairs` values 2 i and 2 i + 1."""
+
+    def __init__(self, inv_freq, pairs=False, device="cuda"):
+        f = torch.as_tensor(inv_freq, dtype=torch.float64)
+        if f.dim() != 1 or f.numel() % 8 or not bool(torch.isfinite(f).all()):
+            raise DSparkError("Rotary: inv_freq must be finite, one for each pair of values, a "
+                              "multiple of 8 of them")
+        # a position's part of a turn, in units of 2^-64
+        words = [round(x / (2 * math.pi) % 1.0 * 2.0 ** 64) % 2 ** 64 for x in f.tolist()]
+        self.turns = torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in words],
+                                  dtype=torch.int64, device=device)
+        self.dims = 2 * len(words)
+        self.struct = RopeStruct(self.turns.data_ptr(), self.dims,
+                                 ROPE_PAIRS if pairs else ROPE_HALVES)
+        self.ref = ctypes.byref(self.struct)
+
+
+def dspark_rope_append(cache: KVCache, q, k, v, position, slot, rotary: Rotary, q_out,
+                       q_weight=None, k_weight=None, eps=1e-6, stream=None):
+    """q, q_out bf16 [rows, heads_q, dim], k, v bf16 [rows, heads, dim] (k and v of equal
+    strides); weights bf16 [dim] or None (no norm of that side).  q_out may be q."""
+    what = "dspark_rope_append"
+    heads_q = _size(what, "q", q, 3)[1]
+    qp, rows, q_row, q_head = _rows_view(what, "q", q, heads_q, cache.dim)
+    kp, *rest = _rows_view(what, "k", k, cache.heads, cache.dim)
+    vp, *also = _rows_view(what, "v", v, cache.heads, cache.dim)
+    op, o_rows, o_row, o_head = _rows_view(what, "q_out", q_out, heads_q, cache.dim)
+    if rest != also or rest[0] != rows or o_rows != rows:
+        raise DSparkError(f"{what}: q, k, v and q_out must have equal rows, k and v equal strides")
+    bf16, width = torch.bfloat16, (cache.dim,)
+    _check(load_library().dspark_rope_append(
+        cache.ref, rows, heads_q, qp, q_row, q_head, kp, vp, rest[1], rest[2],
+        None if q_weight is None else _want(what, "q_weight", q_weight, bf16, width),
+        None if k_weight is None else _want(what, "k_weight", k_weight, bf16, width), eps,
+        rotary.ref, _want(what, "position", position, torch.int32, (rows,)),
+        _want(what, "slot", slot, torch.int64, (rows,)), op, o_row, o_head, _stream(stream)), what)
+
+
+def dspark_chunk_attention_workspace_bytes(cache: KVCache, R, heads_q, max_rows) -> int:
+    return int(load_library().dspark_chunk_attention_workspace_bytes(
+        cache.ref, int(R), int(heads_q), int(max_rows)))
+
+
+def dspark_chunk_attention(cache: KVCache, q, ctx, row_start, block_table, max_rows, scale, out,
+                           lse, workspace, stream=None):
+    """q, out bf16 [rows, heads_q, dim] (views with a dense last dimension); lse may be None."""
+    what, i32 = "dspark_chunk_attention", torch.int32
+    R, heads_q = len(ctx), _size(what, "q", q, 3)[1]
+    qp, rows, q_row, q_head = _rows_view(what, "q", q, heads_q, cache.dim)
+    op, o_rows, o_row, o_head = _rows_view(what, "out", out, heads_q, cache.dim)
+    if o_rows != rows:
+        raise DSparkError(f"{what}: out must have q's rows")
+    pages = _size(what, "block_table", block_table, 2)[1]
+    _check(load_library().dspark_chunk_attention(
+        cache.ref, R, heads_q, max_rows, rows, pages, qp, q_row, q_head,
+        _want(what, "ctx", ctx, i32, (R,)), _want(what, "row_start", row_start, i32, (R + 1,)),
+        _want(what, "block_table", block_table, i32, (R, pages)), scale, op, o_row, o_head,
+        None if lse is None else _want(what, "lse", lse, torch.float32, (rows, heads_q)),
+        _ptr(workspace), workspace.numel(), _stream(stream)), what)
+
+
+def dspark_kv_fork(source, target, page_size, ctx, held, n_free, free_pages, block_table, refs,
+                   copy_from, copy_to, copy_tokens, stream=None):
+    """Writes ctx, held, n_free, block_table and refs in place."""
+    what, i32 = "dspark_kv_fork", torch.int32
+    n, R, pages = len(source), len(ctx), len(free_pages)
+    table = _size(what, "block_table", block_table, 2)
+    _check(load_library().dspark_kv_fork(
+        n, _want(what, "source", source, i32, (n,)), _want(what, "target", target, i32, (n,)), R,
+        page_size, pages, table[1], _want(what, "ctx", ctx, i32, (R,)),
+        _want(what, "held", held, i32, (R,)), _want(what, "n_free", n_free, i32, (1,)),
+        _want(what, "free_pages", free_pages, i32, (pages,)),
+        _want(what, "block_table", block_table, i32, (R, table[1])),
+        _want(what, "refs", refs, i32, (pages,)), _want(what, "copy_from", copy_from, i32, (n,)),
+        _want(what, "copy_to", copy_to, i32, (n,)),
+        _want(what, "copy_tokens", copy_tokens, i32, (n,)), _stream(stream)), what)
+
+
+def dspark_kv_release(ctx, held, n_free, free_pages, block_table, refs, stream=None):
+    """Writes held, n_free, free_pages and refs in place."""
+    what, i32 = "dspark_kv_release", torch.int32
+    R, pages = len(ctx), len(free_pages)
+    table = _size(what, "block_table", block_table, 2)
+    _check(load_library().dspark_kv_release(
+        R, pages, table[1], _want(what, "ctx", ctx, i32, (R,)), _want(what, "held", held, i32, (R,)),
+        _want(what, "n_free", n_free, i32, (1,)),
+        _want(what, "free_pages", free_pages, i32, (pages,)),
+        _want(what, "block_table", block_table, i32, (R, table[1])),
+        _want(what, "refs", refs, i32, (pages,)), _stream(stream)), what)
+
+
+def dspark_kv_squeeze(held, n_free, free_pages, block_table, refs, free_pages_out, block_table_out,
+                      refs_out, new_page, move_from, move_to, n_moves, stream=None):
+    """move_from and move_to have half as many entries as there are pages; the *_out tensors
+    may be the inputs."""
+    what, i32 = "dspark_kv_squeeze", torch.int32
+    R, pages = len(held), len(free_pages)
+    table = _size(what, "block_table", block_table, 2)
+    shape, half = (R, table[1]), (pages // 2,)
+    _check(load_library().dspark_kv_squeeze(
+        R, pages, table[1], _want(what, "held", held, i32, (R,)),
+        _want(what, "n_free", n_free, i32, (1,)),
+        _want(what, "free_pages", free_pages, i32, (pages,)),
+        _want(what, "block_table", block_table, i32, shape),
+        _want(what, "refs", refs, i32, (pages,)),
+        _want(what, "free_pages_out", free_pages_out, i32, (pages,)),
+        _want(what, "block_table_out", block_table_out, i32, shape),
+        _want(what, "refs_out", refs_out, i32, (pages,)),
+        _want(what, "new_page", new_page, i32, (pages,)),
+        _want(what, "move_from", move_from, i32, half), _want(what, "move_to", move_to, i32, half),
+        _want(what, "n_moves", n_moves, i32, (1,)), _stream(stream)), what)
+
+
+def dspark_kv_copy(cache: KVCache, copy_from, copy_to, copy_tokens=None, stream=None):
+    """copy_tokens None: whole pages."""
+    what, i32 = "dspark_kv_copy", torch.int32
+    n = len(copy_from)
+    _check(load_library().dspark_kv_copy(
+        cache.ref, n, _want(what, "copy_from", copy_from, i32, (n,)),
+        _want(what, "copy_to", copy_to, i32, (n,)),
+        None if copy_tokens is None else _want(what, "copy_tokens", copy_tokens, i32, (n,)),
+        _stream(stream)), what)
+
+
 def dspark_device_status(stream=None, clear: bool = True) -> int:
     return int(load_library().dspark_device_status(_stream(stream), 1 if clear else 0))
 
@@ -504,9 +650,12 @@ class PagePool:
 
     `ctx` holds the committed tokens, -1 for a free place; a request enters when its
     prompt's rows are planned with ctx 0, and leaves when its ctx is set to -1 (its
-    pages go back with the next plan)."""
+    pages go back with the next plan).
 
-    def __init__(self, R, n_pages, page_size, max_tokens, n_rows, device="cuda"):
+    A `shared` pool's requests may be forked: continuations share a prompt's full pages,
+    and a page goes back with the last of its holders."""
+
+    def __init__(self, R, n_pages, page_size, max_tokens, n_rows, device="cuda", shared=False):
         new = lambda shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device=device)  # noqa: E731
         self.page_size, self.n_rows = page_size, n_rows
         max_pages = -(-max_tokens // page_size)
@@ -522,10 +671,20 @@ class PagePool:
         self._live, self._step = new(R, torch.bool), new(R)
         self._prompts = False  # the rows planned last are prompts': anc is not theirs
         self._ws = {}
+        self.shared = shared
+        self.refs = None       # holders of a page beyond the first
+        if shared:
+            self.refs = torch.zeros((n_pages,), dtype=torch.int32, device=device)
+            self._copies = [new(R) for _ in range(3)]    # of the last fork: from, to, tokens
+            self.copies = [t[:0] for t in self._copies]
+            self.new_page, self.n_moves = new(n_pages), new(1)
+            self.move_from, self.move_to = new(n_pages // 2), new(n_pages // 2)
 
     def plan(self, length, extra=1, parent=None, stream=None):
         """Rows, pages, slots, positions (and masks, in a round) for `length` + extra new
         rows of each request: extra 1 in a round, 0 for prompts."""
+        if self.shared:
+            self.release(stream)
         dspark_kv_plan(self.ctx, length, extra, parent, self.page_size, self.held, self.n_free,
                        self.free_pages, self.block_table, self.held, self.n_free,
                        self.row_start, self.position, self.slot, self.anc if extra else None,
@@ -536,15 +695,30 @@ class PagePool:
         """One layer's new rows into the planned slots."""
         dspark_kv_append(cache, k, v, self.slot, stream)
 
+    def rope_append(self, cache: KVCache, q, k, v, rotary: Rotary, q_out, q_weight=None,
+                    k_weight=None, eps=1e-6, stream=None):
+        """append, with the queries' and keys' heads normalised (where they have weights) and
+        turned by the planned positions; the queries go to q_out, which may be q."""
+        dspark_rope_append(cache, q, k, v, self.position, self.slot, rotary, q_out, q_weight,
+                           k_weight, eps, stream)
+
     def attend(self, cache: KVCache, q, max_nodes, out, lse=None, scale=None, stream=None):
         """One layer's attention of the rows that plan was last called for, over contexts and
-        trees; a prompt's (up to MAX_NODES rows a request) are chains.  Which of the two is
-        settled at the call: a graph that holds an attend holds its plan too."""
+        trees; a prompt's (max_nodes rows a request at most, any number) are chains.  Which of
+        the two is settled at the call: a graph that holds an attend holds its plan too."""
+        scale = cache.dim ** -0.5 if scale is None else scale
+        if self._prompts and max_nodes > MAX_NODES:
+            need = dspark_chunk_attention_workspace_bytes(cache, len(self.ctx), q.shape[1],
+                                                          max_nodes)
+            ws = self._scratch(need, q.device, stream)
+            dspark_chunk_attention(cache, q, self.ctx, self.row_start, self.block_table, max_nodes,
+                                   scale, out, lse, ws, stream)
+            return
         need = dspark_tree_attention_workspace_bytes(cache, len(self.ctx), q.shape[1], max_nodes)
         ws = self._scratch(need, q.device, stream)
         dspark_tree_attention(cache, q, self.ctx, self.row_start,
                               None if self._prompts else self.anc, self.block_table, max_nodes,
-                              cache.dim ** -0.5 if scale is None else scale, out, lse, ws, stream)
+                              scale, out, lse, ws, stream)
 
     def _scratch(self, need, device, stream):
         """An attention's workspace, which no call on another stream may use meanwhile: kept
@@ -578,6 +752,45 @@ class PagePool:
 
     def compact(self, cache: KVCache, path, stream=None):
         dspark_kv_compact(cache, self.ctx_before, self.accepted, path, self.block_table, stream)
+
+    def _needs_shared(self, what):
+        if not self.shared:
+            raise DSparkError(f"PagePool.{what}: the pool must be made with shared=True")
+
+    def fork(self, source, target, stream=None):
+        """Free places target[i] become continuations of requests source[i] (int32, one for
+        each fork; source[i] < 0: none).  Each layer's cache then needs copy()."""
+        self._needs_shared("fork")
+        if len(source) > len(self.ctx):
+            raise DSparkError("PagePool.fork: more forks than places")
+        self.copies = [t[:len(source)] for t in self._copies]
+        dspark_kv_fork(source, target, self.page_size, self.ctx, self.held, self.n_free,
+                       self.free_pages, self.block_table, self.refs, *self.copies, stream)
+
+    def copy(self, cache: KVCache, stream=None):
+        """One layer's part of the last fork: the last pages' tokens."""
+        self._needs_shared("copy")
+        dspark_kv_copy(cache, *self.copies, stream)
+
+    def release(self, stream=None):
+        """The pages of the requests that left (ctx -1), now rather than with the next plan."""
+        self._needs_shared("release")
+        dspark_kv_release(self.ctx, self.held, self.n_free, self.free_pages, self.block_table,
+                          self.refs, stream)
+
+    def squeeze(self, stream=None):
+        """The pages in use renamed to the lowest numbers (and those of requests that left given
+        back).  Each layer's cache then needs move(); a planned round's slots are void."""
+        self._needs_shared("squeeze")
+        self.release(stream)
+        dspark_kv_squeeze(self.held, self.n_free, self.free_pages, self.block_table, self.refs,
+                          self.free_pages, self.block_table, self.refs, self.new_page,
+                          self.move_from, self.move_to, self.n_moves, stream)
+
+    def move(self, cache: KVCache, stream=None):
+        """One layer's part of the last squeeze."""
+        self._needs_shared("move")
+        dspark_kv_copy(cache, self.move_from, self.move_to, None, stream)
 
 
 @dataclass

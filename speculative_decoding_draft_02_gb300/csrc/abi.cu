@@ -17,6 +17,9 @@ int dspark_status_sts(int clear);
 int dspark_status_selftest(int clear);
 int dspark_status_kv(int clear);
 int dspark_status_attention(int clear);
+int dspark_status_rope(int clear);
+int dspark_status_pages(int clear);
+int dspark_status_chunk(int clear);
 
 extern "C" uint64_t dspark_launch_count(void) { return g_launches.load(); }
 
@@ -39,10 +42,12 @@ extern "C" const char *dspark_error_string(int code) {
 extern "C" int dspark_device_status(dspark_stream_t stream, int clear) {
   if (cudaStreamSynchronize(stream) != cudaSuccess) return DSPARK_ERR_CUDA;
   int first = DSPARK_OK;
-  const int vals[8] = {dspark_status_lmhead(clear), dspark_status_markov(clear),
-                       dspark_status_verify(clear), dspark_status_sched(clear),
-                       dspark_status_sts(clear),    dspark_status_selftest(clear),
-                       dspark_status_kv(clear),     dspark_status_attention(clear)};
+  const int vals[] = {dspark_status_lmhead(clear), dspark_status_markov(clear),
+                      dspark_status_verify(clear), dspark_status_sched(clear),
+                      dspark_status_sts(clear),    dspark_status_selftest(clear),
+                      dspark_status_kv(clear),     dspark_status_attention(clear),
+                      dspark_status_rope(clear),   dspark_status_pages(clear),
+                      dspark_status_chunk(clear)};
   for (int v : vals)
     if (first == DSPARK_OK && v != DSPARK_OK) first = v;
   return first;

@@ -1,8 +1,6 @@
 // kv_cache.cu — the bookkeeping of a round over the target's paged KV cache:
 // rows, pages, slots and masks (plan), writing the rows (append), the confirmed
 // path of a drafted tree (accept) and moving it together (compact).
-#include <cuda_fp8.h>
-
 #include "kv_cache.cuh"
 
 DSPARK_DECLARE_STATUS(s_status_kv)
@@ -287,35 +285,6 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) kv_plan_kernel(const PlanArgs
 }
 
 // ------------------------------------------------------------------ append ----
-
-struct CacheView {
-  uint8_t *k, *v;
-  const float *k_scale, *v_scale;
-  int64_t page_bytes, token_bytes, head_bytes;
-  int n_pages, page_shift, heads, dim;
-};
-
-CacheView view_of(const dspark_kv_cache *c) {
-  const int64_t size = dspark_kv_bytes(c->type);
-  CacheView v;
-  v.k = (uint8_t *)c->k;
-  v.v = (uint8_t *)c->v;
-  v.k_scale = c->k_scale;
-  v.v_scale = c->v_scale;
-  v.page_bytes = c->page_stride * size;
-  v.token_bytes = c->token_stride * size;
-  v.head_bytes = c->head_stride * size;
-  v.n_pages = c->n_pages;
-  v.page_shift = 31 - __builtin_clz((unsigned)c->page_size);
-  v.heads = c->heads;
-  v.dim = c->dim;
-  return v;
-}
-
-// Two f32 values as e4m3, saturating at +-448 (the conversion's finite form).
-__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-}
 
 // Four bf16 over a scale as e4m3 (out of line: it is seldom called).
 __device__ __noinline__ uint32_t divide_four(uint32_t a, uint32_t b, float scale) {
