@@ -1,120 +1,83 @@
-// chunk_attention.cu — dspark_chunk_attention: attention of any number of new rows of each
-// request over its paged cache, each row over the tokens up to its own position.
-//
-//   s_p = scale * q . K_p,  out = sum_p e^{s_p} V_p / sum_p e^{s_p},  p <= ctx + i
+// chunk_attention.cu — dspark_chunk_attention: checks, and the launches of
+// chunk_attention.cuh.
 #include "kv_cache.cuh"
+#include "tcgen05_attn.cuh"
+#include "tensor_map.cuh"
 
 DSPARK_DECLARE_STATUS(s_status_chunk)
 
+#include "chunk_attention.cuh"
+
 namespace {
 
-struct Args {
-  CacheView c;
-  int R, heads_q, max_rows, n_rows, max_pages;
-  const bf16 *q;
+using chunk::Args;
+
+struct Layout {
+  size_t ml, desc, bytes;
+};
+Layout layout_of(int ctas, int dim) {
+  Layout l;
+  l.ml = dspark_align_up((size_t)ctas * 2 * 2 * chunk::BM * dim * sizeof(float), 256);
+  l.desc = l.ml + dspark_align_up((size_t)ctas * 2 * 4 * chunk::BM * sizeof(float), 256);
+  l.bytes = l.desc + dspark_align_up((size_t)ctas * 8 * sizeof(int), 256);
+  return l;
+}
+
+// Few rows leave the 128-row tiles empty: the tree attention has the tokens there.
+bool as_tree(int max_rows) { return max_rows <= DSPARK_MAX_NODES; }
+
+struct Launch {
+  const dspark_kv_cache *cache;
+  Args a;
+  const void *q;
   int64_t q_row, q_head;
-  const int *ctx, *row_start, *block_table;
-  float scale;
-  bf16 *out;
-  int64_t out_row, out_head;
-  float *lse;
+  int ctas;
+  cudaStream_t stream;
 };
 
-// A warp takes a row and a query head, 32 tokens at a time: a lane a token for the scores,
-// D / 32 columns for the sums.
-template <int D, bool FP8>
-__global__ void __launch_bounds__(128) chunk_attention_kernel(const Args a) {
-  constexpr int E = D / 32;
-  __shared__ float qs[4][D];
-  const CacheView &c = a.c;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int group = a.heads_q / c.heads;
-  for (int64_t unit = (int64_t)blockIdx.x * 4 + w; unit < (int64_t)a.n_rows * a.heads_q;
-       unit += (int64_t)gridDim.x * 4) {
-    const int row = (int)(unit / a.heads_q), h = (int)(unit - (int64_t)row * a.heads_q);
-    int lo = 0, hi = a.R - 1;  // the last request whose first row is <= row
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (a.row_start[mid] <= row) lo = mid;
-      else hi = mid - 1;
-    }
-    const int i = row - a.row_start[lo];
-    if (i < 0 || row >= a.row_start[lo + 1]) continue;
-    if (i >= a.max_rows) {
-      dspark_set_status(DSPARK_ERR_LENGTH);
-      continue;
-    }
-    const long long cap = (long long)a.max_pages << c.page_shift;
-    long long total = (long long)max(a.ctx[lo], 0) + i + 1;
-    if (total > cap) {
-      dspark_set_status(DSPARK_ERR_LENGTH);
-      total = cap;
-    }
-    const int g = h / group;
-    const float ks = FP8 && c.k_scale ? c.k_scale[g] : 1.0f;
-    const float vs = FP8 && c.v_scale ? c.v_scale[g] : 1.0f;
-    __syncwarp();
-    for (int d = lane; d < D; d += 32)
-      qs[w][d] = __bfloat162float(a.q[row * a.q_row + h * a.q_head + d]);
-    __syncwarp();
-    float m = -INFINITY, sum = 0.0f, o[E] = {};
-    for (long long p0 = 0; p0 < total; p0 += 32) {
-      const long long p = p0 + lane;
-      int page = -1;
-      int64_t at = 0;
-      float s = -INFINITY;
-      if (p < total) {
-        page = a.block_table[(size_t)lo * a.max_pages + (p >> c.page_shift)];
-        if (page < 0 || page >= c.n_pages) {
-          dspark_set_status(DSPARK_ERR_PAGES);
-          page = -1;
-        }
-        at = page * c.page_bytes + (p & ((1 << c.page_shift) - 1)) * c.token_bytes + g * c.head_bytes;
-        float dot = 0.0f;
-        if (page >= 0)
-          for (int d = 0; d < D; ++d) {
-            float k;
-            if (FP8) {
-              __half_raw r = __nv_cvt_fp8_to_halfraw(c.k[at + d], __NV_E4M3);
-              k = __half2float(__half(r));
-            } else {
-              k = __bfloat162float(reinterpret_cast<const bf16 *>(c.k + at)[d]);
-            }
-            dot = fmaf(qs[w][d], k, dot);
-          }
-        s = dot * (a.scale * ks);
-      }
-      const float top = warp_max(s);
-      const float to = fmaxf(m, top);
-      const float keep = m == -INFINITY ? 0.0f : expf(m - to);
-      const float e = p < total ? (to == -INFINITY ? 0.0f : expf(s - to)) : 0.0f;
-      sum = sum * keep + warp_sum(e);
-#pragma unroll
-      for (int k = 0; k < E; ++k) o[k] *= keep;
-      for (int j = 0; j < 32 && p0 + j < total; ++j) {
-        const float pj = __shfl_sync(0xffffffffu, e, j);
-        const int64_t aj = __shfl_sync(0xffffffffu, at, j);
-        if (__shfl_sync(0xffffffffu, page, j) < 0) continue;
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
-          const int d = lane + 32 * k;
-          float v;
-          if (FP8) {
-            __half_raw r = __nv_cvt_fp8_to_halfraw(c.v[aj + d], __NV_E4M3);
-            v = __half2float(__half(r));
-          } else {
-            v = __bfloat162float(reinterpret_cast<const bf16 *>(c.v + aj)[d]);
-          }
-          o[k] = fmaf(pj, v, o[k]);
-        }
-      }
-      m = to;
-    }
-#pragma unroll
-    for (int k = 0; k < E; ++k)
-      a.out[row * a.out_row + h * a.out_head + lane + 32 * k] = __float2bfloat16_rn(o[k] * vs / sum);
-    if (a.lse && lane == 0) a.lse[(size_t)row * a.heads_q + h] = m + logf(sum);
-  }
+template <int TYPE, int D>
+int launch(const Launch &l) {
+  using G = chunk::Geo<TYPE, D>;
+  const dspark_kv_cache *c = l.cache;
+  const Args &a = l.a;
+  const uint64_t size = G::FP8 ? 1 : 2;
+  const uint64_t dims[4] = {(uint64_t)D, (uint64_t)c->page_size, (uint64_t)c->heads,
+                            (uint64_t)c->n_pages};
+  const uint64_t strides[3] = {c->token_stride * size, c->head_stride * size,
+                               c->page_stride * size};
+  const uint32_t rows = c->page_size < chunk::BT ? c->page_size : chunk::BT;
+  const uint32_t box[4] = {G::FP8 ? (uint32_t)D : 64u, rows, 1, 1};
+  const CUtensorMapDataType type =
+      G::FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle swizzle =
+      G::FP8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  const uint64_t q_dims[3] = {(uint64_t)D, (uint64_t)(a.heads * a.group), (uint64_t)a.n_rows};
+  const uint64_t q_strides[2] = {(uint64_t)l.q_head * 2, (uint64_t)l.q_row * 2};
+  const uint32_t q_box[3] = {64, (uint32_t)a.group, (uint32_t)a.nodes_tile};
+  CUtensorMap tk, tv, tq;
+  if (!make_map(&tk, type, c->k, dims, strides, box, swizzle) ||
+      !make_map(&tv, type, c->v, dims, strides, box, swizzle) ||
+      !make_map(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, l.q, q_dims, q_strides, q_box,
+                CU_TENSOR_MAP_SWIZZLE_128B))
+    return DSPARK_ERR_CUDA;
+  auto kernel = chunk::chunk_attention_kernel<TYPE, D>;
+  static DsparkPerDevice attr;
+  if (dspark_per_device(attr, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    G::SMEM_BYTES) == cudaSuccess
+                   ? 1
+                   : -1;
+      }) < 0)
+    return DSPARK_ERR_CUDA;
+  if (dspark_launch_pdl(kernel, dim3(l.ctas), dim3(G::THREADS), G::SMEM_BYTES, l.stream, tk, tv,
+                        tq, a) != cudaSuccess)
+    return DSPARK_ERR_CUDA;
+  if (dspark_launch_pdl(chunk::chunk_attention_join<D>, dim3(l.ctas, 2, D / 32), dim3(chunk::BM),
+                        0, l.stream, a) != cudaSuccess)
+    return DSPARK_ERR_CUDA;
+  DSPARK_CHECK_LAUNCH();
+  dspark_count_launches(2);
+  return DSPARK_OK;
 }
 
 }  // namespace
@@ -124,7 +87,10 @@ extern "C" size_t dspark_chunk_attention_workspace_bytes(const dspark_kv_cache *
   if (!dspark_kv_cache_ok(cache) || R < 1 || heads_q < 1 || heads_q % cache->heads ||
       heads_q / cache->heads > 64 || max_rows < 1)
     return 0;
-  return 256;
+  const size_t own = layout_of(dspark_sm_count(), cache->dim).bytes;
+  if (!as_tree(max_rows)) return own;
+  const size_t tree = dspark_tree_attention_workspace_bytes(cache, R, heads_q, max_rows);
+  return own > tree ? own : tree;
 }
 
 extern "C" int dspark_chunk_attention(const dspark_kv_cache *cache, int32_t R, int32_t heads_q,
@@ -138,7 +104,7 @@ extern "C" int dspark_chunk_attention(const dspark_kv_cache *cache, int32_t R, i
   const size_t need = dspark_chunk_attention_workspace_bytes(cache, R, heads_q, max_rows);
   if (need == 0 || n_rows < 0 || max_pages < 1) return DSPARK_ERR_ARG;
   if (n_rows == 0) return DSPARK_OK;
-  const int64_t most = (int64_t)1 << 39;
+  const int64_t most = (int64_t)1 << 39;  // elements: a tensor map's strides are below 2^40 bytes
   if (!q || !ctx || !row_start || !block_table || !out ||
       (((uintptr_t)q | (uintptr_t)out) & 15) || q_row_stride <= 0 || q_head_stride <= 0 ||
       q_row_stride >= most || q_head_stride >= most || q_row_stride % 8 || q_head_stride % 8 ||
@@ -147,37 +113,52 @@ extern "C" int dspark_chunk_attention(const dspark_kv_cache *cache, int32_t R, i
     return DSPARK_ERR_ARG;
   if (!workspace || ((uintptr_t)workspace & 255) || workspace_bytes < need)
     return DSPARK_ERR_WORKSPACE;
-  Args a;
-  a.c = view_of(cache);
+  const int64_t tree_out = (int64_t)1 << 24;  // the tree attention's limit
+  if (as_tree(max_rows) && out_row_stride <= tree_out && out_head_stride <= tree_out)
+    return dspark_tree_attention(cache, R, heads_q, max_rows, n_rows, max_pages, q, q_row_stride,
+                                 q_head_stride, ctx, row_start, nullptr, block_table, scale, out,
+                                 out_row_stride, out_head_stride, lse, workspace, workspace_bytes,
+                                 stream);
+  Launch l;
+  l.cache = cache;
+  l.q = q;
+  l.q_row = q_row_stride;
+  l.q_head = q_head_stride;
+  l.ctas = dspark_sm_count();
+  l.stream = stream;
+  const bool fp8 = cache->type == DSPARK_KV_E4M3;
+  const Layout at = layout_of(l.ctas, cache->dim);
+  const int64_t size = dspark_kv_bytes(cache->type);
+  Args &a = l.a;
   a.R = R;
-  a.heads_q = heads_q;
+  a.heads = cache->heads;
+  a.group = heads_q / cache->heads;
+  a.nodes_tile = chunk::BM / a.group;
   a.max_rows = max_rows;
   a.n_rows = n_rows;
   a.max_pages = max_pages;
-  a.q = (const bf16 *)q;
-  a.q_row = q_row_stride;
-  a.q_head = q_head_stride;
+  a.page_shift = 31 - __builtin_clz((unsigned)cache->page_size);
+  a.n_pages = cache->n_pages;
   a.ctx = ctx;
   a.row_start = row_start;
   a.block_table = block_table;
+  a.k_scale = fp8 ? cache->k_scale : nullptr;
+  a.v_scale = fp8 ? cache->v_scale : nullptr;
+  a.v = (const uint8_t *)cache->v;
+  a.page_bytes = cache->page_stride * size;
+  a.token_bytes = cache->token_stride * size;
+  a.head_bytes = cache->head_stride * size;
   a.scale = scale;
   a.out = (bf16 *)out;
   a.out_row = out_row_stride;
   a.out_head = out_head_stride;
   a.lse = lse;
-  const bool fp8 = cache->type == DSPARK_KV_E4M3;
-  const int64_t blocks = ((int64_t)n_rows * heads_q + 3) / 4, cap = (int64_t)dspark_sm_count() * 64;
-  const dim3 grid((unsigned)(blocks < cap ? blocks : cap));
-  if (cache->dim == 64) {
-    if (fp8) chunk_attention_kernel<64, true><<<grid, 128, 0, stream>>>(a);
-    else chunk_attention_kernel<64, false><<<grid, 128, 0, stream>>>(a);
-  } else {
-    if (fp8) chunk_attention_kernel<128, true><<<grid, 128, 0, stream>>>(a);
-    else chunk_attention_kernel<128, false><<<grid, 128, 0, stream>>>(a);
-  }
-  DSPARK_CHECK_LAUNCH();
-  dspark_count_launches(1);
-  return DSPARK_OK;
+  a.part_o = (float4 *)workspace;
+  a.part_ml = (float *)((uint8_t *)workspace + at.ml);
+  a.desc = (int *)((uint8_t *)workspace + at.desc);
+  if (fp8)
+    return cache->dim == 64 ? launch<DSPARK_KV_E4M3, 64>(l) : launch<DSPARK_KV_E4M3, 128>(l);
+  return cache->dim == 64 ? launch<DSPARK_KV_BF16, 64>(l) : launch<DSPARK_KV_BF16, 128>(l);
 }
 
 int dspark_status_chunk(int clear) {

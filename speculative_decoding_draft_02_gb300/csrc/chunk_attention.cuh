@@ -1,0 +1,1022 @@
+// chunk_attention.cuh — attention of any number of new rows of each request over its
+// paged KV cache, each row over the tokens up to its own position, on the tensor cores.
+//
+//   s_p = scale * q . K_p,  out = sum_p e^{s_p} V_p / sum_p e^{s_p},  p <= ctx + i
+//
+// Many rows meet every token here, so the products bound it, and the rows are the
+// 128-row operand: a CTA takes an item, two tiles of 128 rows (nodes x query heads of one
+// KV head) of one request and KV head, over the item's tokens in tiles of 128:
+//   S_x [128 rows x 128 tokens] = Q_x . K^T       O_x [128 x D] += P_x . V     x = 0, 1
+// A thread owns a row (a TMEM lane): maximum, sum and reference of its softmax lie in
+// its registers, with no exchange between threads.  P takes the place of S in tensor
+// memory, as bf16, and is the second product's operand from there: no weight passes
+// through shared memory.  While one tile's softmax runs, the other's products do.
+//
+// The reference of a row's exponents is kept from tile to tile and raised (with O
+// rescaled) only where a weight would exceed 2^RAISE: weights, sums and O have f32's
+// range, so nothing is lost by it.
+//
+// Work is counted in tokens: an item costs its tokens and OVERHEAD more, the list of all
+// items is cut into equal shares, one for each CTA, at tile boundaries, and the pieces of
+// cut items are joined in order by chunk_attention_join (no atomics: the same bits from
+// call to call).  Ragged batches balance so, and few rows over a long context are split
+// over the GPU.
+//
+// One CTA per SM: warp 0 copies K and V (TMA, one copy for a page and 64 columns), warp 1
+// issues the products, warp 2 copies Q, warp 3 clears what no row of the item may meet
+// out of V's last tiles, two groups of four warps do the softmax of a tile each.  Beside
+// an 8-bit cache four more warps widen the tiles to bf16, which holds every e4m3 value.
+// Every wait is bounded; on expiry the CTA raises DSPARK_ERR_TIMEOUT, drains its own
+// copies and MMAs, frees TMEM and exits.
+#pragma once
+#include "tree_attention.cuh"
+
+namespace chunk {
+
+using attn::fewer_registers;
+using attn::more_registers;
+using attn::pack_bf16;
+using attn::warp_wait;
+
+constexpr int BT = 128;             // tokens of a tile
+constexpr int BM = 128;             // rows of a tile of Q
+constexpr int SMEM_LIMIT = 232448;  // 227 KB
+constexpr int CTL_BYTES = 3072;
+constexpr int MAX_SLOTS = 4;
+constexpr int SEGS = 4;             // segments published ahead
+// What beginning and ending an item costs, in tokens; the least share worth a CTA of its
+// own; and the least piece, in tiles, that an item is cut into.
+constexpr int OVERHEAD = 256, MIN_SHARE = 768, MIN_PIECE = 2;
+constexpr float RAISE = 32.0f;      // log2
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+struct Args {
+  int R, heads, group, nodes_tile, max_rows, n_rows, max_pages, page_shift, n_pages;
+  const int *ctx, *row_start, *block_table;
+  const float *k_scale, *v_scale;
+  const uint8_t *v;                     // for non-finite values only
+  int64_t page_bytes, token_bytes, head_bytes;
+  float scale;
+  bf16 *out;
+  int64_t out_row, out_head;
+  float *lse;
+  float4 *part_o;                       // [ctas][2][D / 4][2 BM]
+  float *part_ml;                       // [ctas][2][2][2 BM]
+  int *desc;                            // [ctas][8]: the item each CTA leaves, see below
+};
+// desc: 0 whether the CTA leaves an item to its successors, then its row0, node0, nodes,
+// head; 5 whether the CTA's first item began before it: 1 and goes on after it, 2 and ends.
+
+template <int TYPE, int D>
+struct Geo {
+  static constexpr bool FP8 = TYPE == DSPARK_KV_E4M3;
+  static constexpr int CV = FP8 ? 4 : 0;
+  static constexpr int THREADS = 32 * (12 + CV);
+  static constexpr int REGS_FEW = FP8 ? 56 : 64, REGS_SOFTMAX = FP8 ? 184 : 216, REGS_WIDEN = 88;
+  static_assert(REGS_FEW + 2 * REGS_SOFTMAX + (FP8 ? REGS_WIDEN : 0) <=
+                    65536 / THREADS / 8 * 8 * (THREADS / 128),
+                "a block's registers");
+  static constexpr int SLOT = BT * D * 2, RAW = FP8 ? BT * D : 0;
+  static constexpr int Q_ONE = BM * D * 2, Q_BYTES = 2 * Q_ONE;
+  static constexpr int KS = D == 64 ? 4 : 2, VS = D == 64 ? 4 : (FP8 ? 2 : 3);
+  static constexpr int RAWS = FP8 ? (D == 128 ? 2 : 4) : 0;
+  static constexpr int SMEM_BYTES = (KS + VS) * SLOT + RAWS * RAW + Q_BYTES + CTL_BYTES;
+  static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory");
+  static constexpr uint32_t TMEM_COLS = 512;  // S_0, S_1, O_0, O_1
+};
+
+// A request as the kernel takes it: every later index is in bounds by this.
+struct Request {
+  int row0, n, ctx, total, items;  // items: of one KV head
+  __device__ __forceinline__ bool set(const Args &a, int c, int start, int end) {
+    bool ok = true;
+    row0 = min(max(start, 0), a.n_rows);
+    n = min(max(end, row0), a.n_rows) - row0;
+    if (n > a.max_rows) {
+      n = a.max_rows;
+      ok = false;
+    }
+    ctx = max(c, 0);
+    const long long cap = min((long long)a.max_pages << a.page_shift, 0x7fffff00ll);
+    if ((long long)ctx + n > cap) {
+      total = (int)cap;
+      ok = false;
+    } else {
+      total = ctx + n;
+    }
+    items = (int)(((long long)n + 2 * a.nodes_tile - 1) / (2 * a.nodes_tile));
+    return ok || n == 0;
+  }
+  // the cost of a KV head's first x items
+  __device__ __forceinline__ long long upto(const Args &a, int x) const {
+    const long long each = 2 * a.nodes_tile;
+    long long s = x * ((long long)OVERHEAD + ctx) + each * x * (x + 1) / 2;
+    if (x == items) s -= each * x - n;  // the last item's rows
+    return s;
+  }
+  // an item's tokens, in tiles
+  __device__ __forceinline__ int tiles(const Args &a, int item) const {
+    const long long rows = min((long long)n, (long long)(item + 1) * 2 * a.nodes_tile);
+    return (int)((min((long long)total, ctx + rows) + BT - 1) / BT);
+  }
+};
+
+// A place in the list of all work: tile `tile` of item `item` of (request, head).
+struct Place {
+  int r, h, item, tile;
+};
+__device__ __forceinline__ bool same_item(const Place &a, const Place &b) {
+  return a.r == b.r && a.h == b.h && a.item == b.item;
+}
+__device__ __forceinline__ bool before(const Place &a, const Place &b) {
+  if (a.r != b.r) return a.r < b.r;
+  if (a.h != b.h) return a.h < b.h;
+  return a.item != b.item ? a.item < b.item : a.tile < b.tile;
+}
+
+// Where cost `off` of request r's own lies: both CTAs beside a cut find the same place.
+__device__ __forceinline__ Place locate(const Args &a, const Request &q, int r, long long off) {
+  Place p;
+  p.r = r;
+  const long long each = q.upto(a, q.items);
+  p.h = (int)(off / each);
+  off -= p.h * each;
+  int lo = 0, hi = q.items - 1;  // the last item that begins at or before off
+  while (lo < hi) {
+    const int mid = (int)(((long long)lo + hi + 1) >> 1);
+    if (q.upto(a, mid) <= off) lo = mid;
+    else hi = mid - 1;
+  }
+  p.item = lo;
+  const long long in = off - q.upto(a, lo) - OVERHEAD;
+  const int tiles = q.tiles(a, lo);
+  p.tile = in <= 0 ? 0 : (int)min((in + BT / 2) / BT, (long long)tiles);
+  if (p.tile < MIN_PIECE) p.tile = 0;
+  if (p.tile && tiles - p.tile < MIN_PIECE) {  // the next item's beginning
+    p.tile = 0;
+    if (++p.item == q.items) {
+      p.item = 0;
+      if (++p.h == a.heads) {
+        p.h = 0;
+        ++p.r;
+      }
+    }
+  }
+  return p;
+}
+
+// One CTA's consecutive tiles [tb, te) of one item; none: the end of its share.
+struct Segment {
+  int r, row0, ctx, total, h, node0, nodes, tb, te, tiles;
+  int count[2];     // of these tiles, those that each tile of Q meets
+  float c;          // log2(e) * scale (* the head's K scale)
+  unsigned odd[8];  // the item's nodes with non-finite V
+};
+
+struct Ctl {
+  uint64_t k_full[MAX_SLOTS], k_empty[MAX_SLOTS], v_full[MAX_SLOTS], v_empty[MAX_SLOTS];
+  uint64_t v_ready[MAX_SLOTS];          // and nothing in V that must not be met
+  uint64_t r_full[MAX_SLOTS], r_empty[MAX_SLOTS];
+  // by tile of Q: copied; its last S issued; S, P and the item's O complete
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t seg_full[SEGS], seg_empty[SEGS];
+  long long sums[16];
+  Place first, last;
+  alignas(16) Segment seg[SEGS];
+  int tail[5], head;
+  int abort;
+  uint32_t tmem;
+};
+static_assert(sizeof(Ctl) <= CTL_BYTES, "control block");
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mov.b64 c, {%6, %7};\n fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// D += A . B with A in tensor memory (bf16, two values in a column), by a warp in step.
+__device__ __forceinline__ void umma_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Registers into 32 lanes x 8 columns.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
+// Four 8-bit floats as four bf16 (exact): sign, exponent and mantissa moved to bf16's
+// places, times 2^120 for the exponents' offsets, which subnormals need too; the code of
+// NaN is put in by hand.
+__device__ __forceinline__ uint2 widen_e4m3x4(uint32_t x) {
+  uint32_t o[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t two = __byte_perm(x, 0, i ? 0x3424 : 0x1404);  // each in a half's upper byte
+    const uint32_t bits = (two & 0x80008000u) | ((two >> 4) & 0x07f007f0u);
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(bits), "r"(0x7b807b80u));  // 2^120
+  }
+  if (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if ((x >> (8 * i) & 0x7f) == 0x7f) o[i / 2] |= 0x7fffu << (16 * (i & 1));
+  }
+  return make_uint2(o[0], o[1]);
+}
+
+template <int TYPE, int D>
+__global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
+    chunk_attention_kernel(const __grid_constant__ CUtensorMap tma_k,
+                           const __grid_constant__ CUtensorMap tma_v,
+                           const __grid_constant__ CUtensorMap tma_q,
+                           const __grid_constant__ Args a) {
+  using G = Geo<TYPE, D>;
+  constexpr int HALVES = D / 64;        // 64-column halves of a head
+  constexpr int HALF_BYTES = BT * 128;  // one half of a tile
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t *const sk = smem, *const sv = sk + G::KS * G::SLOT;
+  uint8_t *const sq = sv + G::VS * G::SLOT, *const raws = sq + G::Q_BYTES;
+  Ctl *ctl = reinterpret_cast<Ctl *>(raws + G::RAWS * G::RAW);
+  volatile int *abort = &ctl->abort;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int cta = blockIdx.x;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < MAX_SLOTS; ++s) {
+      tc::mbar_init(&ctl->k_full[s], G::FP8 ? G::CV : 1);
+      tc::mbar_init(&ctl->v_full[s], G::FP8 ? G::CV : 1);
+      tc::mbar_init(&ctl->k_empty[s], 2);  // each tile of Q is done with it
+      tc::mbar_init(&ctl->v_empty[s], 2);
+      tc::mbar_init(&ctl->v_ready[s], 1);
+      tc::mbar_init(&ctl->r_full[s], 1);
+      tc::mbar_init(&ctl->r_empty[s], 4);
+    }
+    for (int x = 0; x < 2; ++x) {
+      tc::mbar_init(&ctl->q_full[x], 1);
+      tc::mbar_init(&ctl->q_empty[x], 1);
+      tc::mbar_init(&ctl->s_full[x], 1);
+      tc::mbar_init(&ctl->p_full[x], 4);
+      tc::mbar_init(&ctl->o_full[x], 1);
+    }
+    tc::mbar_init(&ctl->drain, 1);
+    for (int i = 0; i < SEGS; ++i) {
+      tc::mbar_init(&ctl->seg_full[i], 1);
+      // both streams of the issuer, the copies of Q, the warp at V, the softmax's groups,
+      // those that widen
+      tc::mbar_init(&ctl->seg_empty[i], 6 + (G::FP8 ? 1 : 0));
+    }
+    for (int i = 0; i < 5; ++i) ctl->tail[i] = 0;
+    ctl->head = 0;
+    ctl->abort = 0;
+    tc::fence_barrier_init();
+    tc::tma_prefetch_desc(&tma_k);
+    tc::tma_prefetch_desc(&tma_v);
+    tc::tma_prefetch_desc(&tma_q);
+  }
+  if (warp == 1) tc::tmem_alloc(&ctl->tmem, G::TMEM_COLS);
+  pdl_trigger();
+  pdl_wait();
+
+  // the list's cost, and where this CTA's share of it begins and ends
+  {
+    const int per = (a.R + G::THREADS - 1) / G::THREADS;
+    const int r_lo = min((int)threadIdx.x * per, a.R), r_hi = min(r_lo + per, a.R);
+    long long mine = 0;
+    Request q;
+    for (int r = r_lo; r < r_hi; ++r) {
+      if (!q.set(a, a.ctx[r], a.row_start[r], a.row_start[r + 1]) && cta == 0)
+        dspark_set_status(DSPARK_ERR_LENGTH);
+      mine += q.upto(a, q.items) * a.heads;
+    }
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += t;
+    }
+    if (lane == 31) ctl->sums[warp] = upto;
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    long long all = 0, below = upto - mine;
+    for (int w = 0; w < G::THREADS / 32; ++w) {
+      all += ctl->sums[w];
+      if (w < warp) below += ctl->sums[w];
+    }
+    const int shares = (int)max(1ll, min((long long)gridDim.x, all / MIN_SHARE));
+    const long long share = all / shares, longer = all - share * shares;
+    if (threadIdx.x == 0) {
+      const Place end = {a.R, 0, 0, 0};
+      ctl->first = ctl->last = end;
+    }
+    __syncthreads();
+    // the thread whose requests a cut lies in finds its place; the last cut is the end
+    for (int side = 0; side < 2; ++side) {
+      const int cut = cta + side;
+      if (cut >= shares) break;
+      const long long u = cut * share + min((long long)cut, longer);
+      if (mine > 0 && below <= u && u < below + mine) {
+        long long off = u - below;
+        int r = r_lo;
+        for (;; ++r) {
+          q.set(a, a.ctx[r], a.row_start[r], a.row_start[r + 1]);
+          const long long m = q.upto(a, q.items) * a.heads;
+          if (off < m) break;
+          off -= m;
+        }
+        (side ? ctl->last : ctl->first) = locate(a, q, r, off);
+      }
+    }
+    __syncthreads();
+  }
+  const uint32_t tmem = ctl->tmem, tmem_o = tmem + 2 * BT;
+
+  if (warp < 4) fewer_registers<G::REGS_FEW>();
+  if (warp == 0) {
+    // -------------------------------------------------- copies of K and V ----
+    const uint64_t pol = tc::policy_evict_normal();
+    const int rows = min(1 << a.page_shift, BT), boxes = BT / rows;
+    const uint32_t box_bytes = (uint32_t)(rows * D * (G::FP8 ? 1 : 2));
+    int at[2] = {0, 0};          // the place of the next copy of K, of V (8 bits: both at [0])
+    uint32_t phase[2] = {0, 0};
+    uint32_t fills = 0;
+    bool ok = true;
+    Place p = ctl->first;
+    const Place last = ctl->last;
+    Request q;
+    int known = -1;
+    for (int published = 0; ok; ++published) {
+      while (before(p, last) && known != p.r) {
+        q.set(a, a.ctx[p.r], a.row_start[p.r], a.row_start[p.r + 1]);
+        known = p.r;
+        if (q.n == 0) p = {p.r + 1, 0, 0, 0};
+      }
+      Segment s;
+      s.tb = s.te = 0;
+      const bool none = !before(p, last);
+      if (!none) {
+        s.r = p.r;
+        s.row0 = q.row0;
+        s.ctx = q.ctx;
+        s.total = q.total;
+        s.h = p.h;
+        s.node0 = p.item * 2 * a.nodes_tile;
+        s.nodes = min(2 * a.nodes_tile, q.n - s.node0);
+        s.tiles = q.tiles(a, p.item);
+        s.tb = p.tile;
+        s.te = same_item(p, last) ? last.tile : s.tiles;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int rows_x = min(s.nodes - x * a.nodes_tile, a.nodes_tile);
+          const long long sees = min((long long)q.total,
+                                     (long long)q.ctx + s.node0 + x * a.nodes_tile + rows_x);
+          const int tiles_x = rows_x > 0 ? (int)((sees + BT - 1) / BT) : 0;
+          s.count[x] = max(0, min(s.te, tiles_x) - s.tb);
+        }
+        s.c = a.scale * LOG2E * (a.k_scale ? a.k_scale[p.h] : 1.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s.odd[i] = 0;
+        p.tile = 0;
+        if (++p.item == q.items) {
+          p.item = 0;
+          if (++p.h == a.heads) p = {p.r + 1, 0, 0, 0};
+        }
+      }
+      const int i = published % SEGS;
+      ok = warp_wait(&ctl->seg_empty[i], ((published / SEGS) & 1) ^ 1, abort);
+      if (ok && lane == 0) {
+        ctl->seg[i] = s;
+        tc::mbar_arrive(&ctl->seg_full[i]);
+      }
+      __syncwarp();
+      if (none) break;
+      for (int tile = s.tb; ok && tile < s.te; ++tile) {
+        const long long t0 = (long long)tile * BT + lane * rows;
+        const bool mine = lane < boxes && t0 < s.total;
+        const int id = mine ? a.block_table[(size_t)s.r * a.max_pages + (t0 >> a.page_shift)] : 0;
+        const int n_boxes = __popc(__ballot_sync(0xffffffffu, mine));
+        const bool in = id >= 0 && id < a.n_pages;
+        if (mine && !in) dspark_set_status(DSPARK_ERR_PAGES);
+        const int z = in ? id : -1;  // outside the map: zeros
+        const int y = (int)(t0 & ((1 << a.page_shift) - 1));
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          const int w = G::FP8 ? 0 : kv, ring = G::FP8 ? G::RAWS : (kv ? G::VS : G::KS);
+          uint64_t *empty = G::FP8 ? ctl->r_empty : (kv ? ctl->v_empty : ctl->k_empty);
+          uint64_t *full = G::FP8 ? ctl->r_full : (kv ? ctl->v_full : ctl->k_full);
+          const int place = w ? at[1] : at[0];
+          const uint32_t turn = w ? phase[1] : phase[0];
+          if (!warp_wait(&empty[place], turn ^ 1, abort)) {
+            ok = false;
+            break;
+          }
+          uint64_t *bar = &full[place];
+          if (lane == 0) tc::mbar_expect_tx(bar, n_boxes * box_bytes);
+          __syncwarp();
+          if (mine) {
+            const CUtensorMap *map = kv ? &tma_v : &tma_k;
+            if constexpr (G::FP8) {
+              tc::tma_load_4d(raws + place * G::RAW + lane * rows * D, map, 0, y, s.h, z, bar, pol);
+            } else {
+              uint8_t *dst = (kv ? sv : sk) + place * G::SLOT + lane * rows * 128;
+#pragma unroll
+              for (int c = 0; c < HALVES; ++c)
+                tc::tma_load_4d(dst + c * HALF_BYTES, map, c * 64, y, s.h, z, bar, pol);
+            }
+          }
+          ++fills;
+          const int next = place + 1 == ring ? 0 : place + 1;
+          if (w) {
+            at[1] = next;
+            phase[1] ^= next == 0;
+          } else {
+            at[0] = next;
+            phase[0] ^= next == 0;
+          }
+        }
+      }
+    }
+    // drain: every copy issued has landed
+    volatile int never = 0;
+    if constexpr (G::FP8) {
+      for (int i = 0; i < G::RAWS; ++i)
+        if ((uint32_t)i < fills) warp_wait(&ctl->r_full[i], i < at[0] ? phase[0] : phase[0] ^ 1, &never);
+    } else {
+      for (int i = 0; i < G::KS; ++i)
+        if ((uint32_t)i < (fills + 1) / 2)
+          warp_wait(&ctl->k_full[i], i < at[0] ? phase[0] : phase[0] ^ 1, &never);
+      for (int i = 0; i < G::VS; ++i)
+        if ((uint32_t)i < fills / 2)
+          warp_wait(&ctl->v_full[i], i < at[1] ? phase[1] : phase[1] ^ 1, &never);
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------------- MMA issuer ----
+    // Each tile of Q is a stream of products S, O, S, O, ..; a stream's next S follows
+    // its last O at once, as P's place is S's.  The streams take turns as their operands
+    // come, so that neither waits behind the other.
+    constexpr uint32_t idesc_s = tc::idesc_bf16(BM, BT);
+    constexpr uint32_t idesc_o = tc::idesc_bf16(BM, D) | tc::IDESC_B_MN;
+    struct Stream {
+      uint32_t seg, done, items;  // segments begun, O products and last S's issued, all in all
+      int k, count, tiles;        // tiles of the segment taken; that this stream meets; all
+      int k_slot, v_slot;
+      uint32_t k_phase, v_phase;
+      bool s_out, open, over;     // s_out: S is issued, its O is next
+    } st[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) st[x] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, false, false, false};
+    auto ready = [&](uint64_t *bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, tc::mbar_test(bar, parity)) != 0;
+    };
+    auto next_k = [&](Stream &s) {
+      if (++s.k_slot == G::KS) {
+        s.k_slot = 0;
+        s.k_phase ^= 1;
+      }
+    };
+    auto next_v = [&](Stream &s) {
+      if (++s.v_slot == G::VS) {
+        s.v_slot = 0;
+        s.v_phase ^= 1;
+      }
+    };
+    uint32_t idle = 0;
+    uint64_t since = 0;
+    while (!(st[0].over && st[1].over)) {
+      bool did = false;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        Stream &s = st[x];
+        if (s.over) continue;
+        if (!s.open) {
+          const int i = s.seg % SEGS;
+          if (!ready(&ctl->seg_full[i], (s.seg / SEGS) & 1)) continue;
+          s.tiles = ctl->seg[i].te - ctl->seg[i].tb;
+          s.count = ctl->seg[i].count[x];
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&ctl->seg_empty[i]);
+          ++s.seg;
+          s.k = 0;
+          s.s_out = false;
+          did = true;
+          if (s.tiles == 0) {
+            s.over = true;
+            continue;
+          }
+          s.open = true;
+        }
+        if (s.s_out) {
+          // O of tile k
+          if (!ready(&ctl->p_full[x], s.done & 1) || !ready(&ctl->v_ready[s.v_slot], s.v_phase))
+            continue;
+          did = true;
+          tc::fence_after_sync();
+          const uint64_t vd =
+              tc::smem_desc_sw128_mn(sv + s.v_slot * G::SLOT, D == 128 ? HALF_BYTES : 0);
+#pragma unroll
+          for (int k = 0; k < BT / 16; ++k)
+            umma_ts_warp(tmem_o + x * D, tmem + x * BT + 8 * k, vd + 128 * k, idesc_o,
+                         s.k > 0 || k != 0);
+          tc::umma_commit_warp(&ctl->v_empty[s.v_slot]);
+          if (s.k + 1 == s.count) tc::umma_commit_warp(&ctl->o_full[x]);
+          next_v(s);
+          ++s.done;
+          ++s.k;
+          s.s_out = false;
+        }
+        if (s.k < s.count) {
+          // S of tile k
+          if (!ready(&ctl->k_full[s.k_slot], s.k_phase) ||
+              (s.k == 0 && !ready(&ctl->q_full[x], s.items & 1)))
+            continue;
+          did = true;
+          tc::fence_after_sync();
+          const uint64_t kd = tc::smem_desc_sw128(sk + s.k_slot * G::SLOT);
+          const uint64_t qd = tc::smem_desc_sw128(sq + x * G::Q_ONE);
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc::umma_warp(tmem + x * BT, qd + h * (BM * 128 / 16) + 2 * k,
+                            kd + h * (HALF_BYTES / 16) + 2 * k, idesc_s, (h | k) != 0);
+          tc::umma_commit_warp(&ctl->s_full[x]);
+          tc::umma_commit_warp(&ctl->k_empty[s.k_slot]);
+          if (s.k + 1 == s.count) {
+            tc::umma_commit_warp(&ctl->q_empty[x]);
+            ++s.items;
+          }
+          next_k(s);
+          s.s_out = true;
+        } else if (s.k < s.tiles) {
+          // a tile that no row of this stream sees: given back once it is there
+          if (!ready(&ctl->k_full[s.k_slot], s.k_phase) ||
+              !ready(&ctl->v_ready[s.v_slot], s.v_phase))
+            continue;
+          did = true;
+          if (lane == 0) {
+            tc::mbar_arrive(&ctl->k_empty[s.k_slot]);
+            tc::mbar_arrive(&ctl->v_empty[s.v_slot]);
+          }
+          __syncwarp();
+          next_k(s);
+          next_v(s);
+          ++s.k;
+        }
+        if (s.k == s.tiles) s.open = false;
+      }
+      if (did) {
+        idle = 0;
+        since = 0;
+      } else if ((++idle & 63) == 0) {
+        const uint64_t now = tc::globaltimer();
+        if (since == 0) since = now;
+        if (__any_sync(0xffffffffu, *abort != 0)) break;
+        if (now - since > tc::WAIT_LIMIT_NS) *abort = 1;
+      }
+    }
+    tc::umma_commit_warp(&ctl->drain);  // all MMAs issued have finished
+    volatile int never = 0;
+    warp_wait(&ctl->drain, 0, &never);
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------ copies of Q ----
+    uint32_t uses[2] = {0, 0};
+    bool ok = true;
+    for (uint32_t i = 0; ok; ++i) {
+      ok = warp_wait(&ctl->seg_full[i % SEGS], (i / SEGS) & 1, abort);
+      if (!ok) break;
+      const Segment *n = &ctl->seg[i % SEGS];
+      if (n->tb == n->te) break;
+      const int head = n->h * a.group, row = n->row0 + n->node0;
+      const int count[2] = {n->count[0], n->count[1]};
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&ctl->seg_empty[i % SEGS]);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (count[x] == 0 || !ok) continue;
+        ok = warp_wait(&ctl->q_empty[x], (uses[x] & 1) ^ 1, abort);
+        if (!ok) continue;
+        if (lane == 0) {
+          tc::mbar_expect_tx(&ctl->q_full[x], HALVES * a.nodes_tile * a.group * 128);
+          for (int c = 0; c < HALVES; ++c)
+            tc::tma_load_3d(sq + x * G::Q_ONE + c * BM * 128, &tma_q, c * 64, head,
+                            row + x * a.nodes_tile, &ctl->q_full[x], tc::policy_evict_normal());
+        }
+        __syncwarp();
+        ++uses[x];
+      }
+    }
+    volatile int never = 0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)  // drain
+      if (uses[x]) warp_wait(&ctl->q_full[x], (uses[x] - 1) & 1, &never);
+  } else if (warp == 3) {
+    // ------------------------------------------------- V's last tiles ----
+    // A weight of zero must not meet an infinity or NaN of a token that its row does not
+    // see.  Rows of V past the item's last token are cleared; the non-finite values of
+    // the tokens after its first row's are too, and the epilogue gives them to the rows
+    // that do see them.
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (uint32_t i = 0; ok; ++i) {
+      ok = warp_wait(&ctl->seg_full[i % SEGS], (i / SEGS) & 1, abort);
+      if (!ok) break;
+      Segment *n = &ctl->seg[i % SEGS];
+      const int tb = n->tb, te = n->te;
+      if (tb == te) break;
+      const long long first = (long long)n->ctx + n->node0;  // the first row's own token
+      const long long end = min((long long)n->total, first + n->nodes);
+      for (int tile = tb; ok && tile < te; ++tile) {
+        ok = warp_wait(&ctl->v_full[slot], phase, abort);
+        if (ok && (long long)tile * BT + BT > first + 1) {
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            const int token = q * 32 + lane;
+            const long long pos = (long long)tile * BT + token;
+            uint8_t *row = sv + slot * G::SLOT + token * 128;
+            if (pos >= end) {
+#pragma unroll
+              for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                  *reinterpret_cast<uint4 *>(row + h * HALF_BYTES + ((c ^ (token & 7)) * 16)) =
+                      make_uint4(0, 0, 0, 0);
+            } else if (pos > first) {
+              // the sign bit of a half of odd: its exponent is all ones
+              uint32_t odd = 0;
+#pragma unroll
+              for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  const uint4 y = *reinterpret_cast<const uint4 *>(row + h * HALF_BYTES +
+                                                                   ((c ^ (token & 7)) * 16));
+                  odd |= ((y.x & 0x7f807f80u) + 0x00800080u) | ((y.y & 0x7f807f80u) + 0x00800080u) |
+                         ((y.z & 0x7f807f80u) + 0x00800080u) | ((y.w & 0x7f807f80u) + 0x00800080u);
+                }
+              if (odd & 0x80008000u) {
+                const int node = (int)(pos - first);
+                atomicOr(&n->odd[node >> 5], 1u << (node & 31));
+#pragma unroll 1
+                for (int w = 0; w < HALVES * 32; ++w) {
+                  uint32_t *at = reinterpret_cast<uint32_t *>(row + (w / 32) * HALF_BYTES) + w % 32;
+                  if ((*at & 0x7f80u) == 0x7f80u) *at &= 0xffff0000u;
+                  if ((*at & 0x7f800000u) == 0x7f800000u) *at &= 0xffffu;
+                }
+              }
+            }
+          }
+          tc::fence_async_smem();
+          __threadfence_block();
+        }
+        __syncwarp();
+        if (ok && lane == 0) tc::mbar_arrive(&ctl->v_ready[slot]);
+        if (++slot == G::VS) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
+      if (lane == 0) tc::mbar_arrive(&ctl->seg_empty[i % SEGS]);
+    }
+  } else if (warp < 12) {
+    more_registers<G::REGS_SOFTMAX>();
+    // ----------------------------------------------------------- softmax ----
+    const int x = (warp - 4) >> 2, quarter = warp & 3, m = quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t ts = tmem + lanes + x * BT, to = tmem_o + lanes + x * D;
+    const int my_node = m / a.group, g = m - my_node * a.group;
+    uint32_t tiles_done = 0, items_done = 0;
+    bool ok = true;
+    for (uint32_t seg = 0; ok; ++seg) {
+      ok = warp_wait(&ctl->seg_full[seg % SEGS], (seg / SEGS) & 1, abort);
+      if (!ok) break;
+      const Segment *const n = &ctl->seg[seg % SEGS];
+      const int tb = n->tb, count = n->count[x];
+      if (tb == n->te) break;
+      const float c = n->c;
+      const int node = n->node0 + x * a.nodes_tile + my_node;  // of the request
+      const bool mine = my_node < a.nodes_tile && x * a.nodes_tile + my_node < n->nodes;
+      // tokens that this row sees, and that the tile's first row does
+      const int sees = (int)min((long long)n->total, (long long)n->ctx + node + 1);
+      const int all_see =
+          (int)min((long long)n->total, (long long)n->ctx + n->node0 + x * a.nodes_tile + 1);
+      float nm = 0.0f;  // minus the reference (log2)
+      bool unset = true;
+      float2 l0 = {0.0f, 0.0f}, l1 = {0.0f, 0.0f};
+      for (int k = 0; k < count; ++k, ++tiles_done) {
+        ok = warp_wait(&ctl->s_full[x], tiles_done & 1, abort);
+        if (!ok) break;
+        tc::fence_after_sync();
+        float2 e[64];
+        {
+          uint32_t s[4][32];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tc::tmem_ld32(ts + 32 * j, s[j]);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tc::reg_fence(s[j]);
+#pragma unroll
+          for (int j = 0; j < 64; ++j)
+            e[j] = fma2(make_float2(__uint_as_float(s[j / 16][2 * j % 32]),
+                                    __uint_as_float(s[j / 16][2 * j % 32 + 1])),
+                        make_float2(c, c), make_float2(nm, nm));
+        }
+        const int t0 = (tb + k) * BT;
+        if (t0 + BT > all_see) {
+          const int lim = sees - t0;
+#pragma unroll
+          for (int j = 0; j < 64; ++j) {
+            e[j].x = 2 * j < lim ? e[j].x : -INFINITY;
+            e[j].y = 2 * j + 1 < lim ? e[j].y : -INFINITY;
+          }
+        }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < 64; ++j) top[j & 3] = max3(top[j & 3], e[j].x, e[j].y);
+        const float most = max3(fmaxf(top[0], top[1]), top[2], top[3]);
+        if (__any_sync(0xffffffffu, unset || most > RAISE)) {
+          const bool fresh = unset, number = fabsf(most) < INFINITY;
+          const float raise = number && (fresh || most > RAISE) ? most : 0.0f;
+          if (number) unset = false;
+          const float keep = fresh ? 1.0f : ex2_fast(-raise);
+          if (k > 0 && __any_sync(0xffffffffu, keep != 1.0f)) {
+            // O of the tiles so far is complete: its product came before this S
+            l0.x *= keep;
+            l0.y *= keep;
+            l1.x *= keep;
+            l1.y *= keep;
+#pragma unroll 1
+            for (int d = 0; d < D; d += 16) {
+              uint32_t o[16];
+              tc::tmem_ld16(to + d, o);
+              tc::tmem_wait_ld();
+              tc::reg_fence(o);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
+              tc::tmem_st16(to + d, o);
+            }
+          }
+          nm -= raise;
+#pragma unroll
+          for (int j = 0; j < 64; ++j) e[j] = add2(e[j], make_float2(-raise, -raise));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint32_t pk[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 v = make_float2(ex2_fast(e[8 * j + i].x), ex2_fast(e[8 * j + i].y));
+            if (i & 1) l1 = add2(l1, v);
+            else l0 = add2(l0, v);
+            pk[i] = pack_bf16(v.x, v.y);
+          }
+          tmem_st8(ts + 8 * j, pk);  // two weights a column
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ctl->p_full[x]);
+      }
+      if (!ok) break;
+
+      // ---------------------------------------------------- end of an item ----
+      const bool whole = tb == 0 && n->te == n->tiles;
+      const int piece = tb == 0 ? 1 : 0;
+      const float sum = (l0.x + l0.y) + (l1.x + l1.y);
+      const size_t slot = (size_t)cta * 2 + piece;
+      if (!whole) {
+        float *ml = a.part_ml + slot * 4 * BM + x * BM + m;
+        ml[0] = unset && sum == 0.0f ? -INFINITY : -nm;
+        ml[2 * BM] = sum;
+        if (x == 0 && m == 0) {
+          if (piece) {
+            ctl->tail[0] = 1;
+            ctl->tail[1] = n->row0;
+            ctl->tail[2] = n->node0;
+            ctl->tail[3] = n->nodes;
+            ctl->tail[4] = n->h;
+          } else {
+            ctl->head = n->te == n->tiles ? 2 : 1;
+          }
+        }
+      }
+      if (count > 0) {
+        ok = warp_wait(&ctl->o_full[x], items_done & 1, abort);
+        if (!ok) break;
+        ++items_done;
+        tc::fence_after_sync();
+        const float vs = a.v_scale ? a.v_scale[n->h] : 1.0f;
+        const float f = whole ? __fdividef(vs, sum) : 1.0f;
+        const int64_t row = (int64_t)n->row0 + node;
+        const int head = n->h * a.group + g;
+        if (whole && mine && a.lse)
+          a.lse[row * a.heads * a.group + head] = (log2f(sum) - nm) * LN2;
+        bf16 *const dst = a.out + row * a.out_row + head * a.out_head;
+        unsigned any = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) any |= n->odd[i];
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
+          uint32_t o[32];
+          tc::tmem_ld32(to + d, o);
+          tc::tmem_wait_ld();
+          tc::reg_fence(o);
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * f;
+          if (any) {
+#pragma unroll 1
+            for (int at = 1; at <= node - n->node0 && at < n->nodes; ++at) {
+              if (!(n->odd[at >> 5] >> (at & 31) & 1)) continue;
+              const long long pos = (long long)n->ctx + n->node0 + at;
+              const int page = a.block_table[(size_t)n->r * a.max_pages + (pos >> a.page_shift)];
+              if (page < 0 || page >= a.n_pages) continue;
+              const uint8_t *src = a.v + page * a.page_bytes +
+                                   (pos & ((1 << a.page_shift) - 1)) * a.token_bytes +
+                                   n->h * a.head_bytes;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                float y;
+                if constexpr (G::FP8)
+                  y = (src[d + j] & 0x7f) == 0x7f ? NAN : 0.0f;
+                else
+                  y = __bfloat162float(reinterpret_cast<const bf16 *>(src)[d + j]);
+                if (!(fabsf(y) < INFINITY)) v[j] += y;
+              }
+            }
+          }
+          if (!mine) continue;
+          if (whole) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8)
+              *reinterpret_cast<uint4 *>(dst + d + j) =
+                  make_uint4(pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]),
+                             pack_bf16(v[j + 4], v[j + 5]), pack_bf16(v[j + 6], v[j + 7]));
+          } else {
+            float4 *po = a.part_o + (slot * (D / 4) + d / 4) * 2 * BM + x * BM + m;
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              po[(j / 4) * 2 * BM] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+          }
+        }
+        tc::fence_before_sync();
+      }
+      // the group has read the segment
+      asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + x) : "memory");
+      if (m == 0) tc::mbar_arrive(&ctl->seg_empty[seg % SEGS]);
+    }
+    __syncwarp();
+  } else {
+    if constexpr (G::FP8) {
+      fewer_registers<G::REGS_WIDEN>();
+      // --------------------------------------------- 8-bit tiles made bf16 ----
+      const int w = warp - 12, token = w * 32 + lane;
+      int k_slot = 0, v_slot = 0, raw = 0;
+      uint32_t k_phase = 0, v_phase = 0, raw_phase = 0;
+      bool ok = true;
+      for (uint32_t seg = 0; ok; ++seg) {
+        ok = warp_wait(&ctl->seg_full[seg % SEGS], (seg / SEGS) & 1, abort);
+        if (!ok) break;
+        const int tiles = ctl->seg[seg % SEGS].te - ctl->seg[seg % SEGS].tb;
+        if (tiles == 0) break;
+#pragma unroll 1
+        for (int fill = 0; fill < 2 * tiles; ++fill) {
+          const bool is_v = fill & 1;
+          const int at = is_v ? v_slot : k_slot;
+          ok = warp_wait(&ctl->r_full[raw], raw_phase, abort) &&
+               warp_wait(is_v ? &ctl->v_empty[at] : &ctl->k_empty[at],
+                         (is_v ? v_phase : k_phase) ^ 1, abort);
+          if (!ok) break;
+          const uint8_t *src = raws + raw * G::RAW;
+          uint8_t *dst = (is_v ? sv : sk) + at * G::SLOT;
+          // eight lanes take eight tokens: the swizzles spread both sides over all banks
+          const int raw_x = D == 128 ? token & 7 : (token >> 1) & 3;
+#pragma unroll
+          for (int p = 0; p < D / 16; ++p) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(src + token * D + ((p ^ raw_x) * 16));
+            const uint2 o0 = widen_e4m3x4(v.x), o1 = widen_e4m3x4(v.y), o2 = widen_e4m3x4(v.z),
+                        o3 = widen_e4m3x4(v.w);
+            uint8_t *row = dst + (p / 4) * HALF_BYTES + token * 128;
+            const int cc = (2 * p) % 8;
+            *reinterpret_cast<uint4 *>(row + ((cc ^ (token & 7)) * 16)) =
+                make_uint4(o0.x, o0.y, o1.x, o1.y);
+            *reinterpret_cast<uint4 *>(row + (((cc + 1) ^ (token & 7)) * 16)) =
+                make_uint4(o2.x, o2.y, o3.x, o3.y);
+          }
+          tc::fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tc::mbar_arrive(is_v ? &ctl->v_full[at] : &ctl->k_full[at]);
+            tc::mbar_arrive(&ctl->r_empty[raw]);
+          }
+          if (++raw == G::RAWS) {
+            raw = 0;
+            raw_phase ^= 1;
+          }
+          if (is_v) {
+            if (++v_slot == G::VS) {
+              v_slot = 0;
+              v_phase ^= 1;
+            }
+          } else if (++k_slot == G::KS) {
+            k_slot = 0;
+            k_phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        asm volatile("barrier.cta.sync 3, 128;" ::: "memory");
+        if (w == 0 && lane == 0) tc::mbar_arrive(&ctl->seg_empty[seg % SEGS]);
+      }
+    }
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    if (ctl->abort) dspark_set_status(DSPARK_ERR_TIMEOUT);
+    int *desc = a.desc + cta * 8;
+    for (int i = 0; i < 5; ++i) desc[i] = ctl->tail[i];
+    desc[5] = ctl->head;
+  }
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, G::TMEM_COLS);
+  }
+}
+
+// The cut items: block (c, x, y) joins 32 columns of tile x of the item that CTA c began
+// and could not finish, a thread taking one row, its own pieces in order:
+//   out = sum_k e^{m_k - m} O_k / sum_k e^{m_k - m} l_k,  m the largest m_k.
+template <int D>
+__global__ void __launch_bounds__(BM) chunk_attention_join(const __grid_constant__ Args a) {
+  pdl_trigger();
+  pdl_wait();
+  const int c = blockIdx.x, x = blockIdx.y, d0 = blockIdx.z * 32, m = threadIdx.x;
+  const int *desc = a.desc + c * 8;
+  if (desc[0] == 0) return;
+  const int node = m / a.group, g = m - node * a.group, ctas = gridDim.x;
+  const int in_item = x * a.nodes_tile + node;
+  if (node >= a.nodes_tile || in_item >= desc[3]) return;
+  // piece 0 is CTA c's last one, piece k > 0 CTA (c + k)'s first
+  int pieces = 1;
+  while (c + pieces < ctas) {
+    const int head = a.desc[(c + pieces) * 8 + 5];
+    if (head == 0) break;
+    ++pieces;
+    if (head == 2) break;
+  }
+  auto at = [&](int k) -> size_t { return k ? 2 * (size_t)(c + k) : 2 * (size_t)c + 1; };
+  float top = -INFINITY;
+  for (int k = 0; k < pieces; ++k) top = fmaxf(top, a.part_ml[at(k) * 4 * BM + x * BM + m]);
+  float sum = 0.0f, o[32] = {};
+  for (int k = 0; k < pieces; ++k) {
+    const float *ml = a.part_ml + at(k) * 4 * BM + x * BM + m;
+    if (ml[0] == -INFINITY) continue;  // the row saw nothing there
+    const float w = ex2_fast(ml[0] - top);
+    sum = fmaf(w, ml[2 * BM], sum);
+    const float4 *src = a.part_o + (at(k) * (D / 4) + d0 / 4) * 2 * BM + x * BM + m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 v = src[i * 2 * BM];
+      o[4 * i] = fmaf(w, v.x, o[4 * i]);
+      o[4 * i + 1] = fmaf(w, v.y, o[4 * i + 1]);
+      o[4 * i + 2] = fmaf(w, v.z, o[4 * i + 2]);
+      o[4 * i + 3] = fmaf(w, v.w, o[4 * i + 3]);
+    }
+  }
+  const int h = desc[4], head = h * a.group + g;
+  const int64_t row = (int64_t)desc[1] + desc[2] + in_item;
+  const float f = __fdividef(a.v_scale ? a.v_scale[h] : 1.0f, sum);
+  bf16 *dst = a.out + row * a.out_row + head * a.out_head + d0;
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    *reinterpret_cast<uint4 *>(dst + i) =
+        make_uint4(pack_bf16(o[i] * f, o[i + 1] * f), pack_bf16(o[i + 2] * f, o[i + 3] * f),
+                   pack_bf16(o[i + 4] * f, o[i + 5] * f), pack_bf16(o[i + 6] * f, o[i + 7] * f));
+  if (a.lse && d0 == 0) a.lse[row * a.heads * a.group + head] = (top + log2f(sum)) * LN2;
+}
+
+}  // namespace chunk
