@@ -555,10 +555,11 @@ size_t dspark_chunk_attention_workspace_bytes(const dspark_kv_cache *cache, int3
  *   max_rows  the most rows of a request, >= 1: rows past it are not computed (status
  *             DSPARK_ERR_LENGTH)
  *   out       16-byte aligned, its strides multiples of 8 below 2^39
- * Scores, statistics and sums in f32.  A weight meets V as one bf16 (8 bits; the sum of
- * the weights takes it unrounded), beside an 8-bit cache too, and K, V and q enter their
- * products unrounded.  Where no request has more than DSPARK_MAX_NODES rows the call
- * may be dspark_tree_attention's, with that call's precision. */
+ * Scores, statistics and sums in f32.  Beside a bf16 cache a weight meets V as one bf16
+ * (8 bits; the sum of the weights takes it unrounded); beside an 8-bit one weights and q
+ * are f16 as in dspark_tree_attention, with a power of two for every row and head of q.
+ * Where no request has more than DSPARK_MAX_NODES rows the call may be
+ * dspark_tree_attention's, with that call's precision. */
 int dspark_chunk_attention(const dspark_kv_cache *cache, int32_t R, int32_t heads_q,
                            int32_t max_rows, int32_t n_rows, int32_t max_pages, const void *q,
                            int64_t q_row_stride, int64_t q_head_stride, const int32_t *ctx,

@@ -24,8 +24,13 @@
 //
 // One CTA per SM: warp 0 copies K and V (TMA, one copy for a page and 64 columns), warp 1
 // issues the products, warp 2 copies Q, warp 3 clears what no row of the item may meet
-// out of V's last tiles, two groups of four warps do the softmax of a tile each.  Beside
-// an 8-bit cache four more warps widen the tiles to bf16, which holds every e4m3 value.
+// out of V's last tiles, two groups of four warps do the softmax of a tile each.
+//
+// Beside an 8-bit cache four more warps widen the tiles to f16, which holds every e4m3
+// value and takes one conversion for two of them, in the place where they were copied
+// to, so that as many are in flight as beside a bf16 cache.  They meet
+// Q and P in f16: each row of Q is scaled by the power of two that brings its largest
+// value to 2^14, weights are at most 2^14 and count down to 2^-24.
 // Every wait is bounded; on expiry the CTA raises DSPARK_ERR_TIMEOUT, drains its own
 // copies and MMAs, frees TMEM and exits.
 #pragma once
@@ -42,12 +47,16 @@ constexpr int BT = 128;             // tokens of a tile
 constexpr int BM = 128;             // rows of a tile of Q
 constexpr int SMEM_LIMIT = 232448;  // 227 KB
 constexpr int CTL_BYTES = 3072;
-constexpr int MAX_SLOTS = 4;
+constexpr int MAX_SLOTS = 4;        // of K, of V
 constexpr int SEGS = 4;             // segments published ahead
 // What beginning and ending an item costs, in tokens; the least share worth a CTA of its
 // own; and the least piece, in tiles, that an item is cut into.
 constexpr int OVERHEAD = 256, MIN_SHARE = 768, MIN_PIECE = 2;
-constexpr float RAISE = 32.0f;      // log2
+// log2: how far scores may pass the reference, and where a new reference puts the largest.
+template <bool FP8>
+struct Range {
+  static constexpr float RAISE = FP8 ? 14.0f : 32.0f, PEAK = FP8 ? 6.0f : 0.0f;
+};
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 struct Args {
@@ -76,11 +85,14 @@ struct Geo {
   static_assert(REGS_FEW + 2 * REGS_SOFTMAX + (FP8 ? REGS_WIDEN : 0) <=
                     65536 / THREADS / 8 * 8 * (THREADS / 128),
                 "a block's registers");
-  static constexpr int SLOT = BT * D * 2, RAW = FP8 ? BT * D : 0;
+  // A tile's place.  An 8-bit tile of 128 columns is copied to its second half, where the
+  // row of a token then holds the last 64 of them: a thread that has read its row may
+  // write it.  One of 64 columns is copied behind it.
+  static constexpr int SLOT = BT * D * 2, RAW_AT = D == 128 ? SLOT / 2 : SLOT;
+  static constexpr int PLACE = SLOT + (FP8 && D == 64 ? BT * D : 0);
   static constexpr int Q_ONE = BM * D * 2, Q_BYTES = 2 * Q_ONE;
-  static constexpr int KS = D == 64 ? 4 : 2, VS = D == 64 ? 4 : (FP8 ? 2 : 3);
-  static constexpr int RAWS = FP8 ? (D == 128 ? 2 : 4) : 0;
-  static constexpr int SMEM_BYTES = (KS + VS) * SLOT + RAWS * RAW + Q_BYTES + CTL_BYTES;
+  static constexpr int KS = D == 64 ? 4 : 2, VS = D == 64 ? 4 : 3;
+  static constexpr int SMEM_BYTES = (KS + VS) * PLACE + Q_BYTES + CTL_BYTES;
   static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory");
   static constexpr uint32_t TMEM_COLS = 512;  // S_0, S_1, O_0, O_1
 };
@@ -176,9 +188,9 @@ struct Segment {
 struct Ctl {
   uint64_t k_full[MAX_SLOTS], k_empty[MAX_SLOTS], v_full[MAX_SLOTS], v_empty[MAX_SLOTS];
   uint64_t v_ready[MAX_SLOTS];          // and nothing in V that must not be met
-  uint64_t r_full[MAX_SLOTS], r_empty[MAX_SLOTS];
-  // by tile of Q: copied; its last S issued; S, P and the item's O complete
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t kr_full[MAX_SLOTS], vr_full[MAX_SLOTS];  // 8-bit tiles as they were copied
+  // by tile of Q: copied; in f16 (8 bits); its last S issued; S, P and the item's O complete
+  uint64_t q_full[2], q_ready[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
   uint64_t seg_full[SEGS], seg_empty[SEGS];
   long long sums[16];
   Place first, last;
@@ -186,6 +198,8 @@ struct Ctl {
   int tail[5], head;
   int abort;
   uint32_t tmem;
+  // 8 bits: by which power of two each row of Q was multiplied, of every other item's
+  int16_t q_exp[2][2][BM];
 };
 static_assert(sizeof(Ctl) <= CTL_BYTES, "control block");
 
@@ -228,25 +242,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
       : "memory");
 }
 
-// Four 8-bit floats as four bf16 (exact): sign, exponent and mantissa moved to bf16's
-// places, times 2^120 for the exponents' offsets, which subnormals need too; the code of
-// NaN is put in by hand.
-__device__ __forceinline__ uint2 widen_e4m3x4(uint32_t x) {
-  uint32_t o[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t two = __byte_perm(x, 0, i ? 0x3424 : 0x1404);  // each in a half's upper byte
-    const uint32_t bits = (two & 0x80008000u) | ((two >> 4) & 0x07f007f0u);
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(bits), "r"(0x7b807b80u));  // 2^120
-  }
-  if (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if ((x >> (8 * i) & 0x7f) == 0x7f) o[i / 2] |= 0x7fffu << (16 * (i & 1));
-  }
-  return make_uint2(o[0], o[1]);
-}
-
 template <int TYPE, int D>
 __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
     chunk_attention_kernel(const __grid_constant__ CUtensorMap tma_k,
@@ -257,9 +252,9 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
   constexpr int HALVES = D / 64;        // 64-column halves of a head
   constexpr int HALF_BYTES = BT * 128;  // one half of a tile
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t *const sk = smem, *const sv = sk + G::KS * G::SLOT;
-  uint8_t *const sq = sv + G::VS * G::SLOT, *const raws = sq + G::Q_BYTES;
-  Ctl *ctl = reinterpret_cast<Ctl *>(raws + G::RAWS * G::RAW);
+  uint8_t *const sk = smem, *const sv = sk + G::KS * G::PLACE;
+  uint8_t *const sq = sv + G::VS * G::PLACE;
+  Ctl *ctl = reinterpret_cast<Ctl *>(sq + G::Q_BYTES);
   volatile int *abort = &ctl->abort;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
@@ -271,11 +266,12 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
       tc::mbar_init(&ctl->k_empty[s], 2);  // each tile of Q is done with it
       tc::mbar_init(&ctl->v_empty[s], 2);
       tc::mbar_init(&ctl->v_ready[s], 1);
-      tc::mbar_init(&ctl->r_full[s], 1);
-      tc::mbar_init(&ctl->r_empty[s], 4);
+      tc::mbar_init(&ctl->kr_full[s], 1);
+      tc::mbar_init(&ctl->vr_full[s], 1);
     }
     for (int x = 0; x < 2; ++x) {
       tc::mbar_init(&ctl->q_full[x], 1);
+      tc::mbar_init(&ctl->q_ready[x], 4);
       tc::mbar_init(&ctl->q_empty[x], 1);
       tc::mbar_init(&ctl->s_full[x], 1);
       tc::mbar_init(&ctl->p_full[x], 4);
@@ -284,9 +280,9 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
     tc::mbar_init(&ctl->drain, 1);
     for (int i = 0; i < SEGS; ++i) {
       tc::mbar_init(&ctl->seg_full[i], 1);
-      // both streams of the issuer, the copies of Q, the warp at V, the softmax's groups,
+      // both streams of the issuer, the copies of Q, the warp at V, the softmax's warps,
       // those that widen
-      tc::mbar_init(&ctl->seg_empty[i], 6 + (G::FP8 ? 1 : 0));
+      tc::mbar_init(&ctl->seg_empty[i], 12 + G::CV);
     }
     for (int i = 0; i < 5; ++i) ctl->tail[i] = 0;
     ctl->head = 0;
@@ -360,9 +356,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
     const uint64_t pol = tc::policy_evict_normal();
     const int rows = min(1 << a.page_shift, BT), boxes = BT / rows;
     const uint32_t box_bytes = (uint32_t)(rows * D * (G::FP8 ? 1 : 2));
-    int at[2] = {0, 0};          // the place of the next copy of K, of V (8 bits: both at [0])
-    uint32_t phase[2] = {0, 0};
-    uint32_t fills = 0;
+    int k_slot = 0, v_slot = 0;
+    uint32_t k_phase = 0, v_phase = 0, fills = 0;
     bool ok = true;
     Place p = ctl->first;
     const Place last = ctl->last;
@@ -424,61 +419,59 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
         const int y = (int)(t0 & ((1 << a.page_shift) - 1));
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
-          const int w = G::FP8 ? 0 : kv, ring = G::FP8 ? G::RAWS : (kv ? G::VS : G::KS);
-          uint64_t *empty = G::FP8 ? ctl->r_empty : (kv ? ctl->v_empty : ctl->k_empty);
-          uint64_t *full = G::FP8 ? ctl->r_full : (kv ? ctl->v_full : ctl->k_full);
-          const int place = w ? at[1] : at[0];
-          const uint32_t turn = w ? phase[1] : phase[0];
-          if (!warp_wait(&empty[place], turn ^ 1, abort)) {
+          const int place = kv ? v_slot : k_slot;
+          if (!warp_wait(kv ? &ctl->v_empty[place] : &ctl->k_empty[place],
+                         (kv ? v_phase : k_phase) ^ 1, abort)) {
             ok = false;
             break;
           }
-          uint64_t *bar = &full[place];
+          uint64_t *bar = G::FP8 ? (kv ? &ctl->vr_full[place] : &ctl->kr_full[place])
+                                 : (kv ? &ctl->v_full[place] : &ctl->k_full[place]);
           if (lane == 0) tc::mbar_expect_tx(bar, n_boxes * box_bytes);
           __syncwarp();
           if (mine) {
             const CUtensorMap *map = kv ? &tma_v : &tma_k;
+            uint8_t *dst = (kv ? sv : sk) + place * G::PLACE;
             if constexpr (G::FP8) {
-              tc::tma_load_4d(raws + place * G::RAW + lane * rows * D, map, 0, y, s.h, z, bar, pol);
+              tc::tma_load_4d(dst + G::RAW_AT + lane * rows * D, map, 0, y, s.h, z, bar, pol);
             } else {
-              uint8_t *dst = (kv ? sv : sk) + place * G::SLOT + lane * rows * 128;
 #pragma unroll
               for (int c = 0; c < HALVES; ++c)
-                tc::tma_load_4d(dst + c * HALF_BYTES, map, c * 64, y, s.h, z, bar, pol);
+                tc::tma_load_4d(dst + c * HALF_BYTES + lane * rows * 128, map, c * 64, y, s.h, z,
+                                bar, pol);
             }
           }
           ++fills;
-          const int next = place + 1 == ring ? 0 : place + 1;
-          if (w) {
-            at[1] = next;
-            phase[1] ^= next == 0;
-          } else {
-            at[0] = next;
-            phase[0] ^= next == 0;
+          if (kv) {
+            if (++v_slot == G::VS) {
+              v_slot = 0;
+              v_phase ^= 1;
+            }
+          } else if (++k_slot == G::KS) {
+            k_slot = 0;
+            k_phase ^= 1;
           }
         }
       }
     }
     // drain: every copy issued has landed
     volatile int never = 0;
-    if constexpr (G::FP8) {
-      for (int i = 0; i < G::RAWS; ++i)
-        if ((uint32_t)i < fills) warp_wait(&ctl->r_full[i], i < at[0] ? phase[0] : phase[0] ^ 1, &never);
-    } else {
-      for (int i = 0; i < G::KS; ++i)
-        if ((uint32_t)i < (fills + 1) / 2)
-          warp_wait(&ctl->k_full[i], i < at[0] ? phase[0] : phase[0] ^ 1, &never);
-      for (int i = 0; i < G::VS; ++i)
-        if ((uint32_t)i < fills / 2)
-          warp_wait(&ctl->v_full[i], i < at[1] ? phase[1] : phase[1] ^ 1, &never);
-    }
+    for (int i = 0; i < G::KS; ++i)
+      if ((uint32_t)i < (fills + 1) / 2)
+        warp_wait(G::FP8 ? &ctl->kr_full[i] : &ctl->k_full[i], i < k_slot ? k_phase : k_phase ^ 1,
+                  &never);
+    for (int i = 0; i < G::VS; ++i)
+      if ((uint32_t)i < fills / 2)
+        warp_wait(G::FP8 ? &ctl->vr_full[i] : &ctl->v_full[i], i < v_slot ? v_phase : v_phase ^ 1,
+                  &never);
   } else if (warp == 1) {
     // -------------------------------------------------------- MMA issuer ----
     // Each tile of Q is a stream of products S, O, S, O, ..; a stream's next S follows
     // its last O at once, as P's place is S's.  The streams take turns as their operands
     // come, so that neither waits behind the other.
-    constexpr uint32_t idesc_s = tc::idesc_bf16(BM, BT);
-    constexpr uint32_t idesc_o = tc::idesc_bf16(BM, D) | tc::IDESC_B_MN;
+    constexpr uint32_t idesc_s = G::FP8 ? tc::idesc_f16(BM, BT) : tc::idesc_bf16(BM, BT);
+    constexpr uint32_t idesc_o =
+        (G::FP8 ? tc::idesc_f16(BM, D) : tc::idesc_bf16(BM, D)) | tc::IDESC_B_MN;
     struct Stream {
       uint32_t seg, done, items;  // segments begun, O products and last S's issued, all in all
       int k, count, tiles;        // tiles of the segment taken; that this stream meets; all
@@ -535,7 +528,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
           did = true;
           tc::fence_after_sync();
           const uint64_t vd =
-              tc::smem_desc_sw128_mn(sv + s.v_slot * G::SLOT, D == 128 ? HALF_BYTES : 0);
+              tc::smem_desc_sw128_mn(sv + s.v_slot * G::PLACE, D == 128 ? HALF_BYTES : 0);
 #pragma unroll
           for (int k = 0; k < BT / 16; ++k)
             umma_ts_warp(tmem_o + x * D, tmem + x * BT + 8 * k, vd + 128 * k, idesc_o,
@@ -550,11 +543,11 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
         if (s.k < s.count) {
           // S of tile k
           if (!ready(&ctl->k_full[s.k_slot], s.k_phase) ||
-              (s.k == 0 && !ready(&ctl->q_full[x], s.items & 1)))
+              (s.k == 0 && !ready(G::FP8 ? &ctl->q_ready[x] : &ctl->q_full[x], s.items & 1)))
             continue;
           did = true;
           tc::fence_after_sync();
-          const uint64_t kd = tc::smem_desc_sw128(sk + s.k_slot * G::SLOT);
+          const uint64_t kd = tc::smem_desc_sw128(sk + s.k_slot * G::PLACE);
           const uint64_t qd = tc::smem_desc_sw128(sq + x * G::Q_ONE);
 #pragma unroll
           for (int h = 0; h < HALVES; ++h)
@@ -657,7 +650,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
           for (int q = 0; q < 4; ++q) {
             const int token = q * 32 + lane;
             const long long pos = (long long)tile * BT + token;
-            uint8_t *row = sv + slot * G::SLOT + token * 128;
+            uint8_t *row = sv + slot * G::PLACE + token * 128;
             if (pos >= end) {
 #pragma unroll
               for (int h = 0; h < HALVES; ++h)
@@ -667,6 +660,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
                       make_uint4(0, 0, 0, 0);
             } else if (pos > first) {
               // the sign bit of a half of odd: its exponent is all ones
+              constexpr uint32_t EXP = G::FP8 ? 0x7c00u : 0x7f80u, ONE = 0x8000u - EXP;
+              constexpr uint32_t EXPS = EXP << 16 | EXP, ONES = ONE << 16 | ONE;
               uint32_t odd = 0;
 #pragma unroll
               for (int h = 0; h < HALVES; ++h)
@@ -674,8 +669,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
                 for (int c = 0; c < 8; ++c) {
                   const uint4 y = *reinterpret_cast<const uint4 *>(row + h * HALF_BYTES +
                                                                    ((c ^ (token & 7)) * 16));
-                  odd |= ((y.x & 0x7f807f80u) + 0x00800080u) | ((y.y & 0x7f807f80u) + 0x00800080u) |
-                         ((y.z & 0x7f807f80u) + 0x00800080u) | ((y.w & 0x7f807f80u) + 0x00800080u);
+                  odd |= ((y.x & EXPS) + ONES) | ((y.y & EXPS) + ONES) | ((y.z & EXPS) + ONES) |
+                         ((y.w & EXPS) + ONES);
                 }
               if (odd & 0x80008000u) {
                 const int node = (int)(pos - first);
@@ -683,8 +678,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
 #pragma unroll 1
                 for (int w = 0; w < HALVES * 32; ++w) {
                   uint32_t *at = reinterpret_cast<uint32_t *>(row + (w / 32) * HALF_BYTES) + w % 32;
-                  if ((*at & 0x7f80u) == 0x7f80u) *at &= 0xffff0000u;
-                  if ((*at & 0x7f800000u) == 0x7f800000u) *at &= 0xffffu;
+                  if ((*at & EXP) == EXP) *at &= 0xffff0000u;
+                  if ((*at & EXP << 16) == EXP << 16) *at &= 0xffffu;
                 }
               }
             }
@@ -703,6 +698,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
     }
   } else if (warp < 12) {
     more_registers<G::REGS_SOFTMAX>();
+    using R = Range<G::FP8>;
     // ----------------------------------------------------------- softmax ----
     const int x = (warp - 4) >> 2, quarter = warp & 3, m = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
@@ -716,7 +712,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
       const Segment *const n = &ctl->seg[seg % SEGS];
       const int tb = n->tb, count = n->count[x];
       if (tb == n->te) break;
-      const float c = n->c;
+      float c = n->c;
       const int node = n->node0 + x * a.nodes_tile + my_node;  // of the request
       const bool mine = my_node < a.nodes_tile && x * a.nodes_tile + my_node < n->nodes;
       // tokens that this row sees, and that the tile's first row does
@@ -730,6 +726,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
         ok = warp_wait(&ctl->s_full[x], tiles_done & 1, abort);
         if (!ok) break;
         tc::fence_after_sync();
+        // the row's power of two out of its scores: known since the product is done
+        if (G::FP8 && k == 0) c = attn::times_power(c, -ctl->q_exp[items_done & 1][x][m]);
         float2 e[64];
         {
           uint32_t s[4][32];
@@ -757,9 +755,9 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
 #pragma unroll
         for (int j = 0; j < 64; ++j) top[j & 3] = max3(top[j & 3], e[j].x, e[j].y);
         const float most = max3(fmaxf(top[0], top[1]), top[2], top[3]);
-        if (__any_sync(0xffffffffu, unset || most > RAISE)) {
+        if (__any_sync(0xffffffffu, unset || most > R::RAISE)) {
           const bool fresh = unset, number = fabsf(most) < INFINITY;
-          const float raise = number && (fresh || most > RAISE) ? most : 0.0f;
+          const float raise = number && (fresh || most > R::RAISE) ? most - R::PEAK : 0.0f;
           if (number) unset = false;
           const float keep = fresh ? 1.0f : ex2_fast(-raise);
           if (k > 0 && __any_sync(0xffffffffu, keep != 1.0f)) {
@@ -791,7 +789,12 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
             const float2 v = make_float2(ex2_fast(e[8 * j + i].x), ex2_fast(e[8 * j + i].y));
             if (i & 1) l1 = add2(l1, v);
             else l0 = add2(l0, v);
-            pk[i] = pack_bf16(v.x, v.y);
+            if constexpr (G::FP8) {
+              const __half2 h = __floats2half2_rn(v.x, v.y);
+              pk[i] = *reinterpret_cast<const uint32_t *>(&h);
+            } else {
+              pk[i] = pack_bf16(v.x, v.y);
+            }
           }
           tmem_st8(ts + 8 * j, pk);  // two weights a column
         }
@@ -884,71 +887,115 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
         }
         tc::fence_before_sync();
       }
-      // the group has read the segment
-      asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + x) : "memory");
-      if (m == 0) tc::mbar_arrive(&ctl->seg_empty[seg % SEGS]);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&ctl->seg_empty[seg % SEGS]);
     }
     __syncwarp();
   } else {
     if constexpr (G::FP8) {
       fewer_registers<G::REGS_WIDEN>();
-      // --------------------------------------------- 8-bit tiles made bf16 ----
+      // ------------------------------- 8-bit tiles, and Q, made f16 ----
       const int w = warp - 12, token = w * 32 + lane;
-      int k_slot = 0, v_slot = 0, raw = 0;
-      uint32_t k_phase = 0, v_phase = 0, raw_phase = 0;
+      int k_slot = 0, v_slot = 0;
+      uint32_t k_phase = 0, v_phase = 0, uses[2] = {0, 0};
       bool ok = true;
+      // A tile in its place, a thread a token: its row is read before it is written.
+      auto widen = [&](uint8_t *slot, uint64_t *raw, uint64_t *full, uint32_t phase) {
+        ok = warp_wait(raw, phase, abort);
+        // eight lanes take eight tokens: the swizzles spread both sides over all banks
+        const int raw_x = D == 128 ? token & 7 : (token >> 1) & 3;
+        uint4 v[D / 16];
+#pragma unroll
+        for (int p = 0; p < D / 16; ++p)
+          v[p] = *reinterpret_cast<const uint4 *>(slot + G::RAW_AT + token * D + ((p ^ raw_x) * 16));
+#pragma unroll
+        for (int p = 0; p < D / 16; ++p) {
+          const uint32_t in[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
+          uint32_t o[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o[2 * i] = attn::widen_e4m3x2(in[i] & 0xffffu);
+            o[2 * i + 1] = attn::widen_e4m3x2(in[i] >> 16);
+          }
+          uint8_t *row = slot + (p / 4) * HALF_BYTES + token * 128;
+          const int cc = (2 * p) % 8;
+          *reinterpret_cast<uint4 *>(row + ((cc ^ (token & 7)) * 16)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4 *>(row + (((cc + 1) ^ (token & 7)) * 16)) =
+              make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        tc::fence_async_smem();
+        __syncwarp();
+        if (ok && lane == 0) tc::mbar_arrive(full);
+      };
       for (uint32_t seg = 0; ok; ++seg) {
         ok = warp_wait(&ctl->seg_full[seg % SEGS], (seg / SEGS) & 1, abort);
         if (!ok) break;
-        const int tiles = ctl->seg[seg % SEGS].te - ctl->seg[seg % SEGS].tb;
+        const Segment *n = &ctl->seg[seg % SEGS];
+        const int tiles = n->te - n->tb, count[2] = {n->count[0], n->count[1]};
         if (tiles == 0) break;
 #pragma unroll 1
-        for (int fill = 0; fill < 2 * tiles; ++fill) {
-          const bool is_v = fill & 1;
-          const int at = is_v ? v_slot : k_slot;
-          ok = warp_wait(&ctl->r_full[raw], raw_phase, abort) &&
-               warp_wait(is_v ? &ctl->v_empty[at] : &ctl->k_empty[at],
-                         (is_v ? v_phase : k_phase) ^ 1, abort);
-          if (!ok) break;
-          const uint8_t *src = raws + raw * G::RAW;
-          uint8_t *dst = (is_v ? sv : sk) + at * G::SLOT;
-          // eight lanes take eight tokens: the swizzles spread both sides over all banks
-          const int raw_x = D == 128 ? token & 7 : (token >> 1) & 3;
-#pragma unroll
-          for (int p = 0; p < D / 16; ++p) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(src + token * D + ((p ^ raw_x) * 16));
-            const uint2 o0 = widen_e4m3x4(v.x), o1 = widen_e4m3x4(v.y), o2 = widen_e4m3x4(v.z),
-                        o3 = widen_e4m3x4(v.w);
-            uint8_t *row = dst + (p / 4) * HALF_BYTES + token * 128;
-            const int cc = (2 * p) % 8;
-            *reinterpret_cast<uint4 *>(row + ((cc ^ (token & 7)) * 16)) =
-                make_uint4(o0.x, o0.y, o1.x, o1.y);
-            *reinterpret_cast<uint4 *>(row + (((cc + 1) ^ (token & 7)) * 16)) =
-                make_uint4(o2.x, o2.y, o3.x, o3.y);
-          }
-          tc::fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tc::mbar_arrive(is_v ? &ctl->v_full[at] : &ctl->k_full[at]);
-            tc::mbar_arrive(&ctl->r_empty[raw]);
-          }
-          if (++raw == G::RAWS) {
-            raw = 0;
-            raw_phase ^= 1;
-          }
-          if (is_v) {
-            if (++v_slot == G::VS) {
-              v_slot = 0;
-              v_phase ^= 1;
-            }
-          } else if (++k_slot == G::KS) {
+        for (int t = 0; t < tiles; ++t) {
+          widen(sk + k_slot * G::PLACE, &ctl->kr_full[k_slot], &ctl->k_full[k_slot], k_phase);
+          if (++k_slot == G::KS) {
             k_slot = 0;
             k_phase ^= 1;
           }
+          if (t == 0) {
+            // Q's tiles in place, a thread a row: times the power of two that brings its
+            // largest finite value to 2^14
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t use = x ? uses[1] : uses[0];
+              if ((x ? count[1] : count[0]) == 0) continue;
+              ok = ok && warp_wait(&ctl->q_full[x], use & 1, abort);
+              uint8_t *row = sq + x * G::Q_ONE + token * 128;
+              int most = 0;  // bf16 bits without the sign: ordered as numbers
+#pragma unroll
+              for (int p = 0; p < HALVES * 8; ++p) {
+                const uint4 y = *reinterpret_cast<const uint4 *>(row + (p / 8) * BM * 128 +
+                                                                 ((p % 8) ^ (token & 7)) * 16);
+                const uint32_t v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int lo = v[i] & 0x7fff, hi = v[i] >> 16 & 0x7fff;
+                  most = max(most, max(lo < 0x7f80 ? lo : 0, hi < 0x7f80 ? hi : 0));
+                }
+              }
+              // its exponent is (most >> 7) - 127; a subnormal's is taken as the least
+              const int up = most ? 14 + 127 - max(most >> 7, 1) : 0;
+#pragma unroll
+              for (int p = 0; p < HALVES * 8; ++p) {
+                uint4 *at = reinterpret_cast<uint4 *>(row + (p / 8) * BM * 128 +
+                                                      ((p % 8) ^ (token & 7)) * 16);
+                const uint4 y = *at;
+                const uint32_t v[4] = {y.x, y.y, y.z, y.w};
+                uint32_t o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const __half2 h = __floats2half2_rn(attn::times_power(bf16_lo(v[i]), up),
+                                                      attn::times_power(bf16_hi(v[i]), up));
+                  o[i] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                *at = make_uint4(o[0], o[1], o[2], o[3]);
+              }
+              ctl->q_exp[use & 1][x][token] = (int16_t)up;
+              tc::fence_async_smem();
+              __syncwarp();
+              if (ok && lane == 0) tc::mbar_arrive(&ctl->q_ready[x]);
+              if (x) ++uses[1];
+              else ++uses[0];
+            }
+          }
+          widen(sv + v_slot * G::PLACE, &ctl->vr_full[v_slot], &ctl->v_full[v_slot], v_phase);
+          if (++v_slot == G::VS) {
+            v_slot = 0;
+            v_phase ^= 1;
+          }
+          if (!ok) break;
         }
-        if (!ok) break;
-        asm volatile("barrier.cta.sync 3, 128;" ::: "memory");
-        if (w == 0 && lane == 0) tc::mbar_arrive(&ctl->seg_empty[seg % SEGS]);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ctl->seg_empty[seg % SEGS]);
       }
     }
   }
