@@ -72,6 +72,12 @@ int launch(const Launch &l) {
   if (dspark_launch_pdl(kernel, dim3(l.ctas), dim3(G::THREADS), G::SMEM_BYTES, l.stream, tk, tv,
                         tq, a) != cudaSuccess)
     return DSPARK_ERR_CUDA;
+  // Requests too short to be cut (a table has no place for two pieces) leave nothing to join.
+  if (((int64_t)a.max_pages << a.page_shift) <= (2 * chunk::MIN_PIECE - 1) * chunk::BT) {
+    DSPARK_CHECK_LAUNCH();
+    dspark_count_launches(1);
+    return DSPARK_OK;
+  }
   if (dspark_launch_pdl(chunk::chunk_attention_join<D>, dim3(l.ctas, 2, D / 32), dim3(chunk::BM),
                         0, l.stream, a) != cudaSuccess)
     return DSPARK_ERR_CUDA;

@@ -51,7 +51,7 @@ constexpr int MAX_SLOTS = 4;        // of K, of V
 constexpr int SEGS = 4;             // segments published ahead
 // What beginning and ending an item costs, in tokens; the least share worth a CTA of its
 // own; and the least piece, in tiles, that an item is cut into.
-constexpr int OVERHEAD = 256, MIN_SHARE = 768, MIN_PIECE = 2;
+constexpr int OVERHEAD = 256, MIN_SHARE = 320, MIN_PIECE = 2;
 // log2: how far scores may pass the reference, and where a new reference puts the largest.
 template <bool FP8>
 struct Range {
@@ -95,6 +95,10 @@ struct Geo {
   static constexpr int SMEM_BYTES = (KS + VS) * PLACE + Q_BYTES + CTL_BYTES;
   static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory");
   static constexpr uint32_t TMEM_COLS = 512;  // S_0, S_1, O_0, O_1
+  // Whether O's product begins with half of P.  At 64 columns the softmax is the longer
+  // part (eight chunks of 4096 rows: 1727 us with it, 1812 without); at 128 it changed
+  // nothing (378), and beside an 8-bit cache it cost 8% (604 and 554 us, long contexts).
+  static constexpr bool HALVED = !FP8 && D == 64;
 };
 
 // A request as the kernel takes it: every later index is in bounds by this.
@@ -116,7 +120,7 @@ struct Request {
     } else {
       total = ctx + n;
     }
-    items = (int)(((long long)n + 2 * a.nodes_tile - 1) / (2 * a.nodes_tile));
+    items = (int)(((uint32_t)n + 2 * a.nodes_tile - 1) / (uint32_t)(2 * a.nodes_tile));
     return ok || n == 0;
   }
   // the cost of a KV head's first x items
@@ -129,7 +133,7 @@ struct Request {
   // an item's tokens, in tiles
   __device__ __forceinline__ int tiles(const Args &a, int item) const {
     const long long rows = min((long long)n, (long long)(item + 1) * 2 * a.nodes_tile);
-    return (int)((min((long long)total, ctx + rows) + BT - 1) / BT);
+    return (int)((min((long long)total, ctx + rows) + BT - 1) >> 7);
   }
 };
 
@@ -151,7 +155,7 @@ __device__ __forceinline__ Place locate(const Args &a, const Request &q, int r, 
   Place p;
   p.r = r;
   const long long each = q.upto(a, q.items);
-  p.h = (int)(off / each);
+  p.h = attn::quotient(off, each);
   off -= p.h * each;
   int lo = 0, hi = q.items - 1;  // the last item that begins at or before off
   while (lo < hi) {
@@ -162,7 +166,7 @@ __device__ __forceinline__ Place locate(const Args &a, const Request &q, int r, 
   p.item = lo;
   const long long in = off - q.upto(a, lo) - OVERHEAD;
   const int tiles = q.tiles(a, lo);
-  p.tile = in <= 0 ? 0 : (int)min((in + BT / 2) / BT, (long long)tiles);
+  p.tile = in <= 0 ? 0 : (int)min((in + BT / 2) >> 7, (long long)tiles);
   if (p.tile < MIN_PIECE) p.tile = 0;
   if (p.tile && tiles - p.tile < MIN_PIECE) {  // the next item's beginning
     p.tile = 0;
@@ -189,17 +193,20 @@ struct Ctl {
   uint64_t k_full[MAX_SLOTS], k_empty[MAX_SLOTS], v_full[MAX_SLOTS], v_empty[MAX_SLOTS];
   uint64_t v_ready[MAX_SLOTS];          // and nothing in V that must not be met
   uint64_t kr_full[MAX_SLOTS], vr_full[MAX_SLOTS];  // 8-bit tiles as they were copied
-  // by tile of Q: copied; in f16 (8 bits); its last S issued; S, P and the item's O complete
-  uint64_t q_full[2], q_ready[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
+  // by tile of Q: copied; in f16 (8 bits); its last S issued; S, half of P, P and the item's
+  // O complete
+  uint64_t q_full[2], q_ready[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], drain;
   uint64_t seg_full[SEGS], seg_empty[SEGS];
   long long sums[16];
   Place first, last;
+  Request first_q;  // the request first_r as it was read
+  int first_r;
   alignas(16) Segment seg[SEGS];
   int tail[5], head;
   int abort;
   uint32_t tmem;
-  // 8 bits: by which power of two each row of Q was multiplied, of every other item's
-  int16_t q_exp[2][2][BM];
+  // 8 bits: of each row of Q the largest exponent, by turns of items
+  uint8_t q_exp[2][2][BM];
 };
 static_assert(sizeof(Ctl) <= CTL_BYTES, "control block");
 
@@ -242,6 +249,10 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
       : "memory");
 }
 
+// Of a row of Q beside an 8-bit cache: the power of two that it was multiplied by, from
+// its largest value's exponent (0 for a row of zeros).
+__device__ __forceinline__ int row_exponent(int e) { return e ? 14 + 127 - e : 0; }
+
 template <int TYPE, int D>
 __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
     chunk_attention_kernel(const __grid_constant__ CUtensorMap tma_k,
@@ -274,6 +285,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
       tc::mbar_init(&ctl->q_ready[x], 4);
       tc::mbar_init(&ctl->q_empty[x], 1);
       tc::mbar_init(&ctl->s_full[x], 1);
+      tc::mbar_init(&ctl->p_half[x], 4);
       tc::mbar_init(&ctl->p_full[x], 4);
       tc::mbar_init(&ctl->o_full[x], 1);
     }
@@ -322,11 +334,13 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
       all += ctl->sums[w];
       if (w < warp) below += ctl->sums[w];
     }
-    const int shares = (int)max(1ll, min((long long)gridDim.x, all / MIN_SHARE));
-    const long long share = all / shares, longer = all - share * shares;
+    const int shares = all >= (long long)MIN_SHARE * gridDim.x ? gridDim.x
+                                                                : max((int)all / MIN_SHARE, 1);
+    const long long share = attn::divide_small(all, (uint32_t)shares), longer = all - share * shares;
     if (threadIdx.x == 0) {
       const Place end = {a.R, 0, 0, 0};
       ctl->first = ctl->last = end;
+      ctl->first_r = -1;
     }
     __syncthreads();
     // the thread whose requests a cut lies in finds its place; the last cut is the end
@@ -344,6 +358,10 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
           off -= m;
         }
         (side ? ctl->last : ctl->first) = locate(a, q, r, off);
+        if (side == 0) {
+          ctl->first_q = q;
+          ctl->first_r = r;
+        }
       }
     }
     __syncthreads();
@@ -361,8 +379,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
     bool ok = true;
     Place p = ctl->first;
     const Place last = ctl->last;
-    Request q;
-    int known = -1;
+    Request q = ctl->first_q;
+    int known = ctl->first_r;
     for (int published = 0; ok; ++published) {
       while (before(p, last) && known != p.r) {
         q.set(a, a.ctx[p.r], a.row_start[p.r], a.row_start[p.r + 1]);
@@ -388,7 +406,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
           const int rows_x = min(s.nodes - x * a.nodes_tile, a.nodes_tile);
           const long long sees = min((long long)q.total,
                                      (long long)q.ctx + s.node0 + x * a.nodes_tile + rows_x);
-          const int tiles_x = rows_x > 0 ? (int)((sees + BT - 1) / BT) : 0;
+          const int tiles_x = rows_x > 0 ? (int)((sees + BT - 1) >> 7) : 0;
           s.count[x] = max(0, min(s.te, tiles_x) - s.tb);
         }
         s.c = a.scale * LOG2E * (a.k_scale ? a.k_scale[p.h] : 1.0f);
@@ -477,10 +495,10 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
       int k, count, tiles;        // tiles of the segment taken; that this stream meets; all
       int k_slot, v_slot;
       uint32_t k_phase, v_phase;
-      bool s_out, open, over;     // s_out: S is issued, its O is next
+      bool s_out, half, open, over;  // S is issued, its O is next; half of it is issued
     } st[2];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) st[x] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, false, false, false};
+    for (int x = 0; x < 2; ++x) st[x] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, false, false, false, false};
     auto ready = [&](uint64_t *bar, uint32_t parity) {
       return __all_sync(0xffffffffu, tc::mbar_test(bar, parity)) != 0;
     };
@@ -523,16 +541,29 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
         }
         if (s.s_out) {
           // O of tile k
-          if (!ready(&ctl->p_full[x], s.done & 1) || !ready(&ctl->v_ready[s.v_slot], s.v_phase))
-            continue;
-          did = true;
-          tc::fence_after_sync();
           const uint64_t vd =
               tc::smem_desc_sw128_mn(sv + s.v_slot * G::PLACE, D == 128 ? HALF_BYTES : 0);
+          if (!s.half) {
+            if (!ready(G::HALVED ? &ctl->p_half[x] : &ctl->p_full[x], s.done & 1) ||
+                !ready(&ctl->v_ready[s.v_slot], s.v_phase))
+              continue;
+            did = true;
+            tc::fence_after_sync();
 #pragma unroll
-          for (int k = 0; k < BT / 16; ++k)
-            umma_ts_warp(tmem_o + x * D, tmem + x * BT + 8 * k, vd + 128 * k, idesc_o,
-                         s.k > 0 || k != 0);
+            for (int k = 0; k < BT / 32; ++k)
+              umma_ts_warp(tmem_o + x * D, tmem + x * BT + 8 * k, vd + 128 * k, idesc_o,
+                           s.k > 0 || k != 0);
+            s.half = true;
+          }
+          if (G::HALVED) {
+            if (!ready(&ctl->p_full[x], s.done & 1)) continue;
+            did = true;
+            tc::fence_after_sync();
+          }
+#pragma unroll
+          for (int k = BT / 32; k < BT / 16; ++k)
+            umma_ts_warp(tmem_o + x * D, tmem + x * BT + 8 * k, vd + 128 * k, idesc_o, 1);
+          s.half = false;
           tc::umma_commit_warp(&ctl->v_empty[s.v_slot]);
           if (s.k + 1 == s.count) tc::umma_commit_warp(&ctl->o_full[x]);
           next_v(s);
@@ -727,20 +758,28 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
         if (!ok) break;
         tc::fence_after_sync();
         // the row's power of two out of its scores: known since the product is done
-        if (G::FP8 && k == 0) c = attn::times_power(c, -ctl->q_exp[items_done & 1][x][m]);
+        if (G::FP8 && k == 0) c = attn::times_power(c, -row_exponent(ctl->q_exp[items_done & 1][x][m]));
         float2 e[64];
         {
           uint32_t s[4][32];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) tc::tmem_ld32(ts + 32 * j, s[j]);
+          tc::tmem_ld32(ts, s[0]);
+          tc::tmem_ld32(ts + 32, s[1]);
           tc::tmem_wait_ld();
+          tc::reg_fence(s[0]);
+          tc::reg_fence(s[1]);
+          tc::tmem_ld32(ts + 64, s[2]);  // under the first half's work
+          tc::tmem_ld32(ts + 96, s[3]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) tc::reg_fence(s[j]);
-#pragma unroll
-          for (int j = 0; j < 64; ++j)
+          for (int j = 0; j < 64; ++j) {
+            if (j == 32) {
+              tc::tmem_wait_ld();
+              tc::reg_fence(s[2]);
+              tc::reg_fence(s[3]);
+            }
             e[j] = fma2(make_float2(__uint_as_float(s[j / 16][2 * j % 32]),
                                     __uint_as_float(s[j / 16][2 * j % 32 + 1])),
                         make_float2(c, c), make_float2(nm, nm));
+          }
         }
         const int t0 = (tb + k) * BT;
         if (t0 + BT > all_see) {
@@ -797,6 +836,12 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
             }
           }
           tmem_st8(ts + 8 * j, pk);  // two weights a column
+          if (G::HALVED && j == 3) {  // the product may begin
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&ctl->p_half[x]);
+          }
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
@@ -963,7 +1008,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
                 }
               }
               // its exponent is (most >> 7) - 127; a subnormal's is taken as the least
-              const int up = most ? 14 + 127 - max(most >> 7, 1) : 0;
+              const int top = most ? max(most >> 7, 1) : 0, up = row_exponent(top);
 #pragma unroll
               for (int p = 0; p < HALVES * 8; ++p) {
                 uint4 *at = reinterpret_cast<uint4 *>(row + (p / 8) * BM * 128 +
@@ -979,7 +1024,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
                 }
                 *at = make_uint4(o[0], o[1], o[2], o[3]);
               }
-              ctl->q_exp[use & 1][x][token] = (int16_t)up;
+              ctl->q_exp[use & 1][x][token] = (uint8_t)top;
               tc::fence_async_smem();
               __syncwarp();
               if (ok && lane == 0) tc::mbar_arrive(&ctl->q_ready[x]);
