@@ -28,15 +28,63 @@ struct RopeArgs {
   const int64_t *slot;
 };
 
-constexpr int THREADS = 256, BLOCKS_SM = 4;
-constexpr int AT_ONCE = 4;  // heads of a lane whose loads are in flight together
+constexpr int THREADS = 256, BLOCKS_SM = 2;
+constexpr int BATCH = 4;          // steps of a warp whose loads are asked for together
+constexpr int STEP_BYTES = 1024;  // 32 bytes a lane
+constexpr int SMEM_BYTES = THREADS / 32 * 2 * BATCH * STEP_BYTES;
+enum { Q_HEADS, K_HEADS, V_HEADS };
 
-__device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8]) {
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mov.b64 c, {%6, %7};\n fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+// A lane's 16 values of a head, two chunks of 8, as the first and the second values of
+// eight pairs, two of them in a float2.
+template <bool PAIRS>
+__device__ __forceinline__ void unpack(const uint4 (&x)[2], float2 (&a)[4], float2 (&b)[4]) {
+  const uint32_t v[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16_lo(v[i]);
-    x[2 * i + 1] = bf16_hi(v[i]);
+    if constexpr (PAIRS) {
+      a[i] = make_float2(bf16_lo(v[2 * i]), bf16_lo(v[2 * i + 1]));
+      b[i] = make_float2(bf16_hi(v[2 * i]), bf16_hi(v[2 * i + 1]));
+    } else {
+      a[i] = make_float2(bf16_lo(v[i]), bf16_hi(v[i]));
+      b[i] = make_float2(bf16_lo(v[4 + i]), bf16_hi(v[4 + i]));
+    }
+  }
+}
+// Back in the chunks' order.
+template <bool PAIRS>
+__device__ __forceinline__ void in_order(const float2 (&a)[4], const float2 (&b)[4],
+                                         float (&lo)[8], float (&hi)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (PAIRS) {
+      float *to = i < 2 ? lo + 4 * i : hi + 4 * (i - 2);
+      to[0] = a[i].x;
+      to[1] = b[i].x;
+      to[2] = a[i].y;
+      to[3] = b[i].y;
+    } else {
+      lo[2 * i] = a[i].x;
+      lo[2 * i + 1] = a[i].y;
+      hi[2 * i] = b[i].x;
+      hi[2 * i + 1] = b[i].y;
+    }
   }
 }
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
@@ -49,13 +97,9 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-__device__ __noinline__ uint2 divided_e4m3(const float (&x)[8], float scale) {
-  uint32_t o[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    o[i] = pack_e4m3x2(x[4 * i] / scale, x[4 * i + 1] / scale) |
-           pack_e4m3x2(x[4 * i + 2] / scale, x[4 * i + 3] / scale) << 16;
-  return make_uint2(o[0], o[1]);
+// (out of line: it is seldom called)
+__device__ __noinline__ uint32_t divided_e4m3(float a, float b, float c, float d, float scale) {
+  return pack_e4m3x2(a / scale, b / scale) | pack_e4m3x2(c / scale, d / scale) << 16;
 }
 
 // Eight values over a scale as e4m3, by the scale's reciprocal where the quotient rounds
@@ -72,7 +116,8 @@ __device__ __forceinline__ uint2 scaled_e4m3(const float (&x)[8], float scale, f
     least = min(least, (__float_as_uint(q[i]) + 4) & 0x7ffff);
   }
   if (!near_one || (least < 8 && (__float_as_uint(scale) & 0x7fffff) != 0))
-    return divided_e4m3(x, scale);
+    return make_uint2(divided_e4m3(x[0], x[1], x[2], x[3], scale),
+                      divided_e4m3(x[4], x[5], x[6], x[7], scale));
   uint32_t o[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -82,160 +127,247 @@ __device__ __forceinline__ uint2 scaled_e4m3(const float (&x)[8], float scale, f
 
 // A lane holds 16 values of a head, two chunks of 8: D / 16 lanes a head, 32 * 16 / D
 // heads a warp and step.  Chunks are dealt so that both values of a pair lie in one
-// lane: in halves chunk t and its partner rot / 2 values on, in pairs chunks 2 t and
-// 2 t + 1; lanes past the rotated values take two chunks of the rest.  All lanes with
+// lane: in halves chunk t and its partner rot / 2 values on (lanes past the rotated
+// values take two chunks of the rest), in pairs chunks t and t + D / 16.  All lanes with
 // one t turn by the same eight angles, which the warp computes once a row, one or two a
-// lane.  A warp takes a row, or with few rows a part of its heads (`parts` warps a row).
+// lane, and multiplies by the weights: a head then takes four products a pair, and one
+// factor for its norm.
+//
+// A warp takes a row, or with few rows a part of its steps (`parts` warps a row), the
+// queries' heads first, then the keys', then the values'.  Its loads run one batch of
+// steps ahead, into the lanes' own places in shared memory (no barrier): 128 KB are then
+// in flight on an SM, which registers have no room for.
 template <int D, bool FP8, bool PAIRS>
-__global__ void __launch_bounds__(THREADS) rope_append_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(THREADS, BLOCKS_SM) rope_append_kernel(const RopeArgs a) {
   constexpr int LPH = D / 16, HPW = 32 / LPH, FREQS = D / 64;
+  extern __shared__ __align__(16) uint8_t smem[];
   pdl_trigger();
   pdl_wait();
   const CacheView &c = a.c;
   const int lane = threadIdx.x & 31, t = lane % LPH, sub = lane / LPH;
-  const bool turns = 16 * t < a.rot;
+  uint8_t *const mine = smem + (threadIdx.x >> 5) * 2 * BATCH * STEP_BYTES + lane * 16;
+  // whether the lane's first four pairs turn, and its last four
+  const bool turns[2] = {(PAIRS ? 8 : 16) * t < a.rot, (PAIRS ? 8 * t + D / 2 : 16 * t) < a.rot};
   const int rest = a.rot / 8 + 2 * (t - a.rot / 16);
-  const int lo = 8 * (PAIRS ? 2 * t : (turns ? t : rest));
-  const int hi = PAIRS ? lo + 8 : (turns ? lo + a.rot / 2 : lo + 8);
+  const int lo = 8 * (PAIRS || turns[0] ? t : rest);
+  const int hi = lo + (PAIRS ? D / 2 : turns[0] ? a.rot / 2 : 8);
+  const int steps_q = (a.heads_q + HPW - 1) / HPW, steps_k = (c.heads + HPW - 1) / HPW;
+  const int steps = steps_q + 2 * steps_k;
+  const int64_t n_slots = (int64_t)c.n_pages << c.page_shift;
+  const int64_t warps = (int64_t)gridDim.x * (THREADS / 32);
+  const int64_t units = (int64_t)a.n_rows * a.parts;
+
+  struct Unit {
+    int row, s, end, pos;
+    int64_t slot;
+  };
+  int64_t at = (int64_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5);
+  auto read_unit = [&](Unit &u) {
+    if (at >= units) {
+      u.row = -1;
+      return;
+    }
+    u.row = (int)(at / a.parts);
+    const int part = (int)(at - (int64_t)u.row * a.parts);
+    u.s = (int)((int64_t)steps * part / a.parts);
+    u.end = (int)((int64_t)steps * (part + 1) / a.parts);
+    u.pos = a.position[u.row];
+    u.slot = a.slot[u.row];
+    at += warps;
+  };
+  // the next row that is no padding
+  auto next_unit = [&](Unit &u, Unit &ahead) {
+    do {
+      u = ahead;
+      if (u.row < 0) return;
+      read_unit(ahead);
+    } while (u.pos < 0);
+  };
+  // a batch of steps from u.s on, into one half of the warp's place
+  auto issue = [&](const Unit &u, int half) {
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int s = u.s + i;
+      if (s >= u.end) break;
+      const bool is_q = s < steps_q, is_k = s < steps_q + steps_k;
+      const int h = (s - (is_q ? 0 : is_k ? steps_q : steps_q + steps_k)) * HPW + sub;
+      if (h >= (is_q ? a.heads_q : c.heads)) continue;
+      const bf16 *src = is_q ? a.q + u.row * a.q_row + h * a.q_head
+                             : (is_k ? a.k : a.v) + u.row * a.kv_row + h * a.kv_head;
+      const uint32_t to =
+          (uint32_t)__cvta_generic_to_shared(mine + (half * BATCH + i) * STEP_BYTES);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src + lo) : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + STEP_BYTES / 2),
+                   "l"(src + hi)
+                   : "memory");
+    }
+  };
+
   uint64_t turn[FREQS];
 #pragma unroll
   for (int f = 0; f < FREQS; ++f) {
-    const int i = 8 * t + sub * FREQS + f;  // the pair that this lane computes for lanes t
+    // the pair that this lane computes for lanes t, the j-th of their eight
+    const int j = sub * FREQS + f;
+    const int i = PAIRS ? 4 * t + j + (j < 4 ? 0 : D / 4 - 4) : 8 * t + j;
     turn[f] = 2 * i < a.rot ? a.turns[i] : 0;
   }
-  uint4 wq[2] = {}, wk[2] = {};
-  if (a.q_weight) {
-    wq[0] = *reinterpret_cast<const uint4 *>(a.q_weight + lo);
-    wq[1] = *reinterpret_cast<const uint4 *>(a.q_weight + hi);
-  }
-  if (a.k_weight) {
-    wk[0] = *reinterpret_cast<const uint4 *>(a.k_weight + lo);
-    wk[1] = *reinterpret_cast<const uint4 *>(a.k_weight + hi);
-  }
-  const int heads = a.heads_q + 2 * c.heads, steps = (heads + HPW - 1) / HPW;
-  const int64_t n_slots = (int64_t)c.n_pages << c.page_shift;
-  const int64_t warps = (int64_t)gridDim.x * (THREADS / 32);
-  for (int64_t unit = (int64_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5);
-       unit < (int64_t)a.n_rows * a.parts; unit += warps) {
-    const int row = (int)(unit / a.parts), part = (int)(unit - (int64_t)row * a.parts);
-    const int pos = a.position[row];
-    if (pos < 0) continue;
-    const int64_t slot = a.slot[row];
-    const bool stored = slot >= 0 && slot < n_slots;
-    if (slot >= n_slots && lane == 0) dspark_set_status(DSPARK_ERR_PAGES);
-    const int64_t place = stored ? (slot >> c.page_shift) * c.page_bytes +
-                                       (slot & ((1 << c.page_shift) - 1)) * c.token_bytes
-                                 : 0;
-    const int s0 = (int)((int64_t)steps * part / a.parts);
-    const int s1 = (int)((int64_t)steps * (part + 1) / a.parts);
-    float cs[8], sn[8];
-    bool known = false;
+  Unit u, ahead;
+  read_unit(ahead);
+  next_unit(u, ahead);
+  if (u.row < 0) return;
+  issue(u, 0);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  float my_c[FREQS], my_s[FREQS];
+  float2 ca[4], sa[4], cb[4], sb[4];  // by value: weight times cosine, times sine
+  int turned = -1, kind_made = -1;    // what they are for: a row, its queries or keys
 #pragma unroll 1
-    for (int s = s0; s < s1; s += AT_ONCE) {
-      uint4 x[AT_ONCE][2];
+  for (int half = 0;; half ^= 1) {
+    Unit next = u;
+    next.s += BATCH;
+    if (next.s >= u.end) next_unit(next, ahead);
+    if (next.row >= 0) issue(next, half ^ 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (turned != u.row) {  // under the loads
+      turned = u.row;
+      kind_made = -1;
 #pragma unroll
-      for (int u = 0; u < AT_ONCE; ++u) {
-        const int h = (s + u) * HPW + sub;
-        if (s + u >= s1 || h >= heads) continue;
-        const int g = h - a.heads_q;
-        const bf16 *src = g < 0 ? a.q + row * a.q_row + h * a.q_head
-                                : (g < c.heads ? a.k + row * a.kv_row + g * a.kv_head
-                                               : a.v + row * a.kv_row + (g - c.heads) * a.kv_head);
-        x[u][0] = *reinterpret_cast<const uint4 *>(src + lo);
-        x[u][1] = *reinterpret_cast<const uint4 *>(src + hi);
+      for (int f = 0; f < FREQS; ++f) {
+        const int32_t half_turns = (int32_t)(((uint64_t)u.pos * turn[f]) >> 32);
+        sincospif((float)half_turns * 0x1p-31f, &my_s[f], &my_c[f]);
       }
-      if (!known) {  // under the first loads
-        known = true;
-        float my_c[FREQS], my_s[FREQS];
-#pragma unroll
-        for (int f = 0; f < FREQS; ++f) {
-          const int32_t half_turns = (int32_t)(((uint64_t)pos * turn[f]) >> 32);
-          sincospif((float)half_turns * 0x1p-31f, &my_s[f], &my_c[f]);
+    }
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const bool stored = u.slot >= 0 && u.slot < n_slots;
+    if (u.slot >= n_slots && lane == 0) dspark_set_status(DSPARK_ERR_PAGES);
+    const int64_t place = stored ? (u.slot >> c.page_shift) * c.page_bytes +
+                                       (u.slot & ((1 << c.page_shift) - 1)) * c.token_bytes
+                                 : 0;
+    const int end = min(u.s + BATCH, u.end);
+#pragma unroll 1
+    for (int s = u.s; s < end; ++s) {  // a warp's lanes alike
+      const int kind = s < steps_q ? Q_HEADS : s < steps_q + steps_k ? K_HEADS : V_HEADS;
+      const int h =
+          (s - (kind == Q_HEADS ? 0 : kind == K_HEADS ? steps_q : steps_q + steps_k)) * HPW + sub;
+      const bool there = h < (kind == Q_HEADS ? a.heads_q : c.heads);
+      const uint8_t *from = mine + (half * BATCH + s - u.s) * STEP_BYTES;
+      const uint4 x[2] = {*reinterpret_cast<const uint4 *>(from),
+                          *reinterpret_cast<const uint4 *>(from + STEP_BYTES / 2)};
+      if (kind == V_HEADS && !FP8) {  // V's bits as they are
+        if (there && stored) {
+          uint8_t *dst = c.v + place + h * c.head_bytes;
+          *reinterpret_cast<uint4 *>(dst + 2 * lo) = x[0];
+          *reinterpret_cast<uint4 *>(dst + 2 * hi) = x[1];
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          cs[j] = __shfl_sync(0xffffffffu, my_c[j % FREQS], t + LPH * (j / FREQS));
-          sn[j] = __shfl_sync(0xffffffffu, my_s[j % FREQS], t + LPH * (j / FREQS));
-        }
+        continue;
       }
+      float2 p[4], q[4];
+      unpack<PAIRS>(x, p, q);
+      if (kind != V_HEADS) {
+        const bf16 *weight = kind == Q_HEADS ? a.q_weight : a.k_weight;
+        if (kind_made != kind) {
+          kind_made = kind;
+          uint4 w[2];
+          w[0] = w[1] = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+          if (weight) {
+            w[0] = *reinterpret_cast<const uint4 *>(weight + lo);
+            w[1] = *reinterpret_cast<const uint4 *>(weight + hi);
+          }
+          unpack<PAIRS>(w, ca, cb);
 #pragma unroll
-      for (int u = 0; u < AT_ONCE; ++u) {
-        const int h = (s + u) * HPW + sub, g = h - a.heads_q;
-        if (s + u >= s1) continue;  // a warp's lanes alike
-        const bool there = h < heads, is_q = g < 0, is_v = g >= c.heads;
-        float p[8] = {}, q[8] = {};
-        if (there) {
-          unpack8(x[u][0], p);
-          unpack8(x[u][1], q);
-        }
-        if (a.q_weight || a.k_weight) {
-          float sum = 0.0f;
+          for (int i = 0; i < 4; ++i) {
+            float cs[2], sn[2];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum = fmaf(p[i], p[i], fmaf(q[i], q[i], sum));
-#pragma unroll
-          for (int o = 1; o < LPH; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          if (!is_v && (is_q ? a.q_weight : a.k_weight)) {
-            const float inv = rsqrtf(sum * (1.0f / D) + a.eps);
-            float w[8];
-            unpack8(is_q ? wq[0] : wk[0], w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = p[i] * inv * w[i];
-            unpack8(is_q ? wq[1] : wk[1], w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = q[i] * inv * w[i];
+            for (int j = 0; j < 2; ++j) {
+              const int f = 2 * i + j;
+              cs[j] = __shfl_sync(0xffffffffu, my_c[f % FREQS], t + LPH * (f / FREQS));
+              sn[j] = __shfl_sync(0xffffffffu, my_s[f % FREQS], t + LPH * (f / FREQS));
+            }
+            sa[i] = make_float2(ca[i].x * sn[0], ca[i].y * sn[1]);
+            sb[i] = make_float2(-cb[i].x * sn[0], -cb[i].y * sn[1]);
+            ca[i] = make_float2(ca[i].x * cs[0], ca[i].y * cs[1]);  // 1 where nothing turns
+            cb[i] = make_float2(cb[i].x * cs[0], cb[i].y * cs[1]);
           }
         }
-        if (!there) continue;
-        if (turns && !is_v) {
-          if constexpr (PAIRS) {
+        float inv = 1.0f;
+        if (weight) {
+          float2 sum = mul2(p[0], p[0]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float a0 = p[2 * i], b0 = p[2 * i + 1], a1 = q[2 * i], b1 = q[2 * i + 1];
-              p[2 * i] = a0 * cs[i] - b0 * sn[i];
-              p[2 * i + 1] = b0 * cs[i] + a0 * sn[i];
-              q[2 * i] = a1 * cs[4 + i] - b1 * sn[4 + i];
-              q[2 * i + 1] = b1 * cs[4 + i] + a1 * sn[4 + i];
-            }
-          } else {
+          for (int i = 1; i < 4; ++i) sum = fma2(p[i], p[i], sum);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float a0 = p[i], b0 = q[i];
-              p[i] = a0 * cs[i] - b0 * sn[i];
-              q[i] = b0 * cs[i] + a0 * sn[i];
-            }
+          for (int i = 0; i < 4; ++i) sum = fma2(q[i], q[i], sum);
+          float all = sum.x + sum.y;
+#pragma unroll
+          for (int o = 1; o < LPH; o <<= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+          inv = rsqrtf(all * (1.0f / D) + a.eps);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const float2 pc[2] = {mul2(p[i], ca[i]), mul2(p[i + 1], ca[i + 1])};
+          const float2 qc[2] = {mul2(q[i], cb[i]), mul2(q[i + 1], cb[i + 1])};
+          if (turns[i / 2]) {
+            const float2 ps[2] = {p[i], p[i + 1]};
+            p[i] = fma2(q[i], sb[i], pc[0]);
+            p[i + 1] = fma2(q[i + 1], sb[i + 1], pc[1]);
+            q[i] = fma2(ps[0], sa[i], qc[0]);
+            q[i + 1] = fma2(ps[1], sa[i + 1], qc[1]);
+          } else {  // what does not turn meets nothing else
+            p[i] = pc[0];
+            p[i + 1] = pc[1];
+            q[i] = qc[0];
+            q[i + 1] = qc[1];
           }
         }
-        if (is_q) {
-          bf16 *dst = a.out + row * a.out_row + h * a.out_head;
-          *reinterpret_cast<uint4 *>(dst + lo) = pack8(p);
-          *reinterpret_cast<uint4 *>(dst + hi) = pack8(q);
-          continue;
+        if (weight) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            p[i] = mul2(p[i], make_float2(inv, inv));
+            q[i] = mul2(q[i], make_float2(inv, inv));
+          }
         }
-        if (!stored) continue;
-        const int kv = is_v ? g - c.heads : g;
-        uint8_t *dst = (is_v ? c.v : c.k) + place + kv * c.head_bytes;
+      }
+      if (!there) continue;
+      float y0[8], y1[8];
+      in_order<PAIRS>(p, q, y0, y1);
+      if (kind == Q_HEADS) {
+        bf16 *dst = a.out + u.row * a.out_row + h * a.out_head;
+        *reinterpret_cast<uint4 *>(dst + lo) = pack8(y0);
+        *reinterpret_cast<uint4 *>(dst + hi) = pack8(y1);
+      } else if (stored) {
+        uint8_t *dst = (kind == V_HEADS ? c.v : c.k) + place + h * c.head_bytes;
         if constexpr (FP8) {
-          const float *scales = is_v ? c.v_scale : c.k_scale;
-          const float scale = scales ? scales[kv] : 1.0f, inv = 1.0f / scale;
+          const float *scales = kind == V_HEADS ? c.v_scale : c.k_scale;
+          const float scale = scales ? scales[h] : 1.0f, inv = 1.0f / scale;
           const bool near_one = scale >= 0x1p-96f && scale <= 0x1p96f;
-          *reinterpret_cast<uint2 *>(dst + lo) = scaled_e4m3(p, scale, inv, near_one);
-          *reinterpret_cast<uint2 *>(dst + hi) = scaled_e4m3(q, scale, inv, near_one);
+          *reinterpret_cast<uint2 *>(dst + lo) = scaled_e4m3(y0, scale, inv, near_one);
+          *reinterpret_cast<uint2 *>(dst + hi) = scaled_e4m3(y1, scale, inv, near_one);
         } else {
-          // V's bits as they are
-          *reinterpret_cast<uint4 *>(dst + 2 * lo) = is_v ? x[u][0] : pack8(p);
-          *reinterpret_cast<uint4 *>(dst + 2 * hi) = is_v ? x[u][1] : pack8(q);
+          *reinterpret_cast<uint4 *>(dst + 2 * lo) = pack8(y0);
+          *reinterpret_cast<uint4 *>(dst + 2 * hi) = pack8(y1);
         }
       }
     }
+    if (next.row < 0) break;
+    u = next;
   }
 }
 
-template <int D, bool FP8>
-cudaError_t launch(const RopeArgs &a, bool pairs, dim3 grid, cudaStream_t stream) {
-  return pairs ? dspark_launch_pdl(rope_append_kernel<D, FP8, true>, grid, dim3(THREADS), 0,
-                                   stream, a)
-               : dspark_launch_pdl(rope_append_kernel<D, FP8, false>, grid, dim3(THREADS), 0,
-                                   stream, a);
+template <int D, bool FP8, bool PAIRS>
+cudaError_t launch(const RopeArgs &a, dim3 grid, cudaStream_t stream) {
+  auto kernel = rope_append_kernel<D, FP8, PAIRS>;
+  static DsparkPerDevice attr;
+  if (dspark_per_device(attr, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    SMEM_BYTES) == cudaSuccess
+                   ? 1
+                   : -1;
+      }) < 0)
+    return cudaErrorInvalidValue;
+  return dspark_launch_pdl(kernel, grid, dim3(THREADS), SMEM_BYTES, stream, a);
+}
+template <int D>
+cudaError_t launch(const RopeArgs &a, bool fp8, bool pairs, dim3 grid, cudaStream_t stream) {
+  if (fp8) return pairs ? launch<D, true, true>(a, grid, stream) : launch<D, true, false>(a, grid, stream);
+  return pairs ? launch<D, false, true>(a, grid, stream) : launch<D, false, false>(a, grid, stream);
 }
 
 bool rows_ok(const void *p, int64_t row, int64_t head) {
@@ -287,19 +419,28 @@ extern "C" int dspark_rope_append(const dspark_kv_cache *cache, int32_t n_rows, 
   a.turns = rope->turns;
   a.position = position;
   a.slot = slot;
-  // Rows are split over warps while that fills the GPU: half of its resident warps.
+  const int at_once = 512 / cache->dim;
+  const int steps = (heads_q + at_once - 1) / at_once + 2 * ((cache->heads + at_once - 1) / at_once);
   const int64_t resident = (int64_t)dspark_sm_count() * BLOCKS_SM * (THREADS / 32);
-  const int steps = (heads_q + 2 * cache->heads + 512 / cache->dim - 1) / (512 / cache->dim);
-  const int64_t want = resident / 2 / n_rows;
-  a.parts = (int)(want < 1 ? 1 : want < steps ? want : steps);
+  // Into how many parts a row is split: what leaves the busiest warp the least work, a
+  // part's angles and weights counted as two steps.
+  a.parts = 1;
+  int64_t least = INT64_MAX;
+  for (int parts = 1; parts <= steps && parts <= 64; ++parts) {
+    const int64_t turns = ((int64_t)n_rows * parts + resident - 1) / resident;
+    const int64_t work = turns * ((steps + parts - 1) / parts + 2);
+    if (work < least) {
+      least = work;
+      a.parts = parts;
+    }
+    if (turns > 64) break;
+  }
   const int64_t blocks = ((int64_t)n_rows * a.parts + THREADS / 32 - 1) / (THREADS / 32);
   const int64_t most = resident / (THREADS / 32);
   const dim3 grid((unsigned)(blocks < most ? blocks : most));
   const bool pairs = rope->style == DSPARK_ROPE_PAIRS, fp8 = cache->type == DSPARK_KV_E4M3;
-  const cudaError_t e = cache->dim == 64 ? (fp8 ? launch<64, true>(a, pairs, grid, stream)
-                                                : launch<64, false>(a, pairs, grid, stream))
-                                         : (fp8 ? launch<128, true>(a, pairs, grid, stream)
-                                                : launch<128, false>(a, pairs, grid, stream));
+  const cudaError_t e = cache->dim == 64 ? launch<64>(a, fp8, pairs, grid, stream)
+                                         : launch<128>(a, fp8, pairs, grid, stream);
   if (e != cudaSuccess) return DSPARK_ERR_CUDA;
   DSPARK_CHECK_LAUNCH();
   dspark_count_launches(1);
