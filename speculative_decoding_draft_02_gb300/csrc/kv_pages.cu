@@ -158,19 +158,17 @@ struct ReleaseArgs {
   int *held, *n_free, *free_pages, *refs;
 };
 
-// Holds are numbered request by request and in block order.  Every hold takes one off its
-// page's count, which a page that nobody holds any more then shows as -1; those pages
-// keep, as -(number + 2), the last of their holds, whose place on the stack they
-// take.  Barriers lie between; orders of atomics never matter.  Bound by these
-// steps of dependent reads.
+// Holds are numbered request by request and in block order, and every thread takes some
+// consecutive ones.  Every hold takes one off its page's count, which a page that nobody
+// holds any more then shows as -1; those pages keep, as -(number + 2), the last of their
+// holds, whose place on the stack they take.  Barriers lie between; orders of atomics
+// never matter.  Bound by these steps of dependent reads.
 __global__ void __launch_bounds__(THREADS, 1) kv_release_kernel(const ReleaseArgs a) {
-  extern __shared__ int smem[];
+  constexpr int KEPT = 4;  // pages of a thread's holds that are read once
+  extern __shared__ int first[];  // [R + 1] number of a request's first hold
   __shared__ long long warp_sums[WARPS];
-  int *first = smem;              // [R + 1] number of a request's first hold
-  int *pushed = first + a.R + 1;  // [R] pages that go back before a request's
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int ctas = gridDim.x, cta = blockIdx.x;
-  const int warps = ctas * WARPS, warp = cta * WARPS + (tid >> 5);
+  __shared__ int counts[CLUSTER];  // pages that each CTA gives back
+  const int tid = threadIdx.x, ctas = gridDim.x, cta = blockIdx.x;
   pdl_trigger();
   pdl_wait();
 
@@ -179,8 +177,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_release_kernel(const ReleaseArg
     dspark_set_status(DSPARK_ERR_PAGES);
     top = top < 0 ? 0 : a.n_pages;
   }
-  const int per = (a.R + THREADS - 1) / THREADS;
-  const int r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
+  const int per_r = (a.R + THREADS - 1) / THREADS;
+  const int r0 = min(tid * per_r, a.R), r1 = min(r0 + per_r, a.R);
   long long mine = 0, all;
   for (int r = r0; r < r1; ++r) {
     int h = a.ctx[r] < 0 ? a.held[r] : 0;
@@ -204,79 +202,69 @@ __global__ void __launch_bounds__(THREADS, 1) kv_release_kernel(const ReleaseArg
   }
   if (tid == 0) first[a.R] = (int)all;
   __syncthreads();
-  auto page_at = [&](int r, int j) {
-    const int page = a.block_table[(size_t)r * a.max_pages + j];
+
+  // the page of hold e; -1 outside the cache
+  auto page_of = [&](int e) {
+    int lo = 0, hi = a.R - 1;  // the last request whose first hold is at or before e
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first[mid] <= e) lo = mid;
+      else hi = mid - 1;
+    }
+    const int page = a.block_table[(size_t)lo * a.max_pages + (e - first[lo])];
     return page >= 0 && page < a.n_pages ? page : -1;
   };
+  const int threads = ctas * THREADS, thread = cta * THREADS + tid;
+  const int per = (int)((all + threads - 1) / threads);
+  const int e0 = (int)min((long long)thread * per, all), n = (int)min((long long)per, all - e0);
+  int kept[KEPT];
+#pragma unroll
+  for (int i = 0; i < KEPT; ++i) kept[i] = i < n ? page_of(e0 + i) : -1;
+  auto each = [&](auto &&f) {
+#pragma unroll
+    for (int i = 0; i < KEPT; ++i)
+      if (i < n) f(e0 + i, kept[i]);
+    for (int i = KEPT; i < n; ++i) f(e0 + i, page_of(e0 + i));
+  };
 
-  for (int r = warp; r < a.R; r += warps) {
-    const int n = first[r + 1] - first[r];
-    for (int j = lane; j < n; j += 32) {
-      const int page = page_at(r, j);
-      if (page < 0) {
-        dspark_set_status(DSPARK_ERR_PAGES);
-      } else if (atomicSub(&a.refs[page], 1) < 0) {  // more holds than were counted
-        atomicAdd(&a.refs[page], 1);
-        dspark_set_status(DSPARK_ERR_PAGES);
-      }
+  each([&](int, int page) {
+    if (page < 0) {
+      dspark_set_status(DSPARK_ERR_PAGES);
+    } else if (atomicSub(&a.refs[page], 1) < 0) {  // more holds than were counted
+      atomicAdd(&a.refs[page], 1);
+      dspark_set_status(DSPARK_ERR_PAGES);
     }
-  }
+  });
   __threadfence();
   sync_all(ctas);
-  for (int r = warp; r < a.R; r += warps) {
-    const int e = first[r], n = first[r + 1] - e;
-    for (int j = lane; j < n; j += 32) {
-      const int page = page_at(r, j);
-      if (page >= 0 && __ldcg(&a.refs[page]) < 0) atomicMin(&a.refs[page], -(e + j) - 2);
-    }
-  }
-  __threadfence();
-  sync_all(ctas);
-  // how many each request gives back, by way of held
-  for (int r = warp; r < a.R; r += warps) {
-    const int e = first[r], n = first[r + 1] - e;
-    if (n == 0) continue;
-    int count = 0;
-    for (int j = lane; j < n; j += 32) {
-      const int page = page_at(r, j);
-      count += page >= 0 && __ldcg(&a.refs[page]) == -(e + j) - 2;
-    }
-    count = __reduce_add_sync(0xffffffffu, count);
-    if (lane == 0) __stcg(&a.held[r], count);
-  }
+  each([&](int e, int page) {
+    if (page >= 0 && __ldcg(&a.refs[page]) < 0) atomicMin(&a.refs[page], -e - 2);
+  });
+  for (int r = thread; r < a.R; r += threads)  // every CTA has read held
+    if (first[r + 1] > first[r]) a.held[r] = 0;
   __threadfence();
   sync_all(ctas);
   mine = 0;
-  for (int r = r0; r < r1; ++r) {
-    pushed[r] = first[r + 1] > first[r] ? __ldcg(&a.held[r]) : 0;
-    mine += pushed[r];
-  }
-  at = block_scan(mine, all, warp_sums);
-  for (int r = r0; r < r1; ++r) {
-    const int n = pushed[r];
-    pushed[r] = (int)at;
-    at += n;
-  }
-  __syncthreads();
-  sync_all(ctas);  // every CTA has read held
-  for (int r = warp; r < a.R; r += warps) {
-    const int e = first[r], n = first[r + 1] - e;
-    if (n == 0) continue;
-    long long to = (long long)top + pushed[r];
-    for (int j0 = 0; j0 < n; j0 += 32) {
-      const int j = j0 + lane, page = j < n ? page_at(r, j) : -1;
-      const bool goes = page >= 0 && __ldcg(&a.refs[page]) == -(e + j) - 2;
-      const uint32_t by = __ballot_sync(0xffffffffu, goes);
-      const long long mine_at = to + __popc(by & ((1u << lane) - 1));
-      if (goes) {
-        __stcg(&a.refs[page], 0);
-        if (mine_at < a.n_pages) a.free_pages[mine_at] = page;
-      }
-      to += __popc(by);
+  each([&](int e, int page) { mine += page >= 0 && __ldcg(&a.refs[page]) == -e - 2; });
+  at = top + block_scan(mine, all, warp_sums);
+  if (ctas > 1) {
+    cg::cluster_group cluster = cg::this_cluster();
+    if (tid < ctas) *cluster.map_shared_rank(&counts[cta], tid) = (int)all;
+    cluster.sync();
+    all = 0;
+    for (int i = 0; i < ctas; ++i) {
+      if (i < cta) at += counts[i];
+      all += counts[i];
     }
-    if (lane == 0) a.held[r] = 0;
   }
-  if (cta == 0 && tid == 0) {
+  each([&](int e, int page) {
+    if (page >= 0 && __ldcg(&a.refs[page]) == -e - 2) {
+      __stcg(&a.refs[page], 0);
+      if (at < a.n_pages) a.free_pages[at] = page;
+      ++at;
+    }
+  });
+  if (thread == 0) {
     if (top + all > a.n_pages) dspark_set_status(DSPARK_ERR_PAGES);
     a.n_free[0] = (int)min(top + all, (long long)a.n_pages);
   }
@@ -546,9 +534,9 @@ extern "C" int dspark_kv_release(int32_t R, int32_t n_pages, int32_t max_pages, 
   a.free_pages = free_pages;
   a.refs = refs;
   static DsparkPerDevice once;
-  if (!allow_smem(once, kv_release_kernel, (2 * MAX_R + 1) * (int)sizeof(int)))
+  if (!allow_smem(once, kv_release_kernel, (MAX_R + 1) * (int)sizeof(int)))
     return DSPARK_ERR_CUDA;
-  return launch_tables(kv_release_kernel, a, R <= WARPS, (2 * (size_t)R + 1) * sizeof(int), stream);
+  return launch_tables(kv_release_kernel, a, R <= WARPS, ((size_t)R + 1) * sizeof(int), stream);
 }
 
 extern "C" int dspark_kv_squeeze(int32_t R, int32_t n_pages, int32_t max_pages,
