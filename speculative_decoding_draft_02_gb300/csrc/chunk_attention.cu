@@ -158,6 +158,7 @@ extern "C" int dspark_chunk_attention(const dspark_kv_cache *cache, int32_t R, i
   a.out = (bf16 *)out;
   a.out_row = out_row_stride;
   a.out_head = out_head_stride;
+  a.wide = ((uintptr_t)out & 31) == 0 && out_row_stride % 16 == 0 && out_head_stride % 16 == 0;
   a.lse = lse;
   a.part_o = (float4 *)workspace;
   a.part_ml = (float *)((uint8_t *)workspace + at.ml);

@@ -68,6 +68,7 @@ struct Args {
   float scale;
   bf16 *out;
   int64_t out_row, out_head;
+  int wide;                             // every row of out begins at a multiple of 32 bytes
   float *lse;
   float4 *part_o;                       // [ctas][2][D / 4][2 BM]
   float *part_ml;                       // [ctas][2][2][2 BM]
@@ -249,6 +250,13 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
       : "memory");
 }
 
+// 32 bytes, aligned to as many.
+__device__ __forceinline__ void store32(bf16 *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                        uint32_t e, uint32_t f, uint32_t g, uint32_t h) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b),
+               "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
+               : "memory");
+}
 // Of a row of Q beside an 8-bit cache: the power of two that it was multiplied by, from
 // its largest value's exponent (0 for a row of zeros).
 __device__ __forceinline__ int row_exponent(int e) { return e ? 14 + 127 - e : 0; }
@@ -883,19 +891,60 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
         if (whole && mine && a.lse)
           a.lse[row * a.heads * a.group + head] = (log2f(sum) - nm) * LN2;
         bf16 *const dst = a.out + row * a.out_row + head * a.out_head;
-        unsigned any = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) any |= n->odd[i];
+        // Two lanes write 64 bytes of one row together, of the even lane's and then of the
+        // odd lane's: an SM writes a line's sectors one line at a time (a lane 16 bytes
+        // of its own row: 32 prompts of 256 rows 56 us, a batch of 12 requests 69; 32
+        // bytes: 51 and 63).
+        const bool odd_lane = lane & 1;
+        const unsigned there = __ballot_sync(0xffffffffu, mine) >> (lane & 30);
+        bf16 *const even =
+            reinterpret_cast<bf16 *>(__shfl_sync(
+                0xffffffffu, reinterpret_cast<unsigned long long>(dst), lane & 30)) + 16 * odd_lane;
+        bf16 *const odd =
+            reinterpret_cast<bf16 *>(__shfl_sync(
+                0xffffffffu, reinterpret_cast<unsigned long long>(dst), lane | 1)) + 16 * odd_lane;
+        // rolled: it is fetched anew at every item's end
 #pragma unroll 1
         for (int d = 0; d < D; d += 32) {
           uint32_t o[32];
           tc::tmem_ld32(to + d, o);
           tc::tmem_wait_ld();
           tc::reg_fence(o);
-          float v[32];
+          if (whole) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * f;
-          if (any) {
+            for (int j = 0; j < 16; ++j)
+              o[j] = pack_bf16(__uint_as_float(o[2 * j]) * f, __uint_as_float(o[2 * j + 1]) * f);
+            if (a.wide) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const uint32_t got =
+                    __shfl_xor_sync(0xffffffffu, odd_lane ? o[j] : o[8 + j], 1);
+                if (odd_lane) o[j] = got;
+                else o[8 + j] = got;
+              }
+              if (there & 1) store32(even + d, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
+              if (there & 2) store32(odd + d, o[8], o[9], o[10], o[11], o[12], o[13], o[14], o[15]);
+            } else if (mine) {
+#pragma unroll
+              for (int j = 0; j < 16; j += 4)
+                *reinterpret_cast<uint4 *>(dst + d + 2 * j) =
+                    make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+            }
+          } else if (mine) {
+            float4 *po = a.part_o + (slot * (D / 4) + d / 4) * 2 * BM + x * BM + m;
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              po[(j / 4) * 2 * BM] =
+                  make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]),
+                              __uint_as_float(o[j + 2]), __uint_as_float(o[j + 3]));
+          }
+        }
+        unsigned any = 0;
+        for (int i = 0; i < 8; ++i) any |= n->odd[i];
+        if (any) {  // infinities and NaN, to the rows that see them
+          __syncwarp();  // the row is written, by two lanes
+          if (mine) {
+            float *po = reinterpret_cast<float *>(a.part_o + slot * (D / 4) * 2 * BM + x * BM + m);
 #pragma unroll 1
             for (int at = 1; at <= node - n->node0 && at < n->nodes; ++at) {
               if (!(n->odd[at >> 5] >> (at & 31) & 1)) continue;
@@ -905,29 +954,20 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
               const uint8_t *src = a.v + page * a.page_bytes +
                                    (pos & ((1 << a.page_shift) - 1)) * a.token_bytes +
                                    n->h * a.head_bytes;
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
+#pragma unroll 1
+              for (int d = 0; d < D; ++d) {
                 float y;
                 if constexpr (G::FP8)
-                  y = (src[d + j] & 0x7f) == 0x7f ? NAN : 0.0f;
+                  y = (src[d] & 0x7f) == 0x7f ? NAN : 0.0f;
                 else
-                  y = __bfloat162float(reinterpret_cast<const bf16 *>(src)[d + j]);
-                if (!(fabsf(y) < INFINITY)) v[j] += y;
+                  y = __bfloat162float(reinterpret_cast<const bf16 *>(src)[d]);
+                if (fabsf(y) < INFINITY) continue;
+                if (whole)
+                  dst[d] = __float2bfloat16_rn(__bfloat162float(dst[d]) + y);
+                else
+                  po[(d / 4) * 8 * BM + d % 4] += y;
               }
             }
-          }
-          if (!mine) continue;
-          if (whole) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 8)
-              *reinterpret_cast<uint4 *>(dst + d + j) =
-                  make_uint4(pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]),
-                             pack_bf16(v[j + 4], v[j + 5]), pack_bf16(v[j + 6], v[j + 7]));
-          } else {
-            float4 *po = a.part_o + (slot * (D / 4) + d / 4) * 2 * BM + x * BM + m;
-#pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              po[(j / 4) * 2 * BM] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
           }
         }
         tc::fence_before_sync();
