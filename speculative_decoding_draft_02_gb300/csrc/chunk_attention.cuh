@@ -96,10 +96,6 @@ struct Geo {
   static constexpr int SMEM_BYTES = (KS + VS) * PLACE + Q_BYTES + CTL_BYTES;
   static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory");
   static constexpr uint32_t TMEM_COLS = 512;  // S_0, S_1, O_0, O_1
-  // Whether O's product begins with half of P.  At 64 columns the softmax is the longer
-  // part (eight chunks of 4096 rows: 1727 us with it, 1812 without); at 128 it changed
-  // nothing (378), and beside an 8-bit cache it cost 8% (604 and 554 us, long contexts).
-  static constexpr bool HALVED = !FP8 && D == 64;
 };
 
 // A request as the kernel takes it: every later index is in bounds by this.
@@ -152,17 +148,22 @@ __device__ __forceinline__ bool before(const Place &a, const Place &b) {
 }
 
 // Where cost `off` of request r's own lies: both CTAs beside a cut find the same place.
+// By a warp.
 __device__ __forceinline__ Place locate(const Args &a, const Request &q, int r, long long off) {
+  const int lane = threadIdx.x & 31;
   Place p;
   p.r = r;
   const long long each = q.upto(a, q.items);
   p.h = attn::quotient(off, each);
   off -= p.h * each;
-  int lo = 0, hi = q.items - 1;  // the last item that begins at or before off
-  while (lo < hi) {
-    const int mid = (int)(((long long)lo + hi + 1) >> 1);
-    if (q.upto(a, mid) <= off) lo = mid;
-    else hi = mid - 1;
+  int lo = 0;  // the last item that begins at or before off, 32 candidates at a time
+  for (int n = q.items; n > 1;) {
+    const int step = (int)(((uint32_t)n + 31) >> 5), at = lane * step;
+    const uint32_t by =
+        __ballot_sync(0xffffffffu, (long long)lane * step < n && q.upto(a, lo + at) <= off);
+    const int k = 31 - __clz(by);  // the first one always does
+    lo += k * step;
+    n = min(step, n - k * step);
   }
   p.item = lo;
   const long long in = off - q.upto(a, lo) - OVERHEAD;
@@ -194,14 +195,15 @@ struct Ctl {
   uint64_t k_full[MAX_SLOTS], k_empty[MAX_SLOTS], v_full[MAX_SLOTS], v_empty[MAX_SLOTS];
   uint64_t v_ready[MAX_SLOTS];          // and nothing in V that must not be met
   uint64_t kr_full[MAX_SLOTS], vr_full[MAX_SLOTS];  // 8-bit tiles as they were copied
-  // by tile of Q: copied; in f16 (8 bits); its last S issued; S, half of P, P and the item's
-  // O complete
-  uint64_t q_full[2], q_ready[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], drain;
+  // by tile of Q: copied; in f16 (8 bits); its last S issued; S, P and the item's O complete
+  uint64_t q_full[2], q_ready[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
   uint64_t seg_full[SEGS], seg_empty[SEGS];
   long long sums[16];
+  // the share's first place and the one behind its last: their request, and the cost in it
+  Request cut_q[2];
+  long long cut_off[2];
+  int cut_r[2];
   Place first, last;
-  Request first_q;  // the request first_r as it was read
-  int first_r;
   alignas(16) Segment seg[SEGS];
   int tail[5], head;
   int abort;
@@ -293,7 +295,6 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
       tc::mbar_init(&ctl->q_ready[x], 4);
       tc::mbar_init(&ctl->q_empty[x], 1);
       tc::mbar_init(&ctl->s_full[x], 1);
-      tc::mbar_init(&ctl->p_half[x], 4);
       tc::mbar_init(&ctl->p_full[x], 4);
       tc::mbar_init(&ctl->o_full[x], 1);
     }
@@ -337,40 +338,49 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    long long all = 0, below = upto - mine;
-    for (int w = 0; w < G::THREADS / 32; ++w) {
-      all += ctl->sums[w];
-      if (w < warp) below += ctl->sums[w];
+    // of all warps, and of those before this one
+    long long all = lane < G::THREADS / 32 ? ctl->sums[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, all, o);
+      if (lane >= o) all += t;
     }
+    const long long warps_before = __shfl_sync(0xffffffffu, all, max(warp - 1, 0));
+    const long long below = (warp ? warps_before : 0) + upto - mine;
+    all = __shfl_sync(0xffffffffu, all, 31);
     const int shares = all >= (long long)MIN_SHARE * gridDim.x ? gridDim.x
                                                                 : max((int)all / MIN_SHARE, 1);
-    const long long share = attn::divide_small(all, (uint32_t)shares), longer = all - share * shares;
-    if (threadIdx.x == 0) {
-      const Place end = {a.R, 0, 0, 0};
-      ctl->first = ctl->last = end;
-      ctl->first_r = -1;
-    }
-    __syncthreads();
-    // the thread whose requests a cut lies in finds its place; the last cut is the end
+    const long long share = all >> 32 ? attn::divide_small(all, (uint32_t)shares)
+                                      : (uint32_t)all / (uint32_t)shares;
+    const long long longer = all - share * shares;
+    // the thread whose requests a cut lies in says which one; the last cut is the end
+#pragma unroll
     for (int side = 0; side < 2; ++side) {
       const int cut = cta + side;
-      if (cut >= shares) break;
       const long long u = cut * share + min((long long)cut, longer);
-      if (mine > 0 && below <= u && u < below + mine) {
+      if (threadIdx.x == 0 && (cut >= shares || u >= all)) ctl->cut_r[side] = -1;
+      if (cut < shares && mine > 0 && below <= u && u < below + mine) {
         long long off = u - below;
         int r = r_lo;
-        for (;; ++r) {
-          q.set(a, a.ctx[r], a.row_start[r], a.row_start[r + 1]);
-          const long long m = q.upto(a, q.items) * a.heads;
-          if (off < m) break;
-          off -= m;
+        if (per > 1) {
+          for (;; ++r) {
+            q.set(a, a.ctx[r], a.row_start[r], a.row_start[r + 1]);
+            const long long m = q.upto(a, q.items) * a.heads;
+            if (off < m) break;
+            off -= m;
+          }
         }
-        (side ? ctl->last : ctl->first) = locate(a, q, r, off);
-        if (side == 0) {
-          ctl->first_q = q;
-          ctl->first_r = r;
-        }
+        ctl->cut_r[side] = r;
+        ctl->cut_off[side] = off;
+        ctl->cut_q[side] = q;
       }
+    }
+    __syncthreads();
+    if (warp < 2) {
+      const int r = ctl->cut_r[warp];
+      Place p = {a.R, 0, 0, 0};
+      if (r >= 0) p = locate(a, ctl->cut_q[warp], r, ctl->cut_off[warp]);
+      if (lane == 0) (warp ? ctl->last : ctl->first) = p;
     }
     __syncthreads();
   }
@@ -387,8 +397,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
     bool ok = true;
     Place p = ctl->first;
     const Place last = ctl->last;
-    Request q = ctl->first_q;
-    int known = ctl->first_r;
+    Request q = ctl->cut_q[0];
+    int known = ctl->cut_r[0];
     for (int published = 0; ok; ++published) {
       while (before(p, last) && known != p.r) {
         q.set(a, a.ctx[p.r], a.row_start[p.r], a.row_start[p.r + 1]);
@@ -503,10 +513,10 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
       int k, count, tiles;        // tiles of the segment taken; that this stream meets; all
       int k_slot, v_slot;
       uint32_t k_phase, v_phase;
-      bool s_out, half, open, over;  // S is issued, its O is next; half of it is issued
+      bool s_out, open, over;     // s_out: S is issued, its O is next
     } st[2];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) st[x] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, false, false, false, false};
+    for (int x = 0; x < 2; ++x) st[x] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, false, false, false};
     auto ready = [&](uint64_t *bar, uint32_t parity) {
       return __all_sync(0xffffffffu, tc::mbar_test(bar, parity)) != 0;
     };
@@ -549,29 +559,16 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
         }
         if (s.s_out) {
           // O of tile k
+          if (!ready(&ctl->p_full[x], s.done & 1) || !ready(&ctl->v_ready[s.v_slot], s.v_phase))
+            continue;
+          did = true;
+          tc::fence_after_sync();
           const uint64_t vd =
               tc::smem_desc_sw128_mn(sv + s.v_slot * G::PLACE, D == 128 ? HALF_BYTES : 0);
-          if (!s.half) {
-            if (!ready(G::HALVED ? &ctl->p_half[x] : &ctl->p_full[x], s.done & 1) ||
-                !ready(&ctl->v_ready[s.v_slot], s.v_phase))
-              continue;
-            did = true;
-            tc::fence_after_sync();
 #pragma unroll
-            for (int k = 0; k < BT / 32; ++k)
-              umma_ts_warp(tmem_o + x * D, tmem + x * BT + 8 * k, vd + 128 * k, idesc_o,
-                           s.k > 0 || k != 0);
-            s.half = true;
-          }
-          if (G::HALVED) {
-            if (!ready(&ctl->p_full[x], s.done & 1)) continue;
-            did = true;
-            tc::fence_after_sync();
-          }
-#pragma unroll
-          for (int k = BT / 32; k < BT / 16; ++k)
-            umma_ts_warp(tmem_o + x * D, tmem + x * BT + 8 * k, vd + 128 * k, idesc_o, 1);
-          s.half = false;
+          for (int k = 0; k < BT / 16; ++k)
+            umma_ts_warp(tmem_o + x * D, tmem + x * BT + 8 * k, vd + 128 * k, idesc_o,
+                         s.k > 0 || k != 0);
           tc::umma_commit_warp(&ctl->v_empty[s.v_slot]);
           if (s.k + 1 == s.count) tc::umma_commit_warp(&ctl->o_full[x]);
           next_v(s);
@@ -844,12 +841,6 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
             }
           }
           tmem_st8(ts + 8 * j, pk);  // two weights a column
-          if (G::HALVED && j == 3) {  // the product may begin
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&ctl->p_half[x]);
-          }
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
@@ -1108,18 +1099,23 @@ __global__ void __launch_bounds__(BM) chunk_attention_join(const __grid_constant
   pdl_wait();
   const int c = blockIdx.x, x = blockIdx.y, d0 = blockIdx.z * 32, m = threadIdx.x;
   const int *desc = a.desc + c * 8;
+  const int lane = m & 31;
+  // piece 0 is CTA c's last one, piece k > 0 CTA (c + k)'s first: up to the first CTA whose
+  // piece ends the item
+  int heads_here = c + 1 + lane < (int)gridDim.x ? a.desc[(c + 1 + lane) * 8 + 5] : 2;
   if (desc[0] == 0) return;
-  const int node = m / a.group, g = m - node * a.group, ctas = gridDim.x;
+  int pieces = 1;
+  for (int k = 0;; k += 32) {
+    const uint32_t ends = __ballot_sync(0xffffffffu, heads_here != 1);
+    if (ends) {
+      pieces += k + __ffs((int)ends);
+      break;
+    }
+    heads_here = c + 33 + k + lane < (int)gridDim.x ? a.desc[(c + 33 + k + lane) * 8 + 5] : 2;
+  }
+  const int node = m / a.group, g = m - node * a.group;
   const int in_item = x * a.nodes_tile + node;
   if (node >= a.nodes_tile || in_item >= desc[3]) return;
-  // piece 0 is CTA c's last one, piece k > 0 CTA (c + k)'s first
-  int pieces = 1;
-  while (c + pieces < ctas) {
-    const int head = a.desc[(c + pieces) * 8 + 5];
-    if (head == 0) break;
-    ++pieces;
-    if (head == 2) break;
-  }
   auto at = [&](int k) -> size_t { return k ? 2 * (size_t)(c + k) : 2 * (size_t)c + 1; };
   float top = -INFINITY;
   for (int k = 0; k < pieces; ++k) top = fmaxf(top, a.part_ml[at(k) * 4 * BM + x * BM + m]);
