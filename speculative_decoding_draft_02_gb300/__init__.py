@@ -158,13 +158,15 @@ def _ptr(t: Optional[torch.Tensor]):
 
 # The current stream's handle without making a Stream object (3 us of a 3 us launch).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None)
+_initialized = torch.cuda.is_initialized
 
 
 def _stream(stream: Optional[torch.cuda.Stream]):
     if stream is not None:
         return stream.cuda_stream
-    if _raw_stream is not None and torch.cuda.is_initialized():
-        return _raw_stream(torch._C._cuda_getDevice())
+    if _raw_stream is not None and _initialized():
+        return _raw_stream(_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -354,12 +356,30 @@ def _rows_view(what: str, name: str, t, heads, dim):
     return t.data_ptr(), shape[0], row, head
 
 
+def _heads_view(what: str, name: str, t, dim):
+    """_rows_view for any number of heads: (address, rows, heads, row stride, head stride)."""
+    try:
+        (rows, heads, width), (row, head, one) = t.shape, t.stride()
+        if t.dtype is torch.bfloat16 and width == dim and one == 1 and t.is_cuda:
+            return (t.data_ptr(), rows, heads, row if rows > 1 else dim,
+                    head if heads > 1 else dim)
+    except AttributeError:
+        raise DSparkError(f"{what}: {name} must be a tensor") from None
+    except ValueError:
+        pass
+    raise DSparkError(f"{what}: {name} must be bfloat16 [rows, heads, {dim}] on the GPU with a dense "
+                      "last dimension")
+
+
 def _size(what: str, name: str, t, dims: int):
     """A tensor's shape, of so many dimensions."""
-    shape = getattr(t, "shape", ())
-    if len(shape) != dims:
-        raise DSparkError(f"{what}: {name} must have {dims} dimensions")
-    return shape
+    try:
+        shape = t.shape
+        if len(shape) == dims:
+            return shape
+    except AttributeError:
+        pass
+    raise DSparkError(f"{what}: {name} must have {dims} dimensions")
 
 
 def _masks(what: str, anc, rows: int):
@@ -512,17 +532,18 @@ def dspark_rope_append(cache: KVCache, q, k, v, position, slot, rotary: Rotary, 
                        q_weight=None, k_weight=None, eps=1e-6, stream=None):
     """q, q_out bf16 [rows, heads_q, dim], k, v bf16 [rows, heads, dim] (k and v of equal
     strides); weights bf16 [dim] or None (no norm of that side).  q_out may be q."""
-    what = "dspark_rope_append"
-    heads_q = _size(what, "q", q, 3)[1]
-    qp, rows, q_row, q_head = _rows_view(what, "q", q, heads_q, cache.dim)
-    kp, *rest = _rows_view(what, "k", k, cache.heads, cache.dim)
-    vp, *also = _rows_view(what, "v", v, cache.heads, cache.dim)
-    op, o_rows, o_row, o_head = _rows_view(what, "q_out", q_out, heads_q, cache.dim)
+    what, dim = "dspark_rope_append", cache.dim
+    qp, rows, heads_q, q_row, q_head = _heads_view(what, "q", q, dim)
+    kp, *rest = _heads_view(what, "k", k, dim)
+    vp, *also = _heads_view(what, "v", v, dim)
+    op, o_rows, o_heads, o_row, o_head = _heads_view(what, "q_out", q_out, dim)
     if rest != also or rest[0] != rows or o_rows != rows:
         raise DSparkError(f"{what}: q, k, v and q_out must have equal rows, k and v equal strides")
-    bf16, width = torch.bfloat16, (cache.dim,)
+    if rest[1] != cache.heads or o_heads != heads_q:
+        raise DSparkError(f"{what}: k and v must have the cache's heads, q_out q's")
+    bf16, width = torch.bfloat16, (dim,)
     _check(load_library().dspark_rope_append(
-        cache.ref, rows, heads_q, qp, q_row, q_head, kp, vp, rest[1], rest[2],
+        cache.ref, rows, heads_q, qp, q_row, q_head, kp, vp, rest[2], rest[3],
         None if q_weight is None else _want(what, "q_weight", q_weight, bf16, width),
         None if k_weight is None else _want(what, "k_weight", k_weight, bf16, width), eps,
         rotary.ref, _want(what, "position", position, torch.int32, (rows,)),
@@ -538,11 +559,11 @@ def dspark_chunk_attention(cache: KVCache, q, ctx, row_start, block_table, max_r
                            lse, workspace, stream=None):
     """q, out bf16 [rows, heads_q, dim] (views with a dense last dimension); lse may be None."""
     what, i32 = "dspark_chunk_attention", torch.int32
-    R, heads_q = len(ctx), _size(what, "q", q, 3)[1]
-    qp, rows, q_row, q_head = _rows_view(what, "q", q, heads_q, cache.dim)
-    op, o_rows, o_row, o_head = _rows_view(what, "out", out, heads_q, cache.dim)
-    if o_rows != rows:
-        raise DSparkError(f"{what}: out must have q's rows")
+    qp, rows, heads_q, q_row, q_head = _heads_view(what, "q", q, cache.dim)
+    op, o_rows, o_heads, o_row, o_head = _heads_view(what, "out", out, cache.dim)
+    if o_rows != rows or o_heads != heads_q:
+        raise DSparkError(f"{what}: out must have q's rows and heads")
+    R = _size(what, "ctx", ctx, 1)[0]
     pages = _size(what, "block_table", block_table, 2)[1]
     _check(load_library().dspark_chunk_attention(
         cache.ref, R, heads_q, max_rows, rows, pages, qp, q_row, q_head,
@@ -556,7 +577,8 @@ def dspark_kv_fork(source, target, page_size, ctx, held, n_free, free_pages, blo
                    copy_from, copy_to, copy_tokens, stream=None):
     """Writes ctx, held, n_free, block_table and refs in place."""
     what, i32 = "dspark_kv_fork", torch.int32
-    n, R, pages = len(source), len(ctx), len(free_pages)
+    (n,), (R,) = _size(what, "source", source, 1), _size(what, "ctx", ctx, 1)
+    pages = _size(what, "free_pages", free_pages, 1)[0]
     table = _size(what, "block_table", block_table, 2)
     _check(load_library().dspark_kv_fork(
         n, _want(what, "source", source, i32, (n,)), _want(what, "target", target, i32, (n,)), R,
@@ -572,7 +594,7 @@ def dspark_kv_fork(source, target, page_size, ctx, held, n_free, free_pages, blo
 def dspark_kv_release(ctx, held, n_free, free_pages, block_table, refs, stream=None):
     """Writes held, n_free, free_pages and refs in place."""
     what, i32 = "dspark_kv_release", torch.int32
-    R, pages = len(ctx), len(free_pages)
+    (R,), (pages,) = _size(what, "ctx", ctx, 1), _size(what, "free_pages", free_pages, 1)
     table = _size(what, "block_table", block_table, 2)
     _check(load_library().dspark_kv_release(
         R, pages, table[1], _want(what, "ctx", ctx, i32, (R,)), _want(what, "held", held, i32, (R,)),
@@ -587,7 +609,7 @@ def dspark_kv_squeeze(held, n_free, free_pages, block_table, refs, free_pages_ou
     """move_from and move_to have half as many entries as there are pages; the *_out tensors
     may be the inputs."""
     what, i32 = "dspark_kv_squeeze", torch.int32
-    R, pages = len(held), len(free_pages)
+    (R,), (pages,) = _size(what, "held", held, 1), _size(what, "free_pages", free_pages, 1)
     table = _size(what, "block_table", block_table, 2)
     shape, half = (R, table[1]), (pages // 2,)
     _check(load_library().dspark_kv_squeeze(
@@ -607,7 +629,7 @@ def dspark_kv_squeeze(held, n_free, free_pages, block_table, refs, free_pages_ou
 def dspark_kv_copy(cache: KVCache, copy_from, copy_to, copy_tokens=None, stream=None):
     """copy_tokens None: whole pages."""
     what, i32 = "dspark_kv_copy", torch.int32
-    n = len(copy_from)
+    n = _size(what, "copy_from", copy_from, 1)[0]
     _check(load_library().dspark_kv_copy(
         cache.ref, n, _want(what, "copy_from", copy_from, i32, (n,)),
         _want(what, "copy_to", copy_to, i32, (n,)),
