@@ -558,7 +558,7 @@ size_t dspark_chunk_attention_workspace_bytes(const dspark_kv_cache *cache, int3
  * Scores, statistics and sums in f32.  Beside a bf16 cache a weight meets V as one bf16
  * (8 bits; the sum of the weights takes it unrounded); beside an 8-bit one weights and q
  * are f16 as in dspark_tree_attention, with a power of two for every row and head of q.
- * Where no request has more than DSPARK_MAX_NODES rows the call may be
+ * With few rows (max_rows times the query heads of a KV head at most 32) the call is
  * dspark_tree_attention's, with that call's precision. */
 int dspark_chunk_attention(const dspark_kv_cache *cache, int32_t R, int32_t heads_q,
                            int32_t max_rows, int32_t n_rows, int32_t max_pages, const void *q,
@@ -597,8 +597,8 @@ int dspark_kv_fork(int32_t n, const int32_t *source, const int32_t *target, int3
 /* The pages of every request that has left (ctx < 0): each gives up its hold, and a page
  * that nobody holds any more goes back to the stack, request by request and in block
  * order, a page with several holders that leave together in the place of the last of
- * them.  held becomes 0.  Tables are left as they are.  A table entry outside the cache, or a page with
- * more holders than refs says, sets DSPARK_ERR_PAGES.  R <= 16384. */
+ * them.  held becomes 0.  Tables are left as they are.  A table entry outside the cache,
+ * or a page with more holders than refs says, sets DSPARK_ERR_PAGES.  R <= 16384. */
 int dspark_kv_release(int32_t R, int32_t n_pages, int32_t max_pages, const int32_t *ctx,
                       int32_t *held, int32_t *n_free, int32_t *free_pages,
                       const int32_t *block_table, int32_t *refs, dspark_stream_t stream);

@@ -170,6 +170,14 @@ def _stream(stream: Optional[torch.cuda.Stream]):
     return torch.cuda.current_stream().cuda_stream
 
 
+def _stream_on(what: str, t: torch.Tensor, stream):
+    """_stream, once the current device is the tensor's: a launch goes there."""
+    if t.get_device() != _device():
+        raise DSparkError(f"{what}: the tensors are on device {t.get_device()}, which is not the "
+                          "current one")
+    return _stream(stream)
+
+
 def _bf16(t: torch.Tensor) -> torch.Tensor:
     return t if t.dtype == torch.bfloat16 else t.to(torch.bfloat16)
 
@@ -367,8 +375,8 @@ def _heads_view(what: str, name: str, t, dim):
         raise DSparkError(f"{what}: {name} must be a tensor") from None
     except ValueError:
         pass
-    raise DSparkError(f"{what}: {name} must be bfloat16 [rows, heads, {dim}] on the GPU with a dense "
-                      "last dimension")
+    raise DSparkError(f"{what}: {name} must be bfloat16 [rows, heads, {dim}] on the GPU with a "
+                      "dense last dimension")
 
 
 def _size(what: str, name: str, t, dims: int):
@@ -547,7 +555,8 @@ def dspark_rope_append(cache: KVCache, q, k, v, position, slot, rotary: Rotary, 
         None if q_weight is None else _want(what, "q_weight", q_weight, bf16, width),
         None if k_weight is None else _want(what, "k_weight", k_weight, bf16, width), eps,
         rotary.ref, _want(what, "position", position, torch.int32, (rows,)),
-        _want(what, "slot", slot, torch.int64, (rows,)), op, o_row, o_head, _stream(stream)), what)
+        _want(what, "slot", slot, torch.int64, (rows,)), op, o_row, o_head,
+        _stream_on(what, q, stream)), what)
 
 
 def dspark_chunk_attention_workspace_bytes(cache: KVCache, R, heads_q, max_rows) -> int:
@@ -570,7 +579,7 @@ def dspark_chunk_attention(cache: KVCache, q, ctx, row_start, block_table, max_r
         _want(what, "ctx", ctx, i32, (R,)), _want(what, "row_start", row_start, i32, (R + 1,)),
         _want(what, "block_table", block_table, i32, (R, pages)), scale, op, o_row, o_head,
         None if lse is None else _want(what, "lse", lse, torch.float32, (rows, heads_q)),
-        _ptr(workspace), workspace.numel(), _stream(stream)), what)
+        _ptr(workspace), workspace.numel(), _stream_on(what, q, stream)), what)
 
 
 def dspark_kv_fork(source, target, page_size, ctx, held, n_free, free_pages, block_table, refs,
@@ -588,7 +597,7 @@ def dspark_kv_fork(source, target, page_size, ctx, held, n_free, free_pages, blo
         _want(what, "block_table", block_table, i32, (R, table[1])),
         _want(what, "refs", refs, i32, (pages,)), _want(what, "copy_from", copy_from, i32, (n,)),
         _want(what, "copy_to", copy_to, i32, (n,)),
-        _want(what, "copy_tokens", copy_tokens, i32, (n,)), _stream(stream)), what)
+        _want(what, "copy_tokens", copy_tokens, i32, (n,)), _stream_on(what, ctx, stream)), what)
 
 
 def dspark_kv_release(ctx, held, n_free, free_pages, block_table, refs, stream=None):
@@ -597,11 +606,11 @@ def dspark_kv_release(ctx, held, n_free, free_pages, block_table, refs, stream=N
     (R,), (pages,) = _size(what, "ctx", ctx, 1), _size(what, "free_pages", free_pages, 1)
     table = _size(what, "block_table", block_table, 2)
     _check(load_library().dspark_kv_release(
-        R, pages, table[1], _want(what, "ctx", ctx, i32, (R,)), _want(what, "held", held, i32, (R,)),
-        _want(what, "n_free", n_free, i32, (1,)),
+        R, pages, table[1], _want(what, "ctx", ctx, i32, (R,)),
+        _want(what, "held", held, i32, (R,)), _want(what, "n_free", n_free, i32, (1,)),
         _want(what, "free_pages", free_pages, i32, (pages,)),
         _want(what, "block_table", block_table, i32, (R, table[1])),
-        _want(what, "refs", refs, i32, (pages,)), _stream(stream)), what)
+        _want(what, "refs", refs, i32, (pages,)), _stream_on(what, ctx, stream)), what)
 
 
 def dspark_kv_squeeze(held, n_free, free_pages, block_table, refs, free_pages_out, block_table_out,
@@ -623,7 +632,7 @@ def dspark_kv_squeeze(held, n_free, free_pages, block_table, refs, free_pages_ou
         _want(what, "refs_out", refs_out, i32, (pages,)),
         _want(what, "new_page", new_page, i32, (pages,)),
         _want(what, "move_from", move_from, i32, half), _want(what, "move_to", move_to, i32, half),
-        _want(what, "n_moves", n_moves, i32, (1,)), _stream(stream)), what)
+        _want(what, "n_moves", n_moves, i32, (1,)), _stream_on(what, held, stream)), what)
 
 
 def dspark_kv_copy(cache: KVCache, copy_from, copy_to, copy_tokens=None, stream=None):
@@ -634,7 +643,7 @@ def dspark_kv_copy(cache: KVCache, copy_from, copy_to, copy_tokens=None, stream=
         cache.ref, n, _want(what, "copy_from", copy_from, i32, (n,)),
         _want(what, "copy_to", copy_to, i32, (n,)),
         None if copy_tokens is None else _want(what, "copy_tokens", copy_tokens, i32, (n,)),
-        _stream(stream)), what)
+        _stream_on(what, copy_from, stream)), what)
 
 
 def dspark_device_status(stream=None, clear: bool = True) -> int:

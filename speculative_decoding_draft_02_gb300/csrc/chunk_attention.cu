@@ -23,8 +23,13 @@ Layout layout_of(int ctas, int dim) {
   return l;
 }
 
-// Few rows leave the 128-row tiles empty: the tree attention has the tokens there.
-bool as_tree(int max_rows) { return max_rows <= DSPARK_MAX_NODES; }
+// Few rows leave the 128-row tiles empty: up to 32 of them (nodes x query heads of a KV
+// head) the tree attention, which has the tokens there, is the faster one.  64 requests over
+// 512 to 4096 tokens, 8 KV heads, tree and chunks: 32 rows 82 and 91 us, 64 rows 119 and 94;
+// 8 bits: 91 and 140, 186 and 143.  One request over 4000: 32 rows 22 and 29, 64 rows 26 and 29.
+bool as_tree(int max_rows, int group) {
+  return max_rows <= DSPARK_MAX_NODES && max_rows * group <= 32;
+}
 
 struct Launch {
   const dspark_kv_cache *cache;
@@ -94,7 +99,7 @@ extern "C" size_t dspark_chunk_attention_workspace_bytes(const dspark_kv_cache *
       heads_q / cache->heads > 64 || max_rows < 1)
     return 0;
   const size_t own = layout_of(dspark_sm_count(), cache->dim).bytes;
-  if (!as_tree(max_rows)) return own;
+  if (!as_tree(max_rows, heads_q / cache->heads)) return own;
   const size_t tree = dspark_tree_attention_workspace_bytes(cache, R, heads_q, max_rows);
   return own > tree ? own : tree;
 }
@@ -120,7 +125,8 @@ extern "C" int dspark_chunk_attention(const dspark_kv_cache *cache, int32_t R, i
   if (!workspace || ((uintptr_t)workspace & 255) || workspace_bytes < need)
     return DSPARK_ERR_WORKSPACE;
   const int64_t tree_out = (int64_t)1 << 24;  // the tree attention's limit
-  if (as_tree(max_rows) && out_row_stride <= tree_out && out_head_stride <= tree_out)
+  if (as_tree(max_rows, heads_q / cache->heads) && out_row_stride <= tree_out &&
+      out_head_stride <= tree_out)
     return dspark_tree_attention(cache, R, heads_q, max_rows, n_rows, max_pages, q, q_row_stride,
                                  q_head_stride, ctx, row_start, nullptr, block_table, scale, out,
                                  out_row_stride, out_head_stride, lse, workspace, workspace_bytes,

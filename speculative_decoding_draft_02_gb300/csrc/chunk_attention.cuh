@@ -748,22 +748,24 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
       const Segment *const n = &ctl->seg[seg % SEGS];
       const int tb = n->tb, count = n->count[x];
       if (tb == n->te) break;
-      float c = n->c;
       const int node = n->node0 + x * a.nodes_tile + my_node;  // of the request
       const bool mine = my_node < a.nodes_tile && x * a.nodes_tile + my_node < n->nodes;
       // tokens that this row sees, and that the tile's first row does
       const int sees = (int)min((long long)n->total, (long long)n->ctx + node + 1);
       const int all_see =
           (int)min((long long)n->total, (long long)n->ctx + n->node0 + x * a.nodes_tile + 1);
+      // a row that is none has weights of 1 and calls for nothing
+      float c = mine ? n->c : 0.0f;
       float nm = 0.0f;  // minus the reference (log2)
-      bool unset = true;
+      bool unset = mine;
       float2 l0 = {0.0f, 0.0f}, l1 = {0.0f, 0.0f};
       for (int k = 0; k < count; ++k, ++tiles_done) {
         ok = warp_wait(&ctl->s_full[x], tiles_done & 1, abort);
         if (!ok) break;
         tc::fence_after_sync();
         // the row's power of two out of its scores: known since the product is done
-        if (G::FP8 && k == 0) c = attn::times_power(c, -row_exponent(ctl->q_exp[items_done & 1][x][m]));
+        if (G::FP8 && k == 0)
+          c = attn::times_power(c, -row_exponent(ctl->q_exp[items_done & 1][x][m]));
         float2 e[64];
         {
           uint32_t s[4][32];
@@ -799,7 +801,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
 #pragma unroll
         for (int j = 0; j < 64; ++j) top[j & 3] = max3(top[j & 3], e[j].x, e[j].y);
         const float most = max3(fmaxf(top[0], top[1]), top[2], top[3]);
-        if (__any_sync(0xffffffffu, unset || most > R::RAISE)) {
+        if (__any_sync(0xffffffffu, unset || most > R::RAISE)) {  // the first tile, and rarely
           const bool fresh = unset, number = fabsf(most) < INFINITY;
           const float raise = number && (fresh || most > R::RAISE) ? most - R::PEAK : 0.0f;
           if (number) unset = false;
@@ -932,7 +934,9 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
         }
         unsigned any = 0;
         for (int i = 0; i < 8; ++i) any |= n->odd[i];
-        if (any) {  // infinities and NaN, to the rows that see them
+        // Infinities and NaN, to the rows that see them.  Asked by the warp: bits of later
+        // tokens may still come in.
+        if (__any_sync(0xffffffffu, any != 0)) {
           __syncwarp();  // the row is written, by two lanes
           if (mine) {
             float *po = reinterpret_cast<float *>(a.part_o + slot * (D / 4) * 2 * BM + x * BM + m);
@@ -983,7 +987,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
         uint4 v[D / 16];
 #pragma unroll
         for (int p = 0; p < D / 16; ++p)
-          v[p] = *reinterpret_cast<const uint4 *>(slot + G::RAW_AT + token * D + ((p ^ raw_x) * 16));
+          v[p] = *reinterpret_cast<const uint4 *>(slot + G::RAW_AT + token * D +
+                                                  ((p ^ raw_x) * 16));
 #pragma unroll
         for (int p = 0; p < D / 16; ++p) {
           const uint32_t in[4] = {v[p].x, v[p].y, v[p].z, v[p].w};

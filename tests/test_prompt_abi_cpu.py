@@ -174,3 +174,12 @@ def test_a_pool_that_shares_nothing_refuses_to():
     pool = dsp.PagePool(2, 8, 16, 64, 32, device="cpu", shared=True)
     with pytest.raises(dsp.DSparkError, match="places"):
         pool.fork(torch.zeros(3, dtype=torch.int32), torch.zeros(3, dtype=torch.int32))
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    from types import SimpleNamespace
+    monkeypatch.setattr(dsp, "_device", lambda: 1)
+    monkeypatch.setattr(dsp, "_stream", lambda stream: 77)
+    with pytest.raises(dsp.DSparkError, match="device 0"):
+        dsp._stream_on("call", SimpleNamespace(get_device=lambda: 0), None)
+    assert dsp._stream_on("call", SimpleNamespace(get_device=lambda: 1), None) == 77
