@@ -47,7 +47,10 @@ constexpr int BT = 128;             // tokens of a tile
 constexpr int BM = 128;             // rows of a tile of Q
 constexpr int SMEM_LIMIT = 232448;  // 227 KB
 constexpr int CTL_BYTES = 3 * 1024;
-constexpr int MAX_SLOTS = 4;        // of K, of V
+// Places for tiles of K and of V, each; more of them gain nothing (of V, three with 128 or
+// four with 64 columns: one prompt of 8192 rows 342 us instead of 339, 4 x 8192 rows of 64
+// columns in 8 bits 2152 instead of 2036).
+constexpr int SLOTS = 2;
 constexpr int SEGS = 4;             // segments published ahead
 // What beginning and ending an item costs, in tokens; the least share worth a CTA of its
 // own; and the least piece, in tiles, that an item is cut into.
@@ -92,8 +95,7 @@ struct Geo {
   static constexpr int SLOT = BT * D * 2, RAW_AT = D == 128 ? SLOT / 2 : SLOT;
   static constexpr int PLACE = SLOT + (FP8 && D == 64 ? BT * D : 0);
   static constexpr int Q_ONE = BM * D * 2, Q_BYTES = 2 * Q_ONE;
-  static constexpr int KS = D == 64 ? 4 : 2, VS = D == 64 ? 4 : 3;
-  static constexpr int SMEM_BYTES = (KS + VS) * PLACE + Q_BYTES + CTL_BYTES;
+  static constexpr int SMEM_BYTES = 2 * SLOTS * PLACE + Q_BYTES + CTL_BYTES;
   static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory");
   static constexpr uint32_t TMEM_COLS = 512;  // S_0, S_1, O_0, O_1
 };
@@ -192,9 +194,9 @@ struct Segment {
 };
 
 struct Ctl {
-  uint64_t k_full[MAX_SLOTS], k_empty[MAX_SLOTS], v_full[MAX_SLOTS], v_empty[MAX_SLOTS];
-  uint64_t v_ready[MAX_SLOTS];          // and nothing in V that must not be met
-  uint64_t kr_full[MAX_SLOTS], vr_full[MAX_SLOTS];  // 8-bit tiles as they were copied
+  uint64_t k_full[SLOTS], k_empty[SLOTS], v_full[SLOTS], v_empty[SLOTS];
+  uint64_t v_ready[SLOTS];          // and nothing in V that must not be met
+  uint64_t kr_full[SLOTS], vr_full[SLOTS];  // 8-bit tiles as they were copied
   // by tile of Q: copied; in f16 (8 bits); its last S issued; S, P and the item's O complete
   uint64_t q_full[2], q_ready[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
   uint64_t seg_full[SEGS], seg_empty[SEGS];
@@ -273,15 +275,15 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
   constexpr int HALVES = D / 64;        // 64-column halves of a head
   constexpr int HALF_BYTES = BT * 128;  // one half of a tile
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t *const sk = smem, *const sv = sk + G::KS * G::PLACE;
-  uint8_t *const sq = sv + G::VS * G::PLACE;
+  uint8_t *const sk = smem, *const sv = sk + SLOTS * G::PLACE;
+  uint8_t *const sq = sv + SLOTS * G::PLACE;
   Ctl *ctl = reinterpret_cast<Ctl *>(sq + G::Q_BYTES);
   volatile int *abort = &ctl->abort;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < MAX_SLOTS; ++s) {
+    for (int s = 0; s < SLOTS; ++s) {
       tc::mbar_init(&ctl->k_full[s], G::FP8 ? G::CV : 1);
       tc::mbar_init(&ctl->v_full[s], G::FP8 ? G::CV : 1);
       tc::mbar_init(&ctl->k_empty[s], 2);  // each tile of Q is done with it
@@ -479,11 +481,11 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
           }
           ++fills;
           if (kv) {
-            if (++v_slot == G::VS) {
+            if (++v_slot == SLOTS) {
               v_slot = 0;
               v_phase ^= 1;
             }
-          } else if (++k_slot == G::KS) {
+          } else if (++k_slot == SLOTS) {
             k_slot = 0;
             k_phase ^= 1;
           }
@@ -492,11 +494,11 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
     }
     // drain: every copy issued has landed
     volatile int never = 0;
-    for (int i = 0; i < G::KS; ++i)
+    for (int i = 0; i < SLOTS; ++i)
       if ((uint32_t)i < (fills + 1) / 2)
         warp_wait(G::FP8 ? &ctl->kr_full[i] : &ctl->k_full[i], i < k_slot ? k_phase : k_phase ^ 1,
                   &never);
-    for (int i = 0; i < G::VS; ++i)
+    for (int i = 0; i < SLOTS; ++i)
       if ((uint32_t)i < fills / 2)
         warp_wait(G::FP8 ? &ctl->vr_full[i] : &ctl->v_full[i], i < v_slot ? v_phase : v_phase ^ 1,
                   &never);
@@ -508,10 +510,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
     // which only the other gives back.  P hangs on its own stream alone, so that the warp
     // stays with it until it is there: the tensor pipe holds the other's products meanwhile,
     // and the next are issued sooner than by a round of polls.  A prompt of 8192 rows takes
-    // 371 -> 341 us by that, with 64 columns (4 x 8192) 1808 -> 1600, with 8 bits 2204 ->
-    // 2152; 8 bits with 128 columns, whose tiles come late out of their widening, take
-    // 2830 -> 2940, and poll P too.
-    constexpr bool STAY = !G::FP8 || D == 64;
+    // 371 -> 341 us by that, 4 x 8192 rows of 64 columns 1808 -> 1600, two chunks of 512 over
+    // 40 and 50 thousand tokens in 8 bits 562 -> 551.
     constexpr uint32_t idesc_s = G::FP8 ? tc::idesc_f16(BM, BT) : tc::idesc_bf16(BM, BT);
     constexpr uint32_t idesc_o =
         (G::FP8 ? tc::idesc_f16(BM, D) : tc::idesc_bf16(BM, D)) | tc::IDESC_B_MN;
@@ -544,13 +544,13 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
       return __all_sync(0xffffffffu, there) != 0;
     };
     auto next_k = [&](Stream &s) {
-      if (++s.k_slot == G::KS) {
+      if (++s.k_slot == SLOTS) {
         s.k_slot = 0;
         s.k_phase ^= 1;
       }
     };
     auto next_v = [&](Stream &s) {
-      if (++s.v_slot == G::VS) {
+      if (++s.v_slot == SLOTS) {
         s.v_slot = 0;
         s.v_phase ^= 1;
       }
@@ -584,12 +584,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
         if (s.s_out) {
           // O of tile k
           if (!ready(&ctl->v_ready[s.v_slot], s.v_phase)) continue;
-          if constexpr (STAY) {
-            ok = stay(&ctl->p_full[x], s.done & 1);
-            if (!ok) break;
-          } else if (!ready(&ctl->p_full[x], s.done & 1)) {
-            continue;
-          }
+          ok = stay(&ctl->p_full[x], s.done & 1);
+          if (!ok) break;
           did = true;
           tc::fence_after_sync();
           const uint64_t vd =
@@ -754,7 +750,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
         }
         __syncwarp();
         if (ok && lane == 0) tc::mbar_arrive(&ctl->v_ready[slot]);
-        if (++slot == G::VS) {
+        if (++slot == SLOTS) {
           slot = 0;
           phase ^= 1;
         }
@@ -1047,7 +1043,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
           widen(sk + k_slot * G::PLACE, &ctl->kr_full[k_slot], &ctl->k_full[k_slot], k_phase);
-          if (++k_slot == G::KS) {
+          if (++k_slot == SLOTS) {
             k_slot = 0;
             k_phase ^= 1;
           }
@@ -1098,7 +1094,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
             }
           }
           widen(sv + v_slot * G::PLACE, &ctl->vr_full[v_slot], &ctl->v_full[v_slot], v_phase);
-          if (++v_slot == G::VS) {
+          if (++v_slot == SLOTS) {
             v_slot = 0;
             v_phase ^= 1;
           }
