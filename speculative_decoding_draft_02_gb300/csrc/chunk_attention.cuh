@@ -31,6 +31,14 @@
 // to, so that as many are in flight as beside a bf16 cache.  They meet
 // Q and P in f16: each row of Q is scaled by the power of two that brings its largest
 // value to 2^14, weights are at most 2^14 and count down to 2^-24.
+//
+// What bounds it: a pair of tiles takes the tensor pipe 2048 cycles and about 2900 in
+// all, as S's product reads shared memory at its full rate while P.V, the copies and the
+// widening read and write it too.  In a graph, 32 query heads over 8 KV heads of 128:
+// one prompt of 8192 rows 336 us, 1640 TFLOP/s; eight chunks of 4096 over 4096 2400 us,
+// 1370 (the board's power); two chunks of 512 over 40 and 50 thousand tokens in 8 bits 544
+// us, 1370.  What an item's beginning and end cost counts in batches of short requests:
+// 12 of 1 to 1500 rows 63 us, 640 TFLOP/s.
 // Every wait is bounded; on expiry the CTA raises DSPARK_ERR_TIMEOUT, drains its own
 // copies and MMAs, frees TMEM and exits.
 #pragma once

@@ -57,7 +57,8 @@ struct ForkArgs {
 
 // Every CTA settles all forks for itself (which are sound, which page of the stack each
 // takes: a few KB from L2); behind one barrier the warps of all of them write.  Under a
-// MB: bound by its launch, dependent reads and the barrier.
+// MB: bound by its launch, dependent reads and the barrier (three forks 3.2 us in a graph,
+// one CTA; 480 forks of 32 prompts, 9660 holds, with their release 23 us).
 __global__ void __launch_bounds__(THREADS, 1) kv_fork_kernel(const ForkArgs a) {
   extern __shared__ int smem[];
   __shared__ long long warp_sums[WARPS];
@@ -162,7 +163,9 @@ struct ReleaseArgs {
 // consecutive ones.  Every hold takes one off its page's count, which a page that nobody
 // holds any more then shows as -1; those pages keep, as -(number + 2), the last of their
 // holds, whose place on the stack they take.  Barriers lie between; orders of atomics
-// never matter.  Bound by these steps of dependent reads.
+// never matter.  Bound by these steps of dependent reads: 2 us where nobody has left; the
+// first KEPT pages of a thread are read once (a fork and a release of 480 requests 33 -> 24 us,
+// against reading the table at each of four steps).
 __global__ void __launch_bounds__(THREADS, 1) kv_release_kernel(const ReleaseArgs a) {
   constexpr int KEPT = 4;  // pages of a thread's holds that are read once
   extern __shared__ int first[];  // [R + 1] number of a request's first hold
@@ -280,7 +283,8 @@ struct SqueezeArgs {
 
 // Free pages are marked in new_page; every warp then counts, in a stretch of pages of its
 // own, those that go (in use, U or higher) and those that take them (free, below U), and
-// by the counts of all warps before it knows their ranks.
+// by the counts of all warps before it knows their ranks.  Bound by its five barriers: 96
+// pages 6 us, 8000 pages 12 us in a graph.
 __global__ void __launch_bounds__(THREADS, 1) kv_squeeze_kernel(const SqueezeArgs a) {
   __shared__ int counts[2][CLUSTER * WARPS];  // of every warp of the cluster
   const int tid = threadIdx.x, lane = tid & 31;
@@ -395,7 +399,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_squeeze_kernel(const SqueezeArg
 
 // A block takes some tokens of one page, a thread one 16-byte column (head, part) of
 // every so many of them, K and V together: eight loads before the first store.
-// Neighbouring columns are neighbours in memory where heads are.  Bound by its bytes.
+// Neighbouring columns are neighbours in memory where heads are.  Bound by its bytes: 2010
+// pages of 32 tokens, 8 heads of 128, bf16, read and written in 83 us, 6.4 TB/s.
 constexpr int COPY_THREADS = 256, COPY_TOKENS = 4, COPY_BLOCKS_SM = 8;
 
 __global__ void __launch_bounds__(COPY_THREADS)

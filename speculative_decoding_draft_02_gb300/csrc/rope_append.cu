@@ -4,7 +4,10 @@
 //   y = x / sqrt(mean x^2 + eps) * w,  (a, b) -> (a cos t - b sin t, b cos t + a sin t)
 //
 // Each value is read once and written once; everything else (statistics, angles, the
-// other half of a pair) stays in a warp's registers.  Bound by those bytes.
+// other half of a pair) stays in a warp's registers.  Bound by those bytes: eight prompts
+// of 2048 rows (32 + 8 + 8 heads of 128, bf16) take 66 us in a graph, 6.1 TB/s; 3510 ragged
+// rows in pairs into e4m3 pages 14 us, where latencies and instructions count beside
+// them; four single tokens 3 us, the launch.
 //
 // Angles.  t = 2 pi frac(p turns / 2^64): the product modulo 2^64 is the fraction of a
 // turn, exact but for the rounding of `turns` itself, so no wide floating-point
@@ -136,7 +139,8 @@ __device__ __forceinline__ uint2 scaled_e4m3(const float (&x)[8], float scale, f
 // A warp takes a row, or with few rows a part of its steps (`parts` warps a row), the
 // queries' heads first, then the keys', then the values'.  Its loads run one batch of
 // steps ahead, into the lanes' own places in shared memory (no barrier): 128 KB are then
-// in flight on an SM, which registers have no room for.
+// in flight on an SM, which registers have no room for (with the loads in registers the
+// eight prompts took 80 us).
 template <int D, bool FP8, bool PAIRS>
 __global__ void __launch_bounds__(THREADS, BLOCKS_SM) rope_append_kernel(const RopeArgs a) {
   constexpr int LPH = D / 16, HPW = 32 / LPH, FREQS = D / 64;
