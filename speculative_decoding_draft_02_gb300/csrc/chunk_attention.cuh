@@ -349,6 +349,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
     const int r_lo = min((int)threadIdx.x * per, a.R), r_hi = min(r_lo + per, a.R);
     long long mine = 0;
     Request q;
+#pragma unroll 1
     for (int r = r_lo; r < r_hi; ++r) {
       if (!q.set(a, a.ctx[r], a.row_start[r], a.row_start[r + 1]) && cta == 0)
         dspark_set_status(DSPARK_ERR_LENGTH);
@@ -389,6 +390,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
         long long off = u - below;
         int r = r_lo;
         if (per > 1) {
+#pragma unroll 1
           for (;; ++r) {
             q.set(a, a.ctx[r], a.row_start[r], a.row_start[r + 1]);
             const long long m = q.upto(a, q.items) * a.heads;
@@ -1043,10 +1045,13 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
       fewer_registers<G::REGS_WIDEN>();
       // ------------------------------- 8-bit tiles, and Q, made f16 ----
       const int w = warp - 12, token = w * 32 + lane;
-      int k_slot = 0, v_slot = 0;
-      uint32_t k_phase = 0, v_phase = 0, uses[2] = {0, 0};
+      int slot = 0;
+      uint32_t phase = 0, uses[2] = {0, 0};
       bool ok = true;
-      // A tile in its place, a thread a token: its row is read before it is written.
+      // A tile in its place, a thread a token: its row is read before it is written.  One
+      // copy of this code for K and V: the roles together overrun the instruction cache (with
+      // two, two chunks of 512 over 40 and 50 thousand tokens took 535 us instead of 507,
+      // eight of 4096 over 4096 2750 instead of 2460).
       auto widen = [&](uint8_t *slot, uint64_t *raw, uint64_t *full, uint32_t phase) {
         ok = warp_wait(raw, phase, abort);
         // eight lanes take eight tokens: the swizzles spread both sides over all banks
@@ -1084,12 +1089,11 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
         if (tiles == 0) break;
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
-          widen(sk + k_slot * G::PLACE, &ctl->kr_full[k_slot], &ctl->k_full[k_slot], k_phase);
-          if (++k_slot == SLOTS) {
-            k_slot = 0;
-            k_phase ^= 1;
-          }
-          if (t == 0) {
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            widen((kv ? sv : sk) + slot * G::PLACE, kv ? &ctl->vr_full[slot] : &ctl->kr_full[slot],
+                  kv ? &ctl->v_full[slot] : &ctl->k_full[slot], phase);
+            if (kv || t != 0) continue;
             // Q's tiles in place, a thread a row: times the power of two that brings its
             // largest finite value to 2^14
 #pragma unroll 1
@@ -1135,10 +1139,9 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
               else ++uses[0];
             }
           }
-          widen(sv + v_slot * G::PLACE, &ctl->vr_full[v_slot], &ctl->v_full[v_slot], v_phase);
-          if (++v_slot == SLOTS) {
-            v_slot = 0;
-            v_phase ^= 1;
+          if (++slot == SLOTS) {
+            slot = 0;
+            phase ^= 1;
           }
           if (!ok) break;
         }
