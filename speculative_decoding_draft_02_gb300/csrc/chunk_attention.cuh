@@ -35,10 +35,11 @@
 // What bounds it: a pair of tiles takes the tensor pipe 2048 cycles and about 2900 in
 // all, as S's product reads shared memory at its full rate while P.V, the copies and the
 // widening read and write it too.  In a graph, 32 query heads over 8 KV heads of 128:
-// one prompt of 8192 rows 336 us, 1640 TFLOP/s; eight chunks of 4096 over 4096 2400 us,
-// 1370 (the board's power); two chunks of 512 over 40 and 50 thousand tokens in 8 bits 544
-// us, 1370.  What an item's beginning and end cost counts in batches of short requests:
-// 12 of 1 to 1500 rows 63 us, 640 TFLOP/s.
+// one prompt of 8192 rows 334 us, 1646 TFLOP/s; eight chunks of 4096 over 4096 2400 us,
+// 1370 (the board's power); two chunks of 512 over 40 and 50 thousand tokens in 8 bits 507
+// us, 1470.  What an item's beginning and end cost counts in batches of short requests:
+// 12 of 1 to 1500 rows 60 us, 670 TFLOP/s; there code that is seldom run counts too, as it
+// comes through the instruction cache at about five cycles an instruction.
 // Every wait is bounded; on expiry the CTA raises DSPARK_ERR_TIMEOUT, drains its own
 // copies and MMAs, frees TMEM and exits.
 #pragma once
@@ -55,8 +56,8 @@ constexpr int BM = 128;             // rows of a tile of Q
 constexpr int SMEM_LIMIT = 232448;  // 227 KB
 constexpr int CTL_BYTES = 3 * 1024;
 // Places for tiles of K and of V, each; more of them gain nothing (of V, three with 128 or
-// four with 64 columns: one prompt of 8192 rows 342 us instead of 339, 4 x 8192 rows of 64
-// columns in 8 bits 2152 instead of 2036).
+// four with 64 columns: one prompt of 8192 rows 342 us instead of 339, eight chunks of 4096
+// over 4096 with 64 columns in 8 bits 2152 instead of 2036).
 constexpr int SLOTS = 2;
 constexpr int SEGS = 4;             // segments published ahead
 // What beginning and ending an item costs, in tokens; the least share worth a CTA of its
@@ -553,8 +554,8 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
     // which only the other gives back.  P hangs on its own stream alone, so that the warp
     // stays with it until it is there: the tensor pipe holds the other's products meanwhile,
     // and the next are issued sooner than by a round of polls.  A prompt of 8192 rows takes
-    // 371 -> 341 us by that, 4 x 8192 rows of 64 columns 1808 -> 1600, two chunks of 512 over
-    // 40 and 50 thousand tokens in 8 bits 562 -> 551.
+    // 371 -> 341 us by that, eight chunks of 4096 over 4096 with 64 columns 1808 -> 1600, two
+    // of 512 over 40 and 50 thousand tokens in 8 bits 562 -> 551.
     constexpr uint32_t idesc_s = G::FP8 ? tc::idesc_f16(BM, BT) : tc::idesc_bf16(BM, BT);
     constexpr uint32_t idesc_o =
         (G::FP8 ? tc::idesc_f16(BM, D) : tc::idesc_bf16(BM, D)) | tc::IDESC_B_MN;
@@ -863,7 +864,7 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
         const int t0 = (tb + k) * BT;
         if (t0 + BT > all_see) {
           // by bits, which take half the instructions (32 prompts of 256 rows 53 -> 51 us);
-          // beside 8 bits by comparisons (64 columns, 4 x 8192 rows: 2070 us, by bits 2150)
+          // beside 8 bits by comparisons (eight chunks of 4096 over 4096 2430 us, by bits 2510)
           const int lim = sees - t0;
           if constexpr (G::FP8) {
 #pragma unroll
