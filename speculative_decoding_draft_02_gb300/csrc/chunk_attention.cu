@@ -83,7 +83,7 @@ int launch(const Launch &l) {
     dspark_count_launches(1);
     return DSPARK_OK;
   }
-  if (dspark_launch_pdl(chunk::chunk_attention_join<D>, dim3(l.ctas, 2, D / 32), dim3(chunk::BM),
+  if (dspark_launch_pdl(chunk::chunk_attention_join<D>, dim3(l.ctas, 2, D / 16), dim3(chunk::BM),
                         0, l.stream, a) != cudaSuccess)
     return DSPARK_ERR_CUDA;
   DSPARK_CHECK_LAUNCH();
