@@ -35,10 +35,10 @@
 // What bounds it: a pair of tiles takes the tensor pipe 2048 cycles and about 2900 in
 // all, as S's product reads shared memory at its full rate while P.V, the copies and the
 // widening read and write it too.  In a graph, 32 query heads over 8 KV heads of 128:
-// one prompt of 8192 rows 334 us, 1646 TFLOP/s; eight chunks of 4096 over 4096 2400 us,
+// one prompt of 8192 rows 331 us, 1662 TFLOP/s; eight chunks of 4096 over 4096 2400 us,
 // 1370 (the board's power); two chunks of 512 over 40 and 50 thousand tokens in 8 bits 507
 // us, 1470.  What an item's beginning and end cost counts in batches of short requests:
-// 12 of 1 to 1500 rows 59 us, 685 TFLOP/s; there code that is seldom run counts too, as it
+// 12 of 1 to 1500 rows 57 us, 705 TFLOP/s; there code that is seldom run counts too, as it
 // comes through the instruction cache at about five cycles an instruction.
 // Every wait is bounded; on expiry the CTA raises DSPARK_ERR_TIMEOUT, drains its own
 // copies and MMAs, frees TMEM and exits.
@@ -60,9 +60,11 @@ constexpr int CTL_BYTES = 3 * 1024;
 // over 4096 with 64 columns in 8 bits 2152 instead of 2036).
 constexpr int SLOTS = 2;
 constexpr int SEGS = 4;             // segments published ahead
-// What beginning and ending an item costs, in tokens; the least share worth a CTA of its
-// own; and the least piece, in tiles, that an item is cut into.
-constexpr int OVERHEAD = 256, MIN_SHARE = 320, MIN_PIECE = 2;
+// What beginning and ending an item costs, in tokens (a batch of 12 requests 57 us, by 256
+// 58, by 384 63); the least share worth a CTA of its own, below any item's cost, so that no
+// CTA takes two items while others are free (by 320, 100 rows 9.5 us instead of 7.5); and
+// the least piece, in tiles, that an item is cut into.
+constexpr int OVERHEAD = 192, MIN_SHARE = 192, MIN_PIECE = 2;
 // log2: how far scores may pass the reference, and where a new reference puts the largest.
 template <bool FP8>
 struct Range {
