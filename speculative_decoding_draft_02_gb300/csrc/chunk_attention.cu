@@ -25,8 +25,8 @@ Layout layout_of(int ctas, int dim) {
 
 // Few rows leave the 128-row tiles empty: up to 32 of them (nodes x query heads of a KV
 // head) the tree attention, which has the tokens there, is the faster one.  64 requests over
-// 512 to 4096 tokens, 8 KV heads, tree and chunks: 32 rows 82 and 91 us, 64 rows 119 and 94;
-// 8 bits: 91 and 140, 186 and 143.  One request over 4000: 32 rows 22 and 29, 64 rows 26 and 29.
+// 512 to 4096 tokens, 8 KV heads, tree and chunks: 32 rows 82 and 90 us, 64 rows 119 and 91;
+// 8 bits: 91 and 114, 186 and 114.  One request over 4000: 32 rows 22 and 23, 64 rows 26 and 22.
 bool as_tree(int max_rows, int group) {
   return max_rows <= DSPARK_MAX_NODES && max_rows * group <= 32;
 }
