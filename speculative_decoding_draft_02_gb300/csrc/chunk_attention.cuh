@@ -750,9 +750,11 @@ __global__ void __launch_bounds__(Geo<TYPE, D>::THREADS, 1)
       if (tb == te) break;
       const long long first = (long long)n->ctx + n->node0;  // the first row's own token
       const long long end = min((long long)n->total, first + n->nodes);
+      // what comes before it every row sees; rows may lie past a table that is too short
+      const long long seen = min((long long)n->total, first + 1);
       for (int tile = tb; ok && tile < te; ++tile) {
         ok = warp_wait(&ctl->v_full[slot], phase, abort);
-        if (ok && (long long)tile * BT + BT > first + 1) {
+        if (ok && (long long)tile * BT + BT > seen) {
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             const int token = q * 32 + lane;
