@@ -519,7 +519,7 @@ def dspark_kv_compact(cache: KVCache, ctx, accepted, path, block_table, stream=N
 class Rotary:
     """The rotation of a head's first 2 * len(inv_freq) values (a multiple of 16): pair i by
     position * inv_freq[i] radians, f64.  A pair is values i and i + len(inv_freq), or with
-    `pairs` values 2 i and 2 i + 1."""
+    `pairs` values 2 i and 2 i + 1.  It serves calls on its own device."""
 
     def __init__(self, inv_freq, pairs=False, device="cuda"):
         f = torch.as_tensor(inv_freq, dtype=torch.float64)
@@ -534,6 +534,13 @@ class Rotary:
         self.struct = RopeStruct(self.turns.data_ptr(), self.dims,
                                  ROPE_PAIRS if pairs else ROPE_HALVES)
         self.ref = ctypes.byref(self.struct)
+
+    def on(self, what):
+        """The rotation for a call, once its table is on the current device."""
+        if self.dims and self.turns.get_device() != _device():
+            raise DSparkError(f"{what}: the rotary's turns are on {self.turns.device}, which is not "
+                              "the current GPU")
+        return self.ref
 
 
 def dspark_rope_append(cache: KVCache, q, k, v, position, slot, rotary: Rotary, q_out,
@@ -554,7 +561,7 @@ def dspark_rope_append(cache: KVCache, q, k, v, position, slot, rotary: Rotary, 
         cache.ref, rows, heads_q, qp, q_row, q_head, kp, vp, rest[2], rest[3],
         None if q_weight is None else _want(what, "q_weight", q_weight, bf16, width),
         None if k_weight is None else _want(what, "k_weight", k_weight, bf16, width), eps,
-        rotary.ref, _want(what, "position", position, torch.int32, (rows,)),
+        rotary.on(what), _want(what, "position", position, torch.int32, (rows,)),
         _want(what, "slot", slot, torch.int64, (rows,)), op, o_row, o_head,
         _stream_on(what, q, stream)), what)
 
