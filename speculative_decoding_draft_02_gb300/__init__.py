@@ -146,11 +146,12 @@ def _check(rc: int, what: str):
         raise DSparkError(f"{what} failed: {msg} ({rc})")
 
 
-def _ptr(t: Optional[torch.Tensor]):
+def _ptr(t: Optional[torch.Tensor], device=None):
     if t is None:
         return None
-    if not t.is_cuda:
-        raise DSparkError("tensor must live on the GPU")
+    if not t.is_cuda or (device is not None and t.get_device() != device):
+        raise DSparkError("tensor must live on the GPU" if device is None else
+                          f"tensor must live on device {device}, with the call's others")
     if not t.is_contiguous():
         raise DSparkError("tensor must be contiguous")
     return ctypes.c_void_p(t.data_ptr())
@@ -336,15 +337,20 @@ def dspark_verify_residual_rows(dims, workspace, stream=None):
 # A call's arguments are checked in the 5 to 8 us that the GPU takes for a small one:
 # one expression per tensor, and the message only when it is wanted.
 
-def _want(what: str, name: str, t, dtype, shape) -> int:
-    """The tensor's address, once its type and shape are what the call reads."""
+# A call's first tensor says on which device the others have to be (`device` below); that
+# it is the current one, _stream_on sees to.
+
+def _want(what: str, name: str, t, dtype, shape, device=None) -> int:
+    """The tensor's address, once its type, shape and place are what the call reads."""
     try:
-        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        if (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                and (t.is_cuda if device is None else t.get_device() == device)):
             return t.data_ptr()
     except AttributeError:
         raise DSparkError(f"{what}: {name} must be a tensor") from None
     raise DSparkError(f"{what}: {name} must be a contiguous {dtype} tensor {tuple(shape)} on the "
-                      f"GPU, not {t.dtype} {tuple(t.shape)} on {t.device}")
+                      f"{'' if device is None else 'same '}GPU, not {t.dtype} {tuple(t.shape)} on "
+                      f"{t.device}")
 
 
 def _rows_view(what: str, name: str, t, heads, dim):
@@ -364,19 +370,20 @@ def _rows_view(what: str, name: str, t, heads, dim):
     return t.data_ptr(), shape[0], row, head
 
 
-def _heads_view(what: str, name: str, t, dim):
+def _heads_view(what: str, name: str, t, dim, device=None):
     """_rows_view for any number of heads: (address, rows, heads, row stride, head stride)."""
     try:
         (rows, heads, width), (row, head, one) = t.shape, t.stride()
-        if t.dtype is torch.bfloat16 and width == dim and one == 1 and t.is_cuda:
+        if (t.dtype is torch.bfloat16 and width == dim and one == 1
+                and (t.is_cuda if device is None else t.get_device() == device)):
             return (t.data_ptr(), rows, heads, row if rows > 1 else dim,
                     head if heads > 1 else dim)
     except AttributeError:
         raise DSparkError(f"{what}: {name} must be a tensor") from None
     except ValueError:
         pass
-    raise DSparkError(f"{what}: {name} must be bfloat16 [rows, heads, {dim}] on the GPU with a "
-                      "dense last dimension")
+    raise DSparkError(f"{what}: {name} must be bfloat16 [rows, heads, {dim}] on the "
+                      f"{'' if device is None else 'same '}GPU with a dense last dimension")
 
 
 def _size(what: str, name: str, t, dims: int):
@@ -409,6 +416,8 @@ class KVCache:
             raise DSparkError("KVCache: bfloat16 or float8_e4m3fn")
         if not (k.is_cuda and v.is_cuda):
             raise DSparkError("tensor must live on the GPU")
+        if k.get_device() != v.get_device():
+            raise DSparkError("KVCache: k and v must be on the same GPU")
         if k.stride(3) != 1:
             raise DSparkError("KVCache: the last dimension must be dense")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
@@ -418,7 +427,7 @@ class KVCache:
             if t is not None and not fp8:
                 raise DSparkError("KVCache: a bfloat16 cache has no scales")
             if t is not None:
-                _want("KVCache", name, t, torch.float32, (self.heads,))
+                _want("KVCache", name, t, torch.float32, (self.heads,), k.get_device())
         # strides over a single page or head are never stepped by
         head = k.stride(2) if self.heads > 1 else self.dim
         page = k.stride(0) if self.n_pages > 1 else self.page_size * self.heads * self.dim
@@ -428,6 +437,14 @@ class KVCache:
                                     page, k.stride(1), head, self.n_pages, self.page_size,
                                     self.heads, self.dim, KV_E4M3 if fp8 else KV_BF16)
         self.ref = ctypes.byref(self.struct)
+        self.device = k.get_device()
+
+    def on(self, what, device):
+        """The cache for a call, once it is on the device of the call's tensors."""
+        if self.device != device:
+            raise DSparkError(f"{what}: the cache is on device {self.device}, the tensors on device "
+                              f"{device}")
+        return self.ref
 
 
 def dspark_kv_plan(ctx, length, extra, parent, page_size, held, n_free, free_pages, block_table,
@@ -535,11 +552,11 @@ class Rotary:
                                  ROPE_PAIRS if pairs else ROPE_HALVES)
         self.ref = ctypes.byref(self.struct)
 
-    def on(self, what):
-        """The rotation for a call, once its table is on the current device."""
-        if self.dims and self.turns.get_device() != _device():
-            raise DSparkError(f"{what}: the rotary's turns are on {self.turns.device}, which is not "
-                              "the current GPU")
+    def on(self, what, device):
+        """The rotation for a call, once its table is on the device of the call's tensors."""
+        if self.dims and self.turns.get_device() != device:
+            raise DSparkError(f"{what}: the rotary's turns are on {self.turns.device}, the tensors "
+                              f"on device {device}")
         return self.ref
 
 
@@ -549,20 +566,21 @@ def dspark_rope_append(cache: KVCache, q, k, v, position, slot, rotary: Rotary, 
     strides); weights bf16 [dim] or None (no norm of that side).  q_out may be q."""
     what, dim = "dspark_rope_append", cache.dim
     qp, rows, heads_q, q_row, q_head = _heads_view(what, "q", q, dim)
-    kp, *rest = _heads_view(what, "k", k, dim)
-    vp, *also = _heads_view(what, "v", v, dim)
-    op, o_rows, o_heads, o_row, o_head = _heads_view(what, "q_out", q_out, dim)
+    on = q.get_device()
+    kp, *rest = _heads_view(what, "k", k, dim, on)
+    vp, *also = _heads_view(what, "v", v, dim, on)
+    op, o_rows, o_heads, o_row, o_head = _heads_view(what, "q_out", q_out, dim, on)
     if rest != also or rest[0] != rows or o_rows != rows:
         raise DSparkError(f"{what}: q, k, v and q_out must have equal rows, k and v equal strides")
     if rest[1] != cache.heads or o_heads != heads_q:
         raise DSparkError(f"{what}: k and v must have the cache's heads, q_out q's")
     bf16, width = torch.bfloat16, (dim,)
     _check(load_library().dspark_rope_append(
-        cache.ref, rows, heads_q, qp, q_row, q_head, kp, vp, rest[2], rest[3],
-        None if q_weight is None else _want(what, "q_weight", q_weight, bf16, width),
-        None if k_weight is None else _want(what, "k_weight", k_weight, bf16, width), eps,
-        rotary.on(what), _want(what, "position", position, torch.int32, (rows,)),
-        _want(what, "slot", slot, torch.int64, (rows,)), op, o_row, o_head,
+        cache.on(what, on), rows, heads_q, qp, q_row, q_head, kp, vp, rest[2], rest[3],
+        None if q_weight is None else _want(what, "q_weight", q_weight, bf16, width, on),
+        None if k_weight is None else _want(what, "k_weight", k_weight, bf16, width, on), eps,
+        rotary.on(what, on), _want(what, "position", position, torch.int32, (rows,), on),
+        _want(what, "slot", slot, torch.int64, (rows,), on), op, o_row, o_head,
         _stream_on(what, q, stream)), what)
 
 
@@ -576,17 +594,19 @@ def dspark_chunk_attention(cache: KVCache, q, ctx, row_start, block_table, max_r
     """q, out bf16 [rows, heads_q, dim] (views with a dense last dimension); lse may be None."""
     what, i32 = "dspark_chunk_attention", torch.int32
     qp, rows, heads_q, q_row, q_head = _heads_view(what, "q", q, cache.dim)
-    op, o_rows, o_heads, o_row, o_head = _heads_view(what, "out", out, cache.dim)
+    on = q.get_device()
+    op, o_rows, o_heads, o_row, o_head = _heads_view(what, "out", out, cache.dim, on)
     if o_rows != rows or o_heads != heads_q:
         raise DSparkError(f"{what}: out must have q's rows and heads")
     R = _size(what, "ctx", ctx, 1)[0]
     pages = _size(what, "block_table", block_table, 2)[1]
     _check(load_library().dspark_chunk_attention(
-        cache.ref, R, heads_q, max_rows, rows, pages, qp, q_row, q_head,
-        _want(what, "ctx", ctx, i32, (R,)), _want(what, "row_start", row_start, i32, (R + 1,)),
-        _want(what, "block_table", block_table, i32, (R, pages)), scale, op, o_row, o_head,
-        None if lse is None else _want(what, "lse", lse, torch.float32, (rows, heads_q)),
-        _ptr(workspace), workspace.numel(), _stream_on(what, q, stream)), what)
+        cache.on(what, on), R, heads_q, max_rows, rows, pages, qp, q_row, q_head,
+        _want(what, "ctx", ctx, i32, (R,), on),
+        _want(what, "row_start", row_start, i32, (R + 1,), on),
+        _want(what, "block_table", block_table, i32, (R, pages), on), scale, op, o_row, o_head,
+        None if lse is None else _want(what, "lse", lse, torch.float32, (rows, heads_q), on),
+        _ptr(workspace, on), workspace.numel(), _stream_on(what, q, stream)), what)
 
 
 def dspark_kv_fork(source, target, page_size, ctx, held, n_free, free_pages, block_table, refs,
@@ -596,15 +616,17 @@ def dspark_kv_fork(source, target, page_size, ctx, held, n_free, free_pages, blo
     (n,), (R,) = _size(what, "source", source, 1), _size(what, "ctx", ctx, 1)
     pages = _size(what, "free_pages", free_pages, 1)[0]
     table = _size(what, "block_table", block_table, 2)
+    places, on = _want(what, "ctx", ctx, i32, (R,)), ctx.get_device()
     _check(load_library().dspark_kv_fork(
-        n, _want(what, "source", source, i32, (n,)), _want(what, "target", target, i32, (n,)), R,
-        page_size, pages, table[1], _want(what, "ctx", ctx, i32, (R,)),
-        _want(what, "held", held, i32, (R,)), _want(what, "n_free", n_free, i32, (1,)),
-        _want(what, "free_pages", free_pages, i32, (pages,)),
-        _want(what, "block_table", block_table, i32, (R, table[1])),
-        _want(what, "refs", refs, i32, (pages,)), _want(what, "copy_from", copy_from, i32, (n,)),
-        _want(what, "copy_to", copy_to, i32, (n,)),
-        _want(what, "copy_tokens", copy_tokens, i32, (n,)), _stream_on(what, ctx, stream)), what)
+        n, _want(what, "source", source, i32, (n,), on),
+        _want(what, "target", target, i32, (n,), on), R, page_size, pages, table[1], places,
+        _want(what, "held", held, i32, (R,), on), _want(what, "n_free", n_free, i32, (1,), on),
+        _want(what, "free_pages", free_pages, i32, (pages,), on),
+        _want(what, "block_table", block_table, i32, (R, table[1]), on),
+        _want(what, "refs", refs, i32, (pages,), on),
+        _want(what, "copy_from", copy_from, i32, (n,), on),
+        _want(what, "copy_to", copy_to, i32, (n,), on),
+        _want(what, "copy_tokens", copy_tokens, i32, (n,), on), _stream_on(what, ctx, stream)), what)
 
 
 def dspark_kv_release(ctx, held, n_free, free_pages, block_table, refs, stream=None):
@@ -612,12 +634,13 @@ def dspark_kv_release(ctx, held, n_free, free_pages, block_table, refs, stream=N
     what, i32 = "dspark_kv_release", torch.int32
     (R,), (pages,) = _size(what, "ctx", ctx, 1), _size(what, "free_pages", free_pages, 1)
     table = _size(what, "block_table", block_table, 2)
+    places, on = _want(what, "ctx", ctx, i32, (R,)), ctx.get_device()
     _check(load_library().dspark_kv_release(
-        R, pages, table[1], _want(what, "ctx", ctx, i32, (R,)),
-        _want(what, "held", held, i32, (R,)), _want(what, "n_free", n_free, i32, (1,)),
-        _want(what, "free_pages", free_pages, i32, (pages,)),
-        _want(what, "block_table", block_table, i32, (R, table[1])),
-        _want(what, "refs", refs, i32, (pages,)), _stream_on(what, ctx, stream)), what)
+        R, pages, table[1], places,
+        _want(what, "held", held, i32, (R,), on), _want(what, "n_free", n_free, i32, (1,), on),
+        _want(what, "free_pages", free_pages, i32, (pages,), on),
+        _want(what, "block_table", block_table, i32, (R, table[1]), on),
+        _want(what, "refs", refs, i32, (pages,), on), _stream_on(what, ctx, stream)), what)
 
 
 def dspark_kv_squeeze(held, n_free, free_pages, block_table, refs, free_pages_out, block_table_out,
@@ -628,28 +651,31 @@ def dspark_kv_squeeze(held, n_free, free_pages, block_table, refs, free_pages_ou
     (R,), (pages,) = _size(what, "held", held, 1), _size(what, "free_pages", free_pages, 1)
     table = _size(what, "block_table", block_table, 2)
     shape, half = (R, table[1]), (pages // 2,)
+    holds, on = _want(what, "held", held, i32, (R,)), held.get_device()
     _check(load_library().dspark_kv_squeeze(
-        R, pages, table[1], _want(what, "held", held, i32, (R,)),
-        _want(what, "n_free", n_free, i32, (1,)),
-        _want(what, "free_pages", free_pages, i32, (pages,)),
-        _want(what, "block_table", block_table, i32, shape),
-        _want(what, "refs", refs, i32, (pages,)),
-        _want(what, "free_pages_out", free_pages_out, i32, (pages,)),
-        _want(what, "block_table_out", block_table_out, i32, shape),
-        _want(what, "refs_out", refs_out, i32, (pages,)),
-        _want(what, "new_page", new_page, i32, (pages,)),
-        _want(what, "move_from", move_from, i32, half), _want(what, "move_to", move_to, i32, half),
-        _want(what, "n_moves", n_moves, i32, (1,)), _stream_on(what, held, stream)), what)
+        R, pages, table[1], holds,
+        _want(what, "n_free", n_free, i32, (1,), on),
+        _want(what, "free_pages", free_pages, i32, (pages,), on),
+        _want(what, "block_table", block_table, i32, shape, on),
+        _want(what, "refs", refs, i32, (pages,), on),
+        _want(what, "free_pages_out", free_pages_out, i32, (pages,), on),
+        _want(what, "block_table_out", block_table_out, i32, shape, on),
+        _want(what, "refs_out", refs_out, i32, (pages,), on),
+        _want(what, "new_page", new_page, i32, (pages,), on),
+        _want(what, "move_from", move_from, i32, half, on),
+        _want(what, "move_to", move_to, i32, half, on),
+        _want(what, "n_moves", n_moves, i32, (1,), on), _stream_on(what, held, stream)), what)
 
 
 def dspark_kv_copy(cache: KVCache, copy_from, copy_to, copy_tokens=None, stream=None):
     """copy_tokens None: whole pages."""
     what, i32 = "dspark_kv_copy", torch.int32
     n = _size(what, "copy_from", copy_from, 1)[0]
+    pages, on = _want(what, "copy_from", copy_from, i32, (n,)), copy_from.get_device()
     _check(load_library().dspark_kv_copy(
-        cache.ref, n, _want(what, "copy_from", copy_from, i32, (n,)),
-        _want(what, "copy_to", copy_to, i32, (n,)),
-        None if copy_tokens is None else _want(what, "copy_tokens", copy_tokens, i32, (n,)),
+        cache.on(what, on), n, pages,
+        _want(what, "copy_to", copy_to, i32, (n,), on),
+        None if copy_tokens is None else _want(what, "copy_tokens", copy_tokens, i32, (n,), on),
         _stream_on(what, copy_from, stream)), what)
 
 
