@@ -741,8 +741,11 @@ class PagePool:
             self.refs = torch.zeros((n_pages,), dtype=torch.int32, device=device)
             self._copies = [new(R) for _ in range(3)]    # of the last fork: from, to, tokens
             self.copies = [t[:0] for t in self._copies]
-            self.new_page, self.n_moves = new(n_pages), new(1)
-            self.move_from, self.move_to = new(n_pages // 2), new(n_pages // 2)
+            # of the last squeeze: none yet
+            self.new_page = new(n_pages)
+            self.n_moves = torch.zeros((1,), dtype=torch.int32, device=device)
+            self.move_from, self.move_to = (torch.full((n_pages // 2,), -1, dtype=torch.int32,
+                                                       device=device) for _ in range(2))
 
     def plan(self, length, extra=1, parent=None, stream=None):
         """Rows, pages, slots, positions (and masks, in a round) for `length` + extra new
