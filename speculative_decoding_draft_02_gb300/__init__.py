@@ -830,9 +830,10 @@ class PagePool:
         self._needs_shared("fork")
         if len(source) > len(self.ctx):
             raise DSparkError("PagePool.fork: more forks than places")
-        self.copies = [t[:len(source)] for t in self._copies]
+        copies = [t[:len(source)] for t in self._copies]
         dspark_kv_fork(source, target, self.page_size, self.ctx, self.held, self.n_free,
-                       self.free_pages, self.block_table, self.refs, *self.copies, stream)
+                       self.free_pages, self.block_table, self.refs, *copies, stream)
+        self.copies = copies
 
     def copy(self, cache: KVCache, stream=None):
         """One layer's part of the last fork: the last pages' tokens."""

@@ -1,9 +1,12 @@
 """What PagePool's copies and moves hold before there is anything to copy or move, without a
 GPU."""
+import pytest
 import torch
 
+import speculative_decoding_draft_02_gb300 as dsp
+
 from test_cache_pool_cpu import CACHE, calls  # noqa: F401
-from test_prompt_pool_cpu import more, pool  # noqa: F401
+from test_prompt_pool_cpu import I32, more, pool  # noqa: F401
 
 
 def test_a_pool_that_was_never_squeezed_moves_nothing(more, monkeypatch):  # noqa: F811
@@ -14,3 +17,22 @@ def test_a_pool_that_was_never_squeezed_moves_nothing(more, monkeypatch):  # noq
     p.move(CACHE)
     assert more[-1].name == "dspark_kv_copy" and (more[-1].args[1] < 0).all()
     assert int(p.n_moves) == 0
+
+
+def test_a_fork_that_was_refused_leaves_the_last_ones_copies(more, monkeypatch):  # noqa: F811
+    p = pool(shared=True)
+    three, two = torch.zeros(3, dtype=I32), torch.zeros(2, dtype=I32)
+
+    def refused(*args):
+        raise dsp.DSparkError("refused")
+
+    accepted = dsp.dspark_kv_fork
+    for ready, copies in ((False, 0), (True, 3)):
+        if ready:
+            monkeypatch.setattr(dsp, "dspark_kv_fork", accepted)
+            p.fork(three, three)
+        monkeypatch.setattr(dsp, "dspark_kv_fork", refused)
+        with pytest.raises(dsp.DSparkError, match="refused"):
+            p.fork(two, two)
+        p.copy(CACHE)
+        assert [t.numel() for t in more[-1].args[1:4]] == [copies] * 3
