@@ -826,10 +826,13 @@ class PagePool:
 
     def fork(self, source, target, stream=None):
         """Free places target[i] become continuations of requests source[i] (int32, one for
-        each fork; source[i] < 0: none).  Each layer's cache then needs copy()."""
+        each fork; source[i] < 0: none), places that were just left among them: what those
+        held is given back first.  Each layer's cache then needs copy(), before the next fork
+        or squeeze.  Between rounds only: a commit goes on with every place that is there."""
         self._needs_shared("fork")
         if len(source) > len(self.ctx):
             raise DSparkError("PagePool.fork: more forks than places")
+        self.release(stream)
         copies = [t[:len(source)] for t in self._copies]
         dspark_kv_fork(source, target, self.page_size, self.ctx, self.held, self.n_free,
                        self.free_pages, self.block_table, self.refs, *copies, stream)

@@ -36,3 +36,11 @@ def test_a_fork_that_was_refused_leaves_the_last_ones_copies(more, monkeypatch):
             p.fork(two, two)
         p.copy(CACHE)
         assert [t.numel() for t in more[-1].args[1:4]] == [copies] * 3
+
+
+def test_a_fork_releases_first(more):  # noqa: F811
+    p = pool(shared=True)
+    one = torch.zeros(1, dtype=I32)
+    p.fork(one, one, stream="s")
+    assert [c.name for c in more] == ["dspark_kv_release", "dspark_kv_fork"]
+    assert all(c.args[-1] == "s" for c in more)
