@@ -559,7 +559,9 @@ size_t dspark_chunk_attention_workspace_bytes(const dspark_kv_cache *cache, int3
  * (8 bits; the sum of the weights takes it unrounded); beside an 8-bit one weights and q
  * are f16 as in dspark_tree_attention, with a power of two for every row and head of q.
  * With few rows (max_rows times the query heads of a KV head at most 32) the call is
- * dspark_tree_attention's, with that call's precision. */
+ * dspark_tree_attention's, with that call's precision: it is the bound, not a request's
+ * own rows, that says so.  A request longer than its row of the table is cut there, and
+ * rows past that end see what the table holds. */
 int dspark_chunk_attention(const dspark_kv_cache *cache, int32_t R, int32_t heads_q,
                            int32_t max_rows, int32_t n_rows, int32_t max_pages, const void *q,
                            int64_t q_row_stride, int64_t q_head_stride, const int32_t *ctx,

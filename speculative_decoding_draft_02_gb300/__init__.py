@@ -717,7 +717,8 @@ class PagePool:
     pages go back with the next plan).
 
     A `shared` pool's requests may be forked: continuations share a prompt's full pages,
-    and a page goes back with the last of its holders."""
+    and a page goes back with the last of its holders (with the next plan, fork or
+    squeeze)."""
 
     def __init__(self, R, n_pages, page_size, max_tokens, n_rows, device="cuda", shared=False):
         new = lambda shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device=device)  # noqa: E731
@@ -772,7 +773,14 @@ class PagePool:
     def attend(self, cache: KVCache, q, max_nodes, out, lse=None, scale=None, stream=None):
         """One layer's attention of the rows that plan was last called for, over contexts and
         trees; a prompt's (max_nodes rows a request at most, any number) are chains.  Which of
-        the two is settled at the call: a graph that holds an attend holds its plan too."""
+        the two is settled at the call: a graph that holds an attend holds its plan too.
+
+        A prompt's rows go to the tree attention up to MAX_NODES a request, as they always
+        did: beside a bf16 cache its weights have 16 bits, the chunk attention's 8.  It is the
+        slower one there from about 32 rows x query heads of a KV head on (64 requests over 512
+        to 4096 tokens, 32 heads over 8, 16 rows each: 138 and 114 us, 64 rows: 364 and 135,
+        in 8 bits 799 and 184); dspark_chunk_attention takes the pool's ctx, row_start and
+        block_table as they are."""
         scale = cache.dim ** -0.5 if scale is None else scale
         if self._prompts and max_nodes > MAX_NODES:
             need = dspark_chunk_attention_workspace_bytes(cache, len(self.ctx), q.shape[1],
@@ -839,12 +847,13 @@ class PagePool:
         self.copies = copies
 
     def copy(self, cache: KVCache, stream=None):
-        """One layer's part of the last fork: the last pages' tokens."""
+        """One layer's part of the last fork, once: the last pages' tokens."""
         self._needs_shared("copy")
         dspark_kv_copy(cache, *self.copies, stream)
 
     def release(self, stream=None):
-        """The pages of the requests that left (ctx -1), now rather than with the next plan."""
+        """The pages of the requests that left (ctx -1), now rather than with the next plan, fork
+        or squeeze."""
         self._needs_shared("release")
         dspark_kv_release(self.ctx, self.held, self.n_free, self.free_pages, self.block_table,
                           self.refs, stream)
@@ -859,7 +868,7 @@ class PagePool:
                           self.move_from, self.move_to, self.n_moves, stream)
 
     def move(self, cache: KVCache, stream=None):
-        """One layer's part of the last squeeze."""
+        """One layer's part of the last squeeze, once and before its next rows."""
         self._needs_shared("move")
         dspark_kv_copy(cache, self.move_from, self.move_to, None, stream)
 

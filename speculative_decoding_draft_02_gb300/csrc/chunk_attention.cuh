@@ -13,8 +13,9 @@
 // through shared memory.  While one tile's softmax runs, the other's products do.
 //
 // The reference of a row's exponents is kept from tile to tile and raised (with O
-// rescaled) only where a weight would exceed 2^RAISE: weights, sums and O have f32's
-// range, so nothing is lost by it.
+// rescaled) only where a weight would exceed 2^RAISE.  f32 sums lose nothing by that, but
+// weights of up to 2^32 beside a bf16 cache take that much of O's range: values below 2^64,
+// of up to 2^31 tokens, overflow nowhere, as the header promises; larger ones may.
 //
 // Work is counted in tokens: an item costs its tokens and OVERHEAD more, the list of all
 // items is cut into equal shares, one for each CTA, at tile boundaries, and the pieces of
@@ -34,12 +35,18 @@
 //
 // What bounds it: a pair of tiles takes the tensor pipe 2048 cycles and about 2900 in
 // all, as S's product reads shared memory at its full rate while P.V, the copies and the
-// widening read and write it too.  In a graph, 32 query heads over 8 KV heads of 128:
-// one prompt of 8192 rows 331 us, 1662 TFLOP/s; eight chunks of 4096 over 4096 2400 us,
-// 1370 (the board's power); two chunks of 512 over 40 and 50 thousand tokens in 8 bits 507
-// us, 1470.  What an item's beginning and end cost counts in batches of short requests:
-// 12 of 1 to 1500 rows 57 us, 705 TFLOP/s; there code that is seldom run counts too, as it
-// comes through the instruction cache at about five cycles an instruction.
+// widening read and write it too.  32 query heads over 8 KV heads of 128: one prompt of 8192
+// rows 331 to 343 us (1600 to 1660 TFLOP/s) for the first milliseconds; again and again for
+// seconds, in a graph as by calls, the board's power limit takes the clock to 1810-1840 MHz,
+// and it is 361 to 367 (1500 to 1520).  So eight chunks of 4096 over 4096: 2190 to 2220 us at
+// first, 2500 (1320) for seconds, at 1430 MHz; and two chunks of 512 over 40 and 50 thousand
+// tokens in 8 bits: 507 to 525 at first, 537 (1390) for seconds, at 1940 MHz.
+// What an item's beginning and end cost counts in batches of short requests: 12 of 1 to
+// 1500 rows 57 us, 705 TFLOP/s; there code that is seldom run counts too, as it comes through
+// the instruction cache at about five cycles an instruction.  And an item whose rows fit
+// one tile leaves the second stream of products empty: 64 next tokens over 512 to 4096
+// beside a chunk of 512 rows over 2048 take 127 us, in 8 bits 160, where the bytes take 92
+// and 47; without the chunk 109 and 131 here, 101 and 89 by the tree attention.
 // Every wait is bounded; on expiry the CTA raises DSPARK_ERR_TIMEOUT, drains its own
 // copies and MMAs, frees TMEM and exits.
 #pragma once

@@ -7,7 +7,10 @@
 // other half of a pair) stays in a warp's registers.  Bound by those bytes: eight prompts
 // of 2048 rows (32 + 8 + 8 heads of 128, bf16) take 66 us in a graph, 6.1 TB/s; 3510 ragged
 // rows in pairs into e4m3 pages 14 us, where latencies and instructions count beside
-// them; four single tokens 3 us, the launch.
+// them; four single tokens 3 us, the launch.  Into e4m3 pages instructions bound long ones
+// too: the eight prompts' rows 83 us, 4.5 TB/s.  So they do beside few KV heads, as a step
+// takes 512 / dim heads of one kind and lanes without a head idle: 16384 rows of 8 + 1 + 1
+// heads of 128 26 us (e4m3 34) where the bytes take 12, of 64 21 (29) where they take 6.
 //
 // Angles.  t = 2 pi frac(p turns / 2^64): the product modulo 2^64 is the fraction of a
 // turn, exact but for the rounding of `turns` itself, so no wide floating-point
